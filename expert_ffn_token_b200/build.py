@@ -27,7 +27,8 @@ FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", 
          "--expt-relaxed-constexpr", f"-I{INCLUDE}", f"-I{CSRC}"]
 
 LIB_SOURCES = ["k_route.cu", "k_ffn.cu", "k_decode.cu", "k_gateup_tc.cu", "k_gateup_i8.cu",
-               "k_down_tc.cu", "k_router.cu", "moe_api.cu", "moe_noalloc.cu"]
+               "k_down_tc.cu", "k_router.cu", "k_scored.cu", "k_scaled_quant.cu", "k_scaled_small.cu",
+               "k_scaled_tc.cu", "scaled_api.cu", "moe_api.cu", "moe_noalloc.cu"]
 OPTIONAL_SOURCES: list[str] = []
 SYNTH_SOURCES = ["synth_fill.cu"]
 

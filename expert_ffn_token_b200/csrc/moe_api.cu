@@ -109,6 +109,21 @@ WsLayout ws_layout(const moe_arena *A, int T, int k, uint32_t flags, bool allow_
     return L;
 }
 
+RouteWs route_ws(int T, int E, int k) {
+    const int n_chunks = (T + kChunk - 1) / kChunk;
+    RouteWs L{};
+    size_t p = 0;
+    L.chunk_counts = p;
+    p = align256(p + (size_t)n_chunks * E * 4);
+    L.chunk_base = p;
+    p = align256(p + (size_t)n_chunks * E * 4);
+    L.jobs = p;
+    p = align256(p + sizeof(Job) * (size_t)(std::min<int64_t>(E, (int64_t)T * k) + 1));
+    L.njobs = p;
+    L.total = align256(p + 4);
+    return L;
+}
+
 moe_status check_forward_args(const moe_arena *arena, const float *d_x, const float *d_logits,
                               int T, int k, const float *d_out, uint32_t flags) {
     if (!arena || !d_x || !d_logits || !d_out) return MOE_ERR_INVALID_ARG;
@@ -253,20 +268,10 @@ moe_status moe_quantize_act(const float *d_x, int T, int H, int8_t *d_q, uint16_
     return MOE_OK;
 }
 
-static size_t route_ws_bytes(int T, int E, int k) {
-    const int n_chunks = (T + kChunk - 1) / kChunk;
-    size_t p = 0;
-    p = align256(p + (size_t)n_chunks * E * 4);   // chunk counts
-    p = align256(p + (size_t)n_chunks * E * 4);   // chunk cursors
-    p = align256(p + sizeof(Job) * (size_t)(std::min(E, T * k) + 1));
-    p = align256(p + 4);
-    return p;
-}
-
 moe_status moe_route_workspace_size(int T, int E, int k, size_t *bytes) {
     if (!bytes || T <= 0 || E <= 0 || k <= 0 || k > kMaxK || k > E) return MOE_ERR_INVALID_ARG;
     if (E > kMaxE) return MOE_ERR_UNSUPPORTED;
-    *bytes = route_ws_bytes(T, E, k);
+    *bytes = route_ws(T, E, k).total;
     return MOE_OK;
 }
 
@@ -279,16 +284,14 @@ moe_status moe_route_topk(const float *d_logits, int T, int E, int k, int32_t *d
     if (T <= 0 || E <= 0 || k <= 0 || k > kMaxK || k > E) return MOE_ERR_INVALID_ARG;
     if (E > kMaxE) return MOE_ERR_UNSUPPORTED;
     if (!aligned(d_ws, 256)) return MOE_ERR_ALIGNMENT;
-    if (ws_bytes < route_ws_bytes(T, E, k)) return MOE_ERR_WORKSPACE;
+    const RouteWs L = route_ws(T, E, k);
+    if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
     cudaStream_t st = (cudaStream_t)stream;
-    const int n_chunks = (T + kChunk - 1) / kChunk;
     uint8_t *ws = static_cast<uint8_t *>(d_ws);
-    int32_t *cc = reinterpret_cast<int32_t *>(ws);
-    int32_t *cb = reinterpret_cast<int32_t *>(ws + align256((size_t)n_chunks * E * 4));
-    Job *jobs = reinterpret_cast<Job *>(ws + 2 * align256((size_t)n_chunks * E * 4));
-    int32_t *nj = reinterpret_cast<int32_t *>(
-        ws + 2 * align256((size_t)n_chunks * E * 4) +
-        align256(sizeof(Job) * (size_t)(std::min(E, T * k) + 1)));
+    int32_t *cc = reinterpret_cast<int32_t *>(ws + L.chunk_counts);
+    int32_t *cb = reinterpret_cast<int32_t *>(ws + L.chunk_base);
+    Job *jobs = reinterpret_cast<Job *>(ws + L.jobs);
+    int32_t *nj = reinterpret_cast<int32_t *>(ws + L.njobs);
     if (launch_topk(d_logits, T, E, k, d_ids, d_w, d_status, st) != cudaSuccess) return MOE_ERR_CUDA;
     if (launch_group(d_ids, T, k, E, 0, d_counts, d_offsets, d_perm, d_inv_perm, cc, cb, jobs, nj,
                      st) != cudaSuccess)

@@ -91,6 +91,12 @@ struct WsLayout {
 // operands are left out.
 WsLayout ws_layout(const moe_arena *A, int T, int k, uint32_t flags, bool allow_tc = true);
 
+// Workspace layout of the routing entry points (moe_api.cu): byte offsets.
+struct RouteWs {
+    size_t chunk_counts, chunk_base, jobs, njobs, total;
+};
+RouteWs route_ws(int T, int E, int k);
+
 // The host checks moe_forward makes on its arguments other than the workspace (null pointers,
 // sizes, flag combinations, alignment), before anything is enqueued.
 moe_status check_forward_args(const moe_arena *arena, const float *d_x, const float *d_logits,

@@ -1,0 +1,173 @@
+// scaled.cuh -- shared declarations of the float8 (e4m3, 128-block scaled) operators: element
+// types, the quantiser of one block, and the launchers behind the moe_scaled_* entry points.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "moe_internal.cuh"
+
+namespace moe {
+
+constexpr int kSBlk = 128;                 // columns (and weight rows) per scale
+constexpr float kE4M3Max = 448.0f;
+constexpr int kSmallT = 8;                 // most tokens of the small-batch kernels (MMA columns)
+
+__host__ __device__ inline int sblocks(int n) { return (n + kSBlk - 1) / kSBlk; }
+inline size_t dtype_bytes(int dt) { return dt == MOE_DT_F32 ? 4 : 2; }
+inline bool dtype_ok(int dt) { return dt >= MOE_DT_F32 && dt <= MOE_DT_F16; }
+
+// One call of f with a null pointer of the element type of `dt` (the type is what matters).
+template <typename F>
+inline cudaError_t with_dtype(int dt, F &&f) {
+    switch (dt) {
+        case MOE_DT_F32: return f((float *)nullptr);
+        case MOE_DT_BF16: return f((__nv_bfloat16 *)nullptr);
+        default: return f((__half *)nullptr);
+    }
+}
+
+// ------------------------------------------------------------------ element types
+
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
+template <typename T>
+__device__ __forceinline__ T from_f32(float v);
+template <>
+__device__ __forceinline__ float from_f32<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) {
+    return __float2bfloat16_rn(v);
+}
+template <>
+__device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
+
+// Four consecutive elements at p (16-byte aligned for fp32, 8-byte for the 16-bit types).
+__device__ __forceinline__ float4 load4(const float *p) {
+    return __ldg(reinterpret_cast<const float4 *>(p));
+}
+__device__ __forceinline__ float4 load4(const __nv_bfloat16 *p) {
+    const uint2 r = __ldg(reinterpret_cast<const uint2 *>(p));
+    return make_float4(__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xFFFF0000u),
+                       __uint_as_float(r.y << 16), __uint_as_float(r.y & 0xFFFF0000u));
+}
+__device__ __forceinline__ float4 load4(const __half *p) {
+    const uint2 r = __ldg(reinterpret_cast<const uint2 *>(p));
+    const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&r.x));
+    const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&r.y));
+    return make_float4(a.x, a.y, b.x, b.y);
+}
+
+// ------------------------------------------------------------------ e4m3 of one block
+
+// Two values to two e4m3 bytes (lo in the low byte), nearest, ties to even, clamped to +-448.
+__device__ __forceinline__ uint32_t cvt_e4m3x2(float lo, float hi) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// x / s to the nearest e4m3 without an intermediate rounding: the 64-bit quotient, rounded to
+// fp32 with its lost bits kept as a sticky last bit, converts as the exact quotient would (fp32
+// has 20 bits more than e4m3, and a 64-bit quotient of two fp32 values is never halfway between
+// two e4m3 values unless it is exact).
+static __device__ __noinline__ uint32_t quant4_exact(float4 v, float s) {
+    float f[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const double q = __ddiv_rn((double)f[i], (double)s);
+        float r = __double2float_rz(q);
+        if ((double)r != q) r = __uint_as_float(__float_as_uint(r) | 1u);
+        f[i] = r;
+    }
+    return cvt_e4m3x2(f[0], f[1]) | (cvt_e4m3x2(f[2], f[3]) << 16);
+}
+
+// Four values of a block with scale s > 0 as packed e4m3.  v * RN(1/s) is within 2^-23 of v / s
+// (relative); when the values 2^-21 below and above it convert to the same byte, so does v / s
+// (conversion is monotone).  Otherwise, in about one block of a thousand, or for a scale whose
+// reciprocal is not normal, the exact form decides.  A division for every value costs the
+// quantiser its memory bandwidth.
+__device__ __forceinline__ uint32_t quant4(float4 v, float s, float inv) {
+    const float a = v.x * inv, b = v.y * inv, c = v.z * inv, d = v.w * inv;
+    constexpr float kLo = 1.0f - 0x1p-21f, kHi = 1.0f + 0x1p-21f;
+    const uint32_t lo = cvt_e4m3x2(a * kLo, b * kLo) | (cvt_e4m3x2(c * kLo, d * kLo) << 16);
+    const uint32_t hi = cvt_e4m3x2(a * kHi, b * kHi) | (cvt_e4m3x2(c * kHi, d * kHi) << 16);
+    if (lo != hi || s < 0x1p-120f) return quant4_exact(v, s);
+    return lo;
+}
+
+// The block of 128 values that a warp holds, 4 per lane (0 past the row's end): the packed bytes
+// of the lane's values; *s receives the scale.  Returns the bytes; *finite is false (and bytes and
+// scale 0) when a value was not finite.
+__device__ __forceinline__ uint32_t quant_block(float4 v, float *s, bool *finite) {
+    constexpr unsigned all = 0xffffffffu;
+    // the largest magnitude as integers: a NaN or infinity has the largest bit patterns
+    const uint32_t m = max(max(__float_as_uint(v.x) & 0x7fffffffu, __float_as_uint(v.y) & 0x7fffffffu),
+                           max(__float_as_uint(v.z) & 0x7fffffffu, __float_as_uint(v.w) & 0x7fffffffu));
+    const uint32_t amax = __reduce_max_sync(all, m);
+    const bool fin = amax < 0x7f800000u;
+    const float sc = fin ? __fdiv_rn(__uint_as_float(amax), kE4M3Max) : 0.0f;
+    *s = sc;
+    *finite = fin;
+    return sc > 0.0f ? quant4(v, sc, __frcp_rn(sc)) : 0u;
+}
+
+// ------------------------------------------------------------------ launchers
+
+// ws: moe_route_workspace_size bytes.
+cudaError_t launch_route_scored(const float *logits, int T, int E, int k,
+                                const moe_route_rule &rule, int32_t *ids, float *w,
+                                int32_t *counts, int32_t *offsets, int32_t *perm,
+                                int32_t *inv_perm, uint32_t *status, void *ws, cudaStream_t st);
+
+cudaError_t launch_scaled_quantize(const void *x, int dt, int T, int K, int64_t ldx, uint8_t *q,
+                                   int64_t ldq, float *s, int64_t lds, uint32_t *status,
+                                   cudaStream_t st);
+
+struct ScaledMatmulArgs {
+    const uint8_t *a;
+    int64_t lda;
+    const float *as;
+    int64_t ldas;
+    int M, K;
+    const uint8_t *b;
+    int64_t ldb;
+    const float *bs;
+    int N;
+    void *out;
+    int dt;
+    int64_t ldo;
+    uint32_t *status;
+};
+// The product on the kernel that suits its sizes, and the workspace it needs.
+size_t scaled_matmul_ws_bytes(int M, int N, int K);
+cudaError_t launch_scaled_matmul(const ScaledMatmulArgs &a, void *ws, cudaStream_t st);
+// k_scaled_small.cu: 8 tokens per pass over the weights.
+cudaError_t launch_scaled_small(const ScaledMatmulArgs &a, cudaStream_t st);
+
+constexpr int kScaledMaxDim = 1 << 16;             // hidden and ffn of scaled experts
+constexpr int64_t kScaledMaxSlots = 1 << 24;       // (token, expert) pairs, the shared one's too
+
+struct ScaledExpertsArgs {
+    moe_scaled_weights w;
+    const void *x;
+    int x_dt;
+    int T, k;
+    const int32_t *ids;
+    const float *rw;               // routing weights [T][k]
+    const int32_t *offsets, *perm, *inv_perm;
+    const float *gate;             // [T] or null
+    void *out;
+    int out_dt;
+    uint32_t *status;
+    float *h;                      // small batches: h of (job, token) [jobs][8][ffn]
+};
+// The layer on the kernels that suit T, and the workspace they need for exactly T tokens.
+size_t scaled_experts_ws_bytes(const moe_scaled_weights &w, int T, int k);
+cudaError_t launch_scaled_experts(const ScaledExpertsArgs &a, void *ws, cudaStream_t st);
+// k_scaled_small.cu: T <= kSmallT in two kernels, and the bytes of h between them.
+size_t scaled_small_h_bytes(int T, int k, int shared, int F);
+cudaError_t launch_scaled_experts_small(const ScaledExpertsArgs &a, cudaStream_t st);
+
+}  // namespace moe

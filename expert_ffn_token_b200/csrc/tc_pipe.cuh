@@ -9,6 +9,16 @@
 #include "tc.cuh"
 
 namespace moe {
+
+// cuTensorMapEncodeTiled of the installed driver (null when it has none), and the number of SMs
+// of the current device (k_down_tc.cu).
+using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                              const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                              const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeFn encode_fn();
+int sm_count();
+
 namespace tcp {
 
 using namespace ptx;

@@ -32,13 +32,18 @@ F_KEEP_H = 8
 F_LOOKAHEAD = 16
 F_TC_I8 = 32
 
+DT_F32, DT_BF16, DT_F16 = 0, 1, 2
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
+
 EXPORTED = ["moe_arena_create", "moe_arena_destroy", "moe_workspace_size", "moe_quantize_act",
             "moe_route_workspace_size", "moe_route_topk", "moe_forward", "moe_ws_views",
             "moe_read_status", "moe_debug_dequant", "moe_status_string",
             "moe_kernels_enqueued", "moe_forward_noalloc", "moe_set_timing_events",
             "moe_router_logits", "moe_shared_gate", "moe_set_wait_limit",
             "moe_forward_routed", "moe_chain_workspace_size", "moe_chain_forward",
-            "moe_chain_status"]
+            "moe_chain_status", "moe_route_scored", "moe_scaled_quantize",
+            "moe_scaled_matmul_workspace_size", "moe_scaled_matmul",
+            "moe_scaled_experts_workspace_size", "moe_scaled_experts"]
 
 
 class ExpertDesc(ctypes.Structure):
@@ -68,8 +73,31 @@ class ChainTrace(ctypes.Structure):
                 ("early", ctypes.c_void_p)]
 
 
+class RouteRule(ctypes.Structure):
+    """moe_route_rule: score, expert groups, renormalisation, scale and an optional bias (device
+    pointer to fp32 [E] or None)."""
+    _fields_ = [("score", ctypes.c_int32), ("n_group", ctypes.c_int32),
+                ("topk_group", ctypes.c_int32), ("group_top", ctypes.c_int32),
+                ("renorm", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("d_bias", ctypes.c_void_p)]
+
+    def __init__(self, score=SCORE_SOFTMAX, n_group=1, topk_group=1, group_top=1, renorm=True,
+                 scale=1.0, d_bias=None):
+        super().__init__(score, n_group, topk_group, group_top, int(renorm), scale, d_bias)
+
+
+class ScaledWeights(ctypes.Structure):
+    """moe_scaled_weights."""
+    _fields_ = [("hidden", ctypes.c_int32), ("ffn", ctypes.c_int32),
+                ("n_experts", ctypes.c_int32), ("shared", ctypes.c_int32),
+                ("d_gate", ctypes.c_void_p), ("d_up", ctypes.c_void_p),
+                ("d_down", ctypes.c_void_p), ("d_gate_s", ctypes.c_void_p),
+                ("d_up_s", ctypes.c_void_p), ("d_down_s", ctypes.c_void_p)]
+
+
 _P = ctypes.c_void_p
 _I = ctypes.c_int
+_L = ctypes.c_int64
 _S = ctypes.c_size_t
 _U = ctypes.c_uint32
 
@@ -95,6 +123,14 @@ _lib.moe_forward_routed.argtypes = [_P, _P, _I, _I, _P, _P, _P, _P, _P, _P, _S, 
 _lib.moe_chain_workspace_size.argtypes = [_P, _I, _I, _I, _U, ctypes.POINTER(_S)]
 _lib.moe_chain_forward.argtypes = [_P, _I, _P, _I, _I, _P, _P, _S, _U, _P, _P]
 _lib.moe_chain_status.argtypes = [_P, _I, _P, _I, _I, _U, ctypes.POINTER(_P)]
+_lib.moe_route_scored.argtypes = [_P, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _S, _P]
+_lib.moe_scaled_quantize.argtypes = [_P, _I, _I, _I, _L, _P, _L, _P, _L, _P, _P]
+_lib.moe_scaled_matmul_workspace_size.argtypes = [_I, _I, _I, ctypes.POINTER(_S)]
+_lib.moe_scaled_matmul.argtypes = [_P, _L, _P, _L, _I, _I, _P, _L, _P, _I, _P, _I, _L, _P, _P,
+                                   _S, _P]
+_lib.moe_scaled_experts_workspace_size.argtypes = [_P, _I, _I, ctypes.POINTER(_S)]
+_lib.moe_scaled_experts.argtypes = [_P, _P, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _I, _P, _P,
+                                    _S, _P]
 _lib.moe_kernels_enqueued.argtypes = []
 _lib.moe_kernels_enqueued.restype = ctypes.c_uint64
 
@@ -287,7 +323,61 @@ def debug_dequant(arena: int, expert: int, which: int, d_out: int, stream=None) 
     _check(_lib.moe_debug_dequant(arena, expert, which, d_out, stream), "moe_debug_dequant")
 
 
+def route_scored(d_logits: int, T: int, E: int, k: int, rule: RouteRule, d_ids: int, d_w: int,
+                 d_counts: int, d_offsets: int, d_perm: int, d_inv_perm, d_status, d_ws: int,
+                 ws_bytes: int, stream=None) -> None:
+    """moe_route_scored: route_topk with a RouteRule (workspace: route_workspace_size)."""
+    _check(_lib.moe_route_scored(d_logits, T, E, k, ctypes.addressof(rule), d_ids, d_w, d_counts,
+                                 d_offsets, d_perm, d_inv_perm, d_status, d_ws, ws_bytes, stream),
+           "moe_route_scored")
+
+
+def scaled_quantize(d_x: int, dtype: int, T: int, K: int, ldx: int, d_q: int, ldq: int, d_s: int,
+                    lds: int, d_status=None, stream=None) -> None:
+    _check(_lib.moe_scaled_quantize(d_x, dtype, T, K, ldx, d_q, ldq, d_s, lds, d_status, stream),
+           "moe_scaled_quantize")
+
+
+def scaled_matmul_workspace_size(M: int, N: int, K: int) -> int:
+    n = _S()
+    _check(_lib.moe_scaled_matmul_workspace_size(M, N, K, ctypes.byref(n)),
+           "moe_scaled_matmul_workspace_size")
+    return n.value
+
+
+def scaled_matmul(d_a: int, lda: int, d_as: int, ldas: int, M: int, K: int, d_b: int, ldb: int,
+                  d_bs: int, N: int, d_out: int, dtype: int, ldo: int, d_status=None, d_ws=None,
+                  ws_bytes: int = 0, stream=None) -> None:
+    _check(_lib.moe_scaled_matmul(d_a, lda, d_as, ldas, M, K, d_b, ldb, d_bs, N, d_out, dtype,
+                                  ldo, d_status, d_ws, ws_bytes, stream), "moe_scaled_matmul")
+
+
+def scaled_experts_workspace_size(weights: ScaledWeights, max_tokens: int, k: int) -> int:
+    n = _S()
+    _check(_lib.moe_scaled_experts_workspace_size(ctypes.addressof(weights), max_tokens, k,
+                                                  ctypes.byref(n)),
+           "moe_scaled_experts_workspace_size")
+    return n.value
+
+
+def scaled_experts(weights: ScaledWeights, d_x: int, x_dtype: int, T: int, k: int, d_ids: int,
+                   d_w: int, d_offsets: int, d_perm: int, d_inv_perm: int, d_gate, d_out: int,
+                   out_dtype: int, d_status, d_ws: int, ws_bytes: int, stream=None) -> None:
+    _check(_lib.moe_scaled_experts(ctypes.addressof(weights), d_x, x_dtype, T, k, d_ids, d_w,
+                                   d_offsets, d_perm, d_inv_perm, d_gate, d_out, out_dtype,
+                                   d_status, d_ws, ws_bytes, stream), "moe_scaled_experts")
+
+
 # ------------------------------------------------------------------ torch convenience
+
+
+def dtype_of(t) -> int:
+    """The moe_dtype of a torch tensor (fp32, bf16 or fp16)."""
+    import torch
+    d = {torch.float32: DT_F32, torch.bfloat16: DT_BF16, torch.float16: DT_F16}.get(t.dtype)
+    if d is None:
+        raise MoeError(ERR_UNSUPPORTED, f"dtype {t.dtype}")
+    return d
 
 
 def _stream():
@@ -336,3 +426,89 @@ class Layer:
             self.close()
         except Exception:
             pass
+
+
+def _contiguous(t, name: str, shape=None, dtype=None):
+    """t, checked: on the current CUDA device, contiguous, and of the shape and type asked for."""
+    import torch
+    if not t.is_cuda or t.device.index != torch.cuda.current_device() or not t.is_contiguous():
+        raise ValueError(f"{name}: a contiguous tensor on the current CUDA device is needed")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, not {tuple(shape)}")
+    if dtype is not None and t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
+        raise ValueError(f"{name}: type {t.dtype}")
+    return t
+
+
+class ScaledExperts:
+    """The experts of one layer in e4m3 with 128 x 128 block scales, held in torch tensors, and
+    the workspace for up to max_tokens tokens (marshalling only).
+
+    gate, up [n][ffn][hidden] and down [n][hidden][ffn] (uint8 or float8_e4m3fn), scales fp32
+    [n][ceil(rows / 128)][ceil(cols / 128)], n = experts (+ 1 with `shared`)."""
+
+    def __init__(self, gate, gate_scale, up, up_scale, down, down_scale, max_tokens: int, k: int,
+                 shared: bool = False, rule: RouteRule | None = None):
+        import torch
+        n, f, h = gate.shape
+        fb, hb = -(-f // 128), -(-h // 128)
+        codes = (torch.uint8, torch.float8_e4m3fn)
+        self.tensors = (_contiguous(gate, "gate", (n, f, h), codes),
+                        _contiguous(up, "up", (n, f, h), codes),
+                        _contiguous(down, "down", (n, h, f), codes),
+                        _contiguous(gate_scale, "gate_scale", (n, fb, hb), torch.float32),
+                        _contiguous(up_scale, "up_scale", (n, fb, hb), torch.float32),
+                        _contiguous(down_scale, "down_scale", (n, hb, fb), torch.float32))
+        self.hidden, self.ffn, self.n_experts, self.k = h, f, n - int(shared), k
+        self.rule = RouteRule() if rule is None else rule
+        self.weights = ScaledWeights(h, f, n - int(shared), int(shared),
+                                     *(t.data_ptr() for t in self.tensors))
+        self.max_tokens = max_tokens
+        self.ws_bytes = scaled_experts_workspace_size(self.weights, max_tokens, k)
+        self.ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=gate.device)
+        self.route_bytes = route_workspace_size(max_tokens, self.n_experts, k)
+        self.route_ws = torch.empty(self.route_bytes, dtype=torch.uint8, device=gate.device)
+        self.status_word = torch.zeros(1, dtype=torch.int32, device=gate.device)
+
+    def route(self, logits):
+        """(ids, w, offsets, perm, inv_perm) of fp32 logits [T][experts] by the layer's rule."""
+        import torch
+        T, E, k = logits.shape[0], self.n_experts, self.k
+        _contiguous(logits, "logits", (T, E), torch.float32)
+        new = lambda *s: torch.empty(s, dtype=torch.int32, device=logits.device)  # noqa: E731
+        ids, counts, offsets, perm, inv = new(T, k), new(E), new(E + 1), new(T * k), new(T * k)
+        w = torch.empty((T, k), dtype=torch.float32, device=logits.device)
+        route_scored(logits.data_ptr(), T, E, k, self.rule, ids.data_ptr(), w.data_ptr(),
+                     counts.data_ptr(), offsets.data_ptr(), perm.data_ptr(), inv.data_ptr(),
+                     self.status_word.data_ptr(), self.route_ws.data_ptr(), self.route_bytes,
+                     _stream())
+        return ids, w, offsets, perm, inv
+
+    def forward(self, x, ids, w, offsets, perm, inv_perm, gate=None, out=None):
+        """The experts' combined output [T][hidden] for tokens routed by route() or route_topk."""
+        import torch
+        T, k, E = x.shape[0], self.k, self.n_experts
+        i32, f32 = torch.int32, torch.float32
+        _contiguous(x, "x", (T, self.hidden))
+        _contiguous(ids, "ids", (T, k), i32)
+        _contiguous(w, "w", (T, k), f32)
+        _contiguous(offsets, "offsets", (E + 1,), i32)
+        _contiguous(perm, "perm", (T * k,), i32)
+        _contiguous(inv_perm, "inv_perm", (T * k,), i32)
+        if gate is not None:
+            _contiguous(gate, "gate", (T,), f32)
+        if out is None:
+            out = torch.empty_like(x)
+        _contiguous(out, "out", (T, self.hidden))
+        scaled_experts(self.weights, x.data_ptr(), dtype_of(x), T, k, ids.data_ptr(),
+                       w.data_ptr(), offsets.data_ptr(), perm.data_ptr(), inv_perm.data_ptr(),
+                       None if gate is None else gate.data_ptr(), out.data_ptr(), dtype_of(out),
+                       self.status_word.data_ptr(), self.ws.data_ptr(), self.ws_bytes, _stream())
+        return out
+
+    def __call__(self, x, logits, gate=None, out=None):
+        """route(logits), then forward."""
+        return self.forward(x, *self.route(logits), gate=gate, out=out)
+
+    def status(self, clear: bool = True) -> int:
+        return read_status(self.status_word.data_ptr(), _stream(), clear)

@@ -307,6 +307,121 @@ moe_status moe_chain_forward(const moe_chain_layer *host_layers, int n_layers, c
 moe_status moe_chain_status(const moe_chain_layer *host_layers, int n_layers, void *d_ws, int T,
                             int k, uint32_t flags, uint32_t **d_status_word);
 
+/* ------------------------------------------------------------------------------------------
+ * Scored routing, and experts in 8-bit floating point with block scales.
+ *
+ * The pages route by the softmax of the chosen logits and store their experts as GGUF blocks;
+ * the entry points below have no counterpart there.  They serve checkpoints whose routers score
+ * experts with a sigmoid, a balance bias and expert groups, and whose experts are stored as
+ * e4m3 bytes with one fp32 scale per 128 x 128 weights.
+ *
+ * e4m3 is the OCP 8-bit format of 4 exponent and 3 mantissa bits (largest value 448, codes 0x7f
+ * and 0xff NaN).  A "scaled" activation matrix [M][K] is M rows of e4m3 bytes and one fp32 scale
+ * per row and 128 consecutive columns, stored block-major: d_s[b * lds + m] is the scale of row
+ * m, columns [128 b, 128 b + 128).  A "scaled" weight matrix [N][K] is N rows of e4m3 bytes and
+ * scales [ceil(N / 128)][ceil(K / 128)], one per block of 128 x 128.  A value is byte * scale;
+ * the last block of a row or column may be short.
+ * ---------------------------------------------------------------------------------------- */
+
+/* Element types of activations and outputs. */
+typedef enum {
+    MOE_DT_F32 = 0,
+    MOE_DT_BF16 = 1,
+    MOE_DT_F16 = 2
+} moe_dtype;
+
+/* How a router turns a logit into a score. */
+typedef enum {
+    MOE_SCORE_SOFTMAX = 0,     /* softmax over all E logits */
+    MOE_SCORE_SIGMOID = 1      /* 1 / (1 + exp(-logit))     */
+} moe_score;
+
+/* A routing rule (host memory, read during the call).  With s_e the score and
+ * v_e = s_e + d_bias[e] (v_e = s_e when d_bias is NULL) of expert e:
+ *   groups    the E experts are n_group runs of E / n_group; a group's value is the sum of its
+ *             group_top largest v_e, and only the topk_group groups of largest value stay
+ *             (ties: the lower group)
+ *   ids       the k largest v_e of the groups that stay, in descending order (ties: the lower
+ *             id); the bias takes no part in the weights
+ *   weights   scale * s_e, divided by the sum of the k chosen scores when renorm != 0 (weights
+ *             0 when that sum is 0)
+ * Scores, values and group sums are those of 64-bit arithmetic; without a bias the experts are
+ * ordered by their logits, which both scores follow.                                         */
+typedef struct {
+    int32_t score;             /* moe_score */
+    int32_t n_group;           /* 1..32, divides E; 1: no groups */
+    int32_t topk_group;        /* 1..n_group */
+    int32_t group_top;         /* 1 or 2, at most E / n_group */
+    int32_t renorm;
+    float scale;               /* finite */
+    const float *d_bias;       /* fp32 [E] or NULL */
+} moe_route_rule;
+
+/* moe_route_topk with a rule: the same outputs (d_ids, d_w, d_counts, d_offsets, d_perm,
+ * d_inv_perm, all as there), workspace (moe_route_workspace_size for T, E, k) and limits
+ * (1 <= k <= min(E, 32), E <= 4096); k <= topk_group * E / n_group.  A token with a logit or a
+ * v_e that is not finite gets ids 0..k-1, weights 1/k and MOE_ERR_NONFINITE in d_status (may be
+ * NULL).  An expert is masked by a large negative finite logit or bias.                      */
+moe_status moe_route_scored(const float *d_logits, int T, int E, int k,
+                            const moe_route_rule *host_rule, int32_t *d_ids, float *d_w,
+                            int32_t *d_counts, int32_t *d_offsets, int32_t *d_perm,
+                            int32_t *d_inv_perm, uint32_t *d_status, void *d_ws,
+                            size_t ws_bytes, void *stream);
+
+/* d_x [T][K] (dtype: moe_dtype, rows ldx elements apart, any alignment of its type) -> a scaled
+ * matrix: d_q rows ldq bytes apart (16-byte aligned, ldq a multiple of 16), d_s with lds >= T.
+ * Per row and 128 columns: s = amax / 448 in fp32 and q = the e4m3 value nearest x / s (ties to
+ * even; the quotient is not rounded in between); a block whose s is 0 is stored as zeros, a block with a
+ * non-finite value as zeros with MOE_ERR_NONFINITE in d_status (may be NULL).  Bytes of d_q past
+ * column K are left as they were.  T may be 0.                                               */
+moe_status moe_scaled_quantize(const void *d_x, int dtype, int T, int K, int64_t ldx,
+                               uint8_t *d_q, int64_t ldq, float *d_s, int64_t lds,
+                               uint32_t *d_status, void *stream);
+
+/* d_out [M][N] (dtype, rows ldo elements apart) = the scaled activations d_a [M][K] (rows lda
+ * bytes apart, scales d_as with stride ldas >= M) times the transposed scaled weights d_b [N][K]
+ * (rows ldb bytes apart, scales d_bs contiguous): every block of 128 k is summed in fp32, scaled
+ * in fp32 and added up in fp32, in an order that depends on the sizes alone; one rounding to
+ * dtype at the end.  d_a and d_b 16-byte aligned, lda and ldb multiples of 16 (bytes past column
+ * K are not used).  d_out aligned to its type.  d_status (may be NULL) receives device-side
+ * errors.  The workspace (moe_scaled_matmul_workspace_size; may be 0 bytes, then d_ws may be
+ * NULL) is 256-byte aligned scratch.  M may be 0.                                            */
+moe_status moe_scaled_matmul_workspace_size(int M, int N, int K, size_t *bytes);
+moe_status moe_scaled_matmul(const uint8_t *d_a, int64_t lda, const float *d_as, int64_t ldas,
+                             int M, int K, const uint8_t *d_b, int64_t ldb, const float *d_bs,
+                             int N, void *d_out, int dtype, int64_t ldo, uint32_t *d_status,
+                             void *d_ws, size_t ws_bytes, void *stream);
+
+/* The experts of one layer as scaled matrices, n_experts of them plus, when shared != 0, one
+ * more at index n_experts for the always-on shared expert.  gate and up [n][ffn][hidden], down
+ * [n][hidden][ffn], contiguous, 16-byte aligned; scales [n][ceil(rows / 128)][ceil(cols / 128)].
+ * hidden and ffn are multiples of 16.                                                        */
+typedef struct {
+    int32_t hidden, ffn, n_experts, shared;
+    const uint8_t *d_gate, *d_up, *d_down;
+    const float *d_gate_s, *d_up_s, *d_down_s;
+} moe_scaled_weights;
+
+/* a4-a7 on scaled experts, for tokens routed by moe_route_scored or moe_route_topk (d_ids, d_w,
+ * d_offsets, d_perm, d_inv_perm as written there for T, n_experts, k):
+ *   x^ = d_x [T][hidden] as moe_scaled_quantize stores it, g = W_gate x^, u = W_up x^,
+ *   h = g / (1 + exp(-g)) * u in fp32, h^ = h quantised likewise per 128 values of ffn,
+ *   y = W_down h^, d_out[t] = sum_j w[t][j] y[t][ids[t][j]] (+ gate[t] y[t][shared])
+ * with d_x and d_out [T][hidden] contiguous of x_dtype and out_dtype, 16-byte aligned, d_gate
+ * fp32 [T] (NULL: 1; only with shared).  A routed id or a slot outside its range is skipped and
+ * reported as MOE_ERR_BOUNDS in d_status (may be NULL), a non-finite block of x or h is taken as
+ * zeros and reported as MOE_ERR_NONFINITE.  1 <= T <= the max_tokens the workspace was sized for
+ * (moe_scaled_experts_workspace_size; 256-byte aligned scratch).  Results do not change from
+ * call to call.                                                                              */
+moe_status moe_scaled_experts_workspace_size(const moe_scaled_weights *host_weights,
+                                             int max_tokens, int k, size_t *bytes);
+moe_status moe_scaled_experts(const moe_scaled_weights *host_weights, const void *d_x,
+                              int x_dtype, int T, int k, const int32_t *d_ids, const float *d_w,
+                              const int32_t *d_offsets, const int32_t *d_perm,
+                              const int32_t *d_inv_perm, const float *d_gate, void *d_out,
+                              int out_dtype, uint32_t *d_status, void *d_ws, size_t ws_bytes,
+                              void *stream);
+
 /* Number of kernels this library has enqueued (or recorded into a CUDA graph under stream
  * capture) in this process since it was loaded.  Counting a captured forward gives the
  * kernels each replay of that graph launches. */

@@ -1,0 +1,451 @@
+"""GPU checks of scored routing and of the float8 block-scaled operators against plain 64-bit forms
+(scaled_ref), at the sizes and masks where they can go wrong, and of a run of them together."""
+import numpy as np
+import pytest
+
+import scaled_ref as ref
+
+from gpu_helpers import torch_cuda
+
+pytestmark = pytest.mark.gpu
+
+EPS = {"float32": 2.0 ** -24, "bfloat16": 2.0 ** -8, "float16": 2.0 ** -11}   # half a step
+
+
+@pytest.fixture(scope="module")
+def torch():
+    t = torch_cuda()
+    from expert_ffn_token_b200 import moe  # noqa: F401  (fails loudly if the library is missing)
+    return t
+
+
+@pytest.fixture(scope="module")
+def moe(torch):
+    from expert_ffn_token_b200 import moe as m
+    return m
+
+
+def _stream(torch):
+    return torch.cuda.current_stream().cuda_stream
+
+
+def _dev(torch, a):
+    return torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+# ------------------------------------------------------------------ scored routing
+
+RULES = {
+    "softmax": dict(score="softmax", renorm=True),
+    "softmax kept": dict(score="softmax", renorm=False, scale=1.5),
+    "softmax bias": dict(score="softmax", renorm=True, bias=0.01),
+    "sigmoid": dict(score="sigmoid", renorm=False),
+    "sigmoid bias": dict(score="sigmoid", renorm=True, scale=2.5, bias=0.3),
+    "groups top1": dict(score="softmax", renorm=True, n_group=4, topk_group=2, group_top=1),
+    "groups top1 bias": dict(score="sigmoid", renorm=True, n_group=4, topk_group=3, group_top=1,
+                             bias=0.2),
+    "groups top2": dict(score="sigmoid", renorm=True, n_group=4, topk_group=1, group_top=2),
+    "groups top2 bias": dict(score="sigmoid", renorm=True, scale=2.5, n_group=4, topk_group=2,
+                             group_top=2, bias=0.3),
+}
+
+
+def run_route(torch, moe, l, k, score="softmax", n_group=1, topk_group=1, group_top=1, renorm=True,
+              scale=1.0, bias=None):
+    T, E = l.shape
+    ld = _dev(torch, l)
+    bd = None if bias is None else _dev(torch, bias)
+    new = lambda n: torch.full((n,), -7, dtype=torch.int32, device="cuda")  # noqa: E731
+    ids, counts, offs, perm, inv = new(T * k), new(E), new(E + 1), new(T * k), new(T * k)
+    w = torch.full((T, k), -7.0, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    n = moe.route_workspace_size(T, E, k)
+    ws = torch.full((n,), 171, dtype=torch.uint8, device="cuda")
+    rule = moe.RouteRule(moe.SCORE_SIGMOID if score == "sigmoid" else moe.SCORE_SOFTMAX, n_group,
+                         topk_group, group_top, renorm, scale,
+                         None if bd is None else bd.data_ptr())
+    moe.route_scored(ld.data_ptr(), T, E, k, rule, ids.data_ptr(), w.data_ptr(), counts.data_ptr(),
+                     offs.data_ptr(), perm.data_ptr(), inv.data_ptr(), status.data_ptr(),
+                     ws.data_ptr(), n, _stream(torch))
+    torch.cuda.synchronize()
+    out = [t.cpu().numpy() for t in (ids.view(T, k), w, counts, offs, perm, inv)]
+    return (*out, int(status.item()))
+
+
+def check_route(torch, moe, l, k, rule):
+    T, E = l.shape
+    rule = dict(rule)
+    ids, w, counts, offs, perm, inv, status = run_route(torch, moe, l, k, **rule)
+    full = dict(score="softmax", n_group=1, topk_group=1, group_top=1, renorm=True, scale=1.0,
+                bias=None)
+    full.update(rule)
+    rid, rw = ref.route(l, k, **full)
+    assert status == 0
+    assert np.array_equal(ids, rid)
+    # the scores are 64-bit; a weight rounds to fp32 once (the normal range's half step, and
+    # half the smallest subnormal below it)
+    assert (np.abs(w - rw) <= 2.0 ** -23 * np.abs(rw) + 2.0 ** -149).all()
+    rc, ro, rp, ri = ref.group(rid, E)
+    assert np.array_equal(counts, rc) and np.array_equal(offs, ro)
+    assert np.array_equal(perm, rp) and np.array_equal(inv, ri)
+
+
+@pytest.mark.parametrize("name", list(RULES))
+@pytest.mark.parametrize("T,E,k", [(1, 256, 8), (3, 512, 10), (17, 20, 3), (65, 64, 6),
+                                   (300, 132, 12), (2, 4096, 32), (1500, 512, 10)])
+def test_route_scored(torch, moe, name, T, E, k):
+    rng = np.random.default_rng(T * 7919 + E + k)
+    rule = dict(RULES[name])
+    if "bias" in rule:
+        rule["bias"] = (rule["bias"] * rng.standard_normal(E)).astype(np.float32)
+    l = (2 * rng.standard_normal((T, E))).astype(np.float32)
+    check_route(torch, moe, l, k, rule)
+
+
+@pytest.mark.parametrize("name", list(RULES))
+def test_route_scored_ties_and_masks(torch, moe, name):
+    """Logits on a coarse grid (ties go to the lower id), experts masked by the lowest fp32 value,
+    rows with fewer open experts than k, rows with none, rows of one value."""
+    T, E, k = 64, 64, 8
+    rng = np.random.default_rng(5)
+    l = np.round(2 * rng.standard_normal((T, E))).astype(np.float32)
+    low = np.finfo(np.float32).min
+    l[:16, rng.permutation(E)[:40]] = low
+    l[16:24, 5:] = low
+    l[24:28] = low
+    l[28:32] = 3.0
+    l[32:36] = 0.0
+    l[36:40] = -90.0
+    l[40:44] *= 20
+    rule = dict(RULES[name])
+    if "bias" in rule:
+        rule["bias"] = (np.round(4 * rng.standard_normal(E)) / 8).astype(np.float32)
+    check_route(torch, moe, l, k, rule)
+
+
+@pytest.mark.parametrize("name", ["softmax", "sigmoid bias", "groups top2 bias"])
+def test_route_scored_near_ties(torch, moe, name):
+    """Neighbouring fp32 logits and biases: scores that differ in their last fp32 bits only are
+    ordered as their 64-bit values are."""
+    T, E, k = 128, 96, 8
+    rng = np.random.default_rng(11)
+    base = rng.standard_normal((T, 1)).astype(np.float32)
+    steps = rng.integers(-3, 4, (T, E)).astype(np.float32)
+    l = (base + steps * np.spacing(np.abs(base))).astype(np.float32)
+    rule = dict(RULES[name])
+    if "bias" in rule:
+        rule["bias"] = (0.25 + rng.integers(-2, 3, E) * 2.0 ** -25).astype(np.float32)
+    check_route(torch, moe, l, k, rule)
+
+
+def test_route_scored_non_finite_rows(torch, moe):
+    T, E, k = 9, 40, 4
+    rng = np.random.default_rng(2)
+    l = rng.standard_normal((T, E)).astype(np.float32)
+    l[1, 39], l[4, 0], l[7, 20] = np.nan, np.inf, -np.inf
+    ids, w, counts, offs, perm, inv, status = run_route(torch, moe, l, k, score="sigmoid")
+    assert status == moe.ERR_NONFINITE
+    rid, _ = ref.route(np.nan_to_num(l, nan=0, posinf=0, neginf=0), k, "sigmoid", 1, 1, 1, True, 1.0,
+                       None)
+    for t in (1, 4, 7):
+        rid[t] = np.arange(k)
+        assert np.array_equal(w[t], np.full(k, 0.25, np.float32))
+    assert np.array_equal(ids, rid)
+    assert np.array_equal(counts, ref.group(rid, E)[0])
+    bias = np.zeros(E, np.float32)
+    bias[3] = np.nan
+    ids, _, _, _, _, _, status = run_route(torch, moe, np.zeros((2, E), np.float32), k, bias=bias)
+    assert status == moe.ERR_NONFINITE and np.array_equal(ids, np.tile(np.arange(k), (2, 1)))
+
+
+# ------------------------------------------------------------------ quantiser
+
+
+def run_quantize(torch, moe, x, ldx=None, ldq=None, extra_rows=0):
+    """x: torch tensor on the device [T][K] (a view with stride ldx)."""
+    T, K = x.shape
+    ldx = x.stride(0) if ldx is None else ldx
+    ldq = -(-K // 16) * 16 if ldq is None else ldq
+    q = torch.full((T, ldq), 0xAB, dtype=torch.uint8, device="cuda")
+    lds = T + extra_rows
+    s = torch.full((ref.blocks(K), lds), -3.0, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    moe.scaled_quantize(x.data_ptr(), moe.dtype_of(x), T, K, ldx, q.data_ptr(), ldq, s.data_ptr(),
+                        lds, status.data_ptr(), _stream(torch))
+    torch.cuda.synchronize()
+    return q.cpu().numpy(), s.cpu().numpy(), int(status.item())
+
+
+@pytest.mark.parametrize("dtype", list(EPS))
+@pytest.mark.parametrize("T,K,pad", [(1, 1, 0), (1, 128, 0), (3, 2560, 0), (5, 130, 0), (7, 127, 3),
+                                     (66, 300, 4), (129, 641, 1), (4, 4096, 8)])
+def test_quantize_bits(torch, moe, dtype, T, K, pad):
+    rng = np.random.default_rng(T * 31 + K)
+    x = rng.standard_normal((T, K + pad)) * np.exp(3 * rng.standard_normal((T, 1)))
+    x[:, ::7] *= 20
+    xd = _dev(torch, x).to(getattr(torch, dtype))[:, :K]
+    q, s, status = run_quantize(torch, moe, xd, ldx=K + pad, ldq=-(-K // 16) * 16 + 32, extra_rows=3)
+    rq, rs = ref.quantize(xd.double().cpu().numpy())
+    # a few of these values pass the largest fp16: their blocks are reported
+    assert status == (0 if bool(torch.isfinite(xd).all()) else moe.ERR_NONFINITE)
+    assert np.array_equal(q[:, :K], rq) and np.array_equal(s[:, :T], rs)
+    assert (q[:, K:] == 0xAB).all() and (s[:, T:] == -3.0).all()      # left as they were
+
+
+def test_quantize_ties_zeros_and_extremes(torch, moe):
+    """Quotients exactly halfway between e4m3 values, all-zero blocks, subnormal scales, the
+    largest and smallest magnitudes."""
+    rows = [np.concatenate([[448.0], ref._MID, [0.0]])[:128], np.zeros(128),
+            np.full(128, 1e-45), np.full(128, -3e-42) * (1 + np.arange(128) % 3),
+            np.linspace(-3.4e38, 3.4e38, 128), np.concatenate([[1e-36], np.full(127, 1e-44)]),
+            -np.concatenate([[448.0 * 2 ** -9], ref._MID * 2.0 ** -9, [0.0]])[:128]]
+    x = np.stack(rows).astype(np.float32)
+    q, s, status = run_quantize(torch, moe, _dev(torch, x))
+    rq, rs = ref.quantize(x)
+    assert status == 0
+    assert np.array_equal(s, rs)
+    assert np.array_equal(ref.E4M3[q], ref.E4M3[rq])
+    rng = np.random.default_rng(3)
+    x = np.ldexp(rng.integers(-64, 65, (400, 256)).astype(np.float32), rng.integers(-20, 20, (400, 1)))
+    q, s, _ = run_quantize(torch, moe, _dev(torch, x.astype(np.float32)))
+    rq, rs = ref.quantize(x)
+    assert np.array_equal(s, rs) and np.array_equal(ref.E4M3[q], ref.E4M3[rq])
+
+
+def test_quantize_non_finite_blocks(torch, moe):
+    x = np.random.default_rng(0).standard_normal((6, 384)).astype(np.float32)
+    x[0, 5], x[2, 200], x[5, 383] = np.nan, np.inf, -np.inf
+    q, s, status = run_quantize(torch, moe, _dev(torch, x))
+    rq, rs = ref.quantize(x)
+    assert status == moe.ERR_NONFINITE
+    assert np.array_equal(q, rq) and np.array_equal(s, rs)
+    assert s[0, 0] == 0 and s[1, 2] == 0 and s[2, 5] == 0 and (q[0, :128] == 0).all()
+
+
+# ------------------------------------------------------------------ product
+
+
+@pytest.mark.parametrize("dtype", list(EPS))
+@pytest.mark.parametrize("M,N,K", [(1, 1, 1), (1, 16, 128), (1, 1280, 2560), (2, 130, 64), (7, 33, 300),
+                                   (8, 257, 1000), (9, 16, 16), (16, 300, 128), (17, 128, 130),
+                                   (64, 640, 2560), (127, 129, 257), (128, 256, 384), (129, 513, 500),
+                                   (300, 100, 1296), (777, 1001, 144), (40, 2560, 4096),
+                                   (1, 520, 8192), (513, 700, 640)])
+def test_matmul(torch, moe, dtype, M, N, K):
+    rng = np.random.default_rng(M * 131 + N * 17 + K)
+    lda, ldb, ldas, ldo = -(-K // 16) * 16 + 16, -(-K // 16) * 16 + 32, M + 3, N + 5
+    # bytes past column K are NaN codes, scales past row M NaN: neither may be used
+    a, b = np.full((M, lda), 0x7F, np.uint8), np.full((N, ldb), 0xFF, np.uint8)
+    a[:, :K] = ref.encode(np.clip(rng.standard_normal((M, K)) * 130, -448, 448))
+    b[:, :K] = ref.encode(np.clip(rng.standard_normal((N, K)) * 130, -448, 448))
+    sa = np.full((ref.blocks(K), ldas), np.nan, np.float32)
+    sa[:, :M] = np.exp(rng.standard_normal((ref.blocks(K), M))) * 1e-2
+    sb = (np.exp(rng.standard_normal((ref.blocks(N), ref.blocks(K)))) * 1e-3).astype(np.float32)
+    ad, bd, sad, sbd = (_dev(torch, v) for v in (a, b, sa, sb))
+    out = torch.full((M, ldo), -9.0, dtype=getattr(torch, dtype), device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    nb = moe.scaled_matmul_workspace_size(M, N, K)
+    ws = torch.full((max(nb, 1),), 255, dtype=torch.uint8, device="cuda")
+
+    def call():
+        moe.scaled_matmul(ad.data_ptr(), lda, sad.data_ptr(), ldas, M, K, bd.data_ptr(), ldb,
+                          sbd.data_ptr(), N, out.data_ptr(), moe.dtype_of(out), ldo,
+                          status.data_ptr(), ws.data_ptr(), nb, _stream(torch))
+        torch.cuda.synchronize()
+        return out.clone()
+
+    first = call()
+    got = first.double().cpu().numpy()
+    want, mag = ref.matmul(ref.wide_act(a[:, :K], sa[:, :M]), ref.wide_weight(b[:, :K], sb))
+    assert int(status.item()) == 0
+    err = np.abs(got[:, :N] - want)
+    assert (err <= mag * ref.product_error(ref.blocks(K)) + np.abs(want) * EPS[dtype] +
+            2.0 ** -25).all(), (err / mag).max()
+    assert (got[:, N:] == -9.0).all()
+    assert torch.equal(first.view(torch.uint8), call().view(torch.uint8))       # repeats bit for bit
+
+
+def test_matmul_nan_and_zero_scales(torch, moe):
+    """A NaN code reaches its row or column and no other; zero scales give zeros."""
+    for M in (3, 40):
+        N, K = 70, 256
+        rng = np.random.default_rng(M)
+        a = ref.encode(rng.standard_normal((M, K)) * 100)
+        b = ref.encode(rng.standard_normal((N, K)) * 100)
+        a[1, 130], b[5, 7] = 0x7F, 0xFF
+        sa = np.ones((2, M), np.float32)
+        sa[:, 2] = 0.0
+        sb = np.ones((1, 2), np.float32)
+        ad, bd, sad, sbd = (_dev(torch, v) for v in (a, b, sa, sb))
+        out = torch.zeros(M, N, device="cuda")
+        moe.scaled_matmul(ad.data_ptr(), K, sad.data_ptr(), M, M, K, bd.data_ptr(), K, sbd.data_ptr(),
+                          N, out.data_ptr(), 0, N, None, None, 0, _stream(torch))
+        got = out.cpu().numpy()
+        want = np.zeros((M, N), bool)
+        want[1], want[:, 5] = True, True
+        assert np.array_equal(np.isnan(got), want)
+        assert (got[2][~want[2]] == 0).all()
+
+
+# ------------------------------------------------------------------ experts
+
+
+def make_layer(torch, moe, rng, E, H, F, k, shared, T):
+    W = {"shared": shared}
+    for name, rows, cols in (("gate", F, H), ("up", F, H), ("down", H, F)):
+        W[name] = ref.random_weights(rng, E + int(shared), rows, cols)
+    t = [_dev(torch, W[n][i]) for n in ("gate", "up", "down") for i in (0, 1)]
+    return W, moe.ScaledExperts(*t, T, k, shared=shared)
+
+
+def run_experts(torch, layer, x, ids, w, gate, out_dtype):
+    E = layer.n_experts
+    counts, offs, perm, inv = ref.group(ids, E)
+    layer.ws.fill_(0xA5)
+    out = torch.full(x.shape, float("nan"), dtype=out_dtype, device="cuda")
+    layer.forward(x, _dev(torch, ids), _dev(torch, w), _dev(torch, offs), _dev(torch, perm),
+                  _dev(torch, inv), gate=None if gate is None else _dev(torch, gate), out=out)
+    torch.cuda.synchronize()
+    return out
+
+
+@pytest.mark.parametrize("xt,ot", [("bfloat16", "bfloat16"), ("float32", "float32"),
+                                   ("float16", "float16"), ("bfloat16", "float32")])
+@pytest.mark.parametrize("T,E,k,H,F,shared", [
+    (1, 8, 2, 256, 128, False), (1, 6, 6, 144, 48, True), (2, 16, 4, 512, 640, True),
+    (3, 40, 5, 384, 144, True), (8, 5, 3, 272, 272, False), (9, 8, 2, 256, 128, False),
+    (16, 4, 4, 400, 80, True), (33, 24, 3, 144, 400, True), (150, 3, 2, 640, 256, True),
+    (130, 64, 1, 256, 16, False), (300, 2, 1, 16, 128, True)])
+def test_experts(torch, moe, xt, ot, T, E, k, H, F, shared):
+    rng = np.random.default_rng(T * 1009 + E * 31 + H + F)
+    W, layer = make_layer(torch, moe, rng, E, H, F, k, shared, T)
+    x = rng.standard_normal((T, H))
+    x[:, ::50] *= 20
+    xd = _dev(torch, x).to(getattr(torch, xt))
+    ids = np.argsort(-rng.standard_normal((T, E)), 1)[:, :k].astype(np.int32)
+    w = rng.random((T, k)).astype(np.float32)
+    gate = rng.random(T).astype(np.float32) if shared and T % 2 else None
+    out = run_experts(torch, layer, xd, ids, w, gate, getattr(torch, ot))
+    assert layer.status() == 0
+    want, tol = ref.experts(xd.double().cpu().numpy(), ids, w, gate, W)
+    err = np.abs(out.double().cpu().numpy() - want)
+    assert (err <= tol + np.abs(want) * EPS[ot] + 2.0 ** -25).all(), (err / tol).max()
+    again = run_experts(torch, layer, xd, ids, w, gate, getattr(torch, ot))
+    assert torch.equal(out.view(torch.uint8), again.view(torch.uint8))
+
+
+@pytest.mark.parametrize("T", [1, 7, 20])
+def test_experts_same_expert_twice(torch, moe, T):
+    """An id that a token names twice counts with both weights."""
+    E, k, H, F = 6, 3, 256, 128
+    rng = np.random.default_rng(T)
+    W, layer = make_layer(torch, moe, rng, E, H, F, k, False, T)
+    x = rng.standard_normal((T, H)).astype(np.float32)
+    ids = rng.integers(0, E, (T, k)).astype(np.int32)
+    ids[0] = 2
+    w = rng.random((T, k)).astype(np.float32)
+    out = run_experts(torch, layer, _dev(torch, x), ids, w, None, torch.float32)
+    want, tol = ref.experts(x, ids, w, None, W)
+    assert layer.status() == 0
+    assert (np.abs(out.cpu().numpy() - want) <= tol + np.abs(want) * 2.0 ** -24).all()
+
+
+@pytest.mark.parametrize("T", [4, 40])
+def test_experts_non_finite_and_zero_tokens(torch, moe, T):
+    """A block of x that is not finite is taken as zeros and reported; other tokens keep their
+    bits; a token of zeros gives zeros."""
+    E, k, H, F = 8, 2, 384, 128
+    rng = np.random.default_rng(T)
+    W, layer = make_layer(torch, moe, rng, E, H, F, k, True, T)
+    x = rng.standard_normal((T, H)).astype(np.float32)
+    x[2] = 0.0
+    ids = np.argsort(-rng.standard_normal((T, E)), 1)[:, :k].astype(np.int32)
+    w = rng.random((T, k)).astype(np.float32)
+    clean = run_experts(torch, layer, _dev(torch, x), ids, w, None, torch.float32).cpu().numpy()
+    assert layer.status() == 0
+    assert (clean[2] == 0).all()
+    bad = x.copy()
+    bad[1, 200] = np.inf
+    got = run_experts(torch, layer, _dev(torch, bad), ids, w, None, torch.float32).cpu().numpy()
+    assert layer.status() == moe.ERR_NONFINITE
+    zeroed = x.copy()
+    zeroed[1, 128:256] = 0
+    same = run_experts(torch, layer, _dev(torch, zeroed), ids, w, None, torch.float32).cpu().numpy()
+    assert np.array_equal(got, same)
+    others = np.arange(T) != 1
+    assert np.array_equal(got[others], clean[others])
+
+
+@pytest.mark.parametrize("T", [3, 40])
+def test_experts_out_of_range_ids_are_skipped(torch, moe, T):
+    """An id or a slot that no router wrote is reported and takes no part; nothing is read past
+    the experts or the slots."""
+    E, k, H, F = 6, 2, 256, 128
+    rng = np.random.default_rng(T)
+    W, layer = make_layer(torch, moe, rng, E, H, F, k, False, T)
+    x = _dev(torch, rng.standard_normal((T, H)).astype(np.float32))
+    ids = np.argsort(-rng.standard_normal((T, E)), 1)[:, :k].astype(np.int32)
+    w = rng.random((T, k)).astype(np.float32)
+    counts, offs, perm, inv = ref.group(ids, E)
+    bad_ids, bad_inv = ids.copy(), inv.copy()
+    bad_ids[1, 0] = E + 3
+    bad_inv[2 * k + 1] = T * k + 5
+    out = torch.zeros(T, H, device="cuda")
+    layer.forward(x, _dev(torch, bad_ids), _dev(torch, w), _dev(torch, offs), _dev(torch, perm),
+                  _dev(torch, bad_inv if T > 8 else inv), out=out)
+    assert layer.status() == moe.ERR_BOUNDS
+    w2 = w.copy()
+    w2[1, 0] = 0
+    if T > 8:
+        w2[2, 1] = 0
+    want, tol = ref.experts(x.cpu().numpy(), ids, w2, None, W)
+    # what is left out differs from what a zero weight adds by the rounding of a sum at most
+    err = np.abs(out.cpu().numpy() - want)
+    assert (err <= tol + np.abs(want) * 2.0 ** -24).all()
+
+
+# ------------------------------------------------------------------ together
+
+
+@pytest.mark.parametrize("T", [1, 6, 37, 200])
+def test_route_then_experts_eager_captured_and_on_another_stream(torch, moe, T):
+    """The router and the experts as a decoder layer runs them, against the plain forms; the same
+    calls replayed from a CUDA graph on new inputs, and run on a side stream, give the same bits."""
+    E, k, H, F = 24, 4, 384, 144
+    rng = np.random.default_rng(T)
+    W, layer = make_layer(torch, moe, rng, E, H, F, k, True, T)
+    bias = _dev(torch, (0.1 * rng.standard_normal(E)).astype(np.float32))
+    layer.rule = moe.RouteRule(moe.SCORE_SIGMOID, 4, 2, 2, True, 2.5, bias.data_ptr())
+    xs = [_dev(torch, rng.standard_normal((T, H))).to(torch.bfloat16) for _ in range(2)]
+    ls = [_dev(torch, (2 * rng.standard_normal((T, E))).astype(np.float32)) for _ in range(2)]
+    gate = _dev(torch, rng.random(T).astype(np.float32))
+    eager = [layer(x, l, gate=gate).clone() for x, l in zip(xs, ls)]
+    assert layer.status() == 0
+    for x, l, o in zip(xs, ls, eager):
+        ids, w = ref.route(l.cpu().numpy(), k, "sigmoid", 4, 2, 2, True, 2.5, bias.cpu().numpy())
+        assert np.array_equal(layer.route(l)[0].cpu().numpy(), ids)
+        want, tol = ref.experts(x.double().cpu().numpy(), ids, w.astype(np.float32),
+                                gate.cpu().numpy(), W)
+        # the routing weights carry half an fp32 step, like a rounding of y
+        err = np.abs(o.double().cpu().numpy() - want)
+        assert (err <= tol + np.abs(want) * EPS["bfloat16"]).all()
+    x, l = xs[0].clone(), ls[0].clone()
+    out = torch.empty_like(x)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        layer(x, l, gate=gate, out=out)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    assert torch.equal(out, eager[0])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        layer(x, l, gate=gate, out=out)
+    for i in (1, 0, 1):
+        x.copy_(xs[i])
+        l.copy_(ls[i])
+        out.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, eager[i])
+    assert layer.status() == 0
