@@ -8,21 +8,25 @@
 // products, fp32 sums); every block starts a new one.  The epilogue warps take it out of tensor
 // memory and add P_b * (as * bs) to running totals in registers.
 //
-// Tile: 128 tokens (the MMA's N side, the tile's own count rounded up to 16) by two M = 128
-// operands of weight rows: 256 rows of one matrix, or 128 gate rows and the 128 up rows of the
-// same ffn values.  Weights sit on the M side so that an expert with few tokens wastes few MMA
-// columns, and so that a tensor-memory lane is a weight row: the block scale of the weights is
-// one number per operand and lanes write neighbouring outputs.  One persistent CTA per SM.
+// Tile: 128 tokens (the MMA's M side) by 256 weight rows (N): rows of one matrix, or 128 gate rows
+// and the 128 up rows of the same ffn values.  Tokens sit on the M side so that a tensor-memory
+// lane is a token: an epilogue thread's scale is then one number per block and operand, held in
+// a register.  With the weights on the M side the scale changes from column to column and has to
+// be read from shared memory, two 16-byte loads per four elements; the loads, not the
+// additions, then bound the kernel (1380 clocks per block of 128 k against 512 of MMA).  An
+// expert with few tokens leaves rows of the MMA unused, which costs nothing that counts: it is
+// bound by its weights' bytes.  One persistent CTA per SM.
 //
 // Roles (384 threads; registers move from the first four warps to the epilogue):
 //   warp 0        TMA producer: weight boxes of 128 rows x 128 bytes, token rows as boxes of 16
 //                 or, for routed tokens, gathered four at a time
 //   warp 1        tensor-memory allocation and the MMA issuer
-//   warps 2-3     scales: as * bs of every column and block, into a ring
-//   warps 4-11    epilogue: lane quarter (warp % 4), 64 columns each, both operands
+//   warps 4-11    epilogue: lane quarter (warp % 4), 64 columns of each 128-row operand; scales
+//                 are loaded four blocks ahead, across tiles
 // Every hand-off is an mbarrier and every wait is bounded (MOE_ERR_TIMEOUT in the status word).
 #include <algorithm>
 
+#include "route_dev.cuh"
 #include "scaled.cuh"
 #include "tc_pipe.cuh"
 
@@ -32,19 +36,22 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kNT = 128;                       // most tokens of a tile
+constexpr int kMT = 128;                       // most tokens of a tile
+constexpr int kNW = 256;                       // weight rows of a tile (gate/up: 128 + 128)
 constexpr int kEpiWarp0 = 4, kEpiWarps = 8;
 constexpr int kThreads = (kEpiWarp0 + kEpiWarps) * 32;
 constexpr uint32_t kOperand = 128 * kSBlk;     // bytes of 128 rows of one block
-constexpr uint32_t kStage = 3 * kOperand;      // two weight operands and the tokens
+constexpr uint32_t kStage = 3 * kOperand;      // the weights' two operands and the tokens
 constexpr int kStages = 4;
-constexpr int kScales = 8;                     // depth of the scale ring
-constexpr int kAccs = 2;                       // accumulator buffers of 2 x 128 columns
+constexpr int kAccs = 2;                       // accumulator buffers of 256 columns
+constexpr int kAhead = 4;                      // blocks whose scales are loaded ahead
+constexpr int kPatch = 16;                     // columns per turn through shared memory (stores)
 constexpr uint32_t kTmemCols = 512;
 constexpr uint64_t kWaitNs = 2000000000ull;    // limit of every wait
 // Registers: 384 threads launch with 168 each (64512); the first warpgroup keeps 64 and the two
 // epilogue warpgroups take 216: 128 * 64 + 256 * 216 = 63488.
 constexpr int kLaunchRegs = 168, kRoleRegs = 64, kEpiRegs = 216;
+static_assert(sizeof(Job) == sizeof(int4), "a slice is loaded as one vector");
 static_assert(128 * kRoleRegs + 256 * kEpiRegs <= kThreads * kLaunchRegs, "register split");
 
 enum Mode { kGateUp, kDown, kDense };
@@ -54,8 +61,8 @@ struct TcArgs {
     int rows;                    // weight rows per expert (gate/up: of each of the two)
     int row_tiles;
     int M;                       // dense: rows of a
-    const Job *jobs;             // experts: written by k_scaled_jobs
-    const int32_t *njobs;
+    const Job *slices;           // experts: runs of up to 128 slots (k_scaled_slices)
+    const int32_t *nslices;
     const int32_t *perm;
     int T, k, routed;            // routed = T * k
     const float *as;
@@ -67,6 +74,7 @@ struct TcArgs {
     int64_t slots;
     void *out;
     int64_t ldo;
+    bool vec;                    // out rows are 32-byte aligned and rows a multiple of 16
     uint32_t *status;
 };
 
@@ -75,41 +83,41 @@ struct Tile {
     bool shared;
 };
 
-struct Walk {
-    int j = 0, base = 0;
-};
-
-// Tile i (increasing) of the order: job, 128-token slice, row tile.
+// Tile i: row tiles innermost, so that the CTAs that run at the same time share an expert's
+// weights (its slices follow one another) and a slice's tokens.
 template <int kMode>
-__device__ __forceinline__ bool tile_at(const TcArgs &a, int nj, Walk &c, int i, Tile &t) {
-    while (c.j < nj) {
-        const Job jb = kMode == kDense ? Job{0, 0, a.M, 0} : a.jobs[c.j];
-        const int cnt = (jb.n + kNT - 1) / kNT * a.row_tiles;
-        if (i < c.base + cnt) {
-            const int sl = (i - c.base) / a.row_tiles;
-            t.rt = (i - c.base) - sl * a.row_tiles;
-            t.e = jb.expert;
-            t.slot = jb.slot0 + sl * kNT;
-            t.n = min(kNT, jb.n - sl * kNT);
-            t.npad = (t.n + 15) & ~15;
-            t.shared = jb.shared != 0;
-            return true;
-        }
-        c.base += cnt;
-        c.j++;
+__device__ __forceinline__ Tile tile_at(const TcArgs &a, int i) {
+    Tile t;
+    const int s = i / a.row_tiles;
+    t.rt = i - s * a.row_tiles;
+    if (kMode == kDense) {
+        t.e = 0;
+        t.slot = s * kMT;
+        t.n = min(kMT, a.M - t.slot);
+        t.shared = false;
+    } else {
+        const int4 v = __ldg(reinterpret_cast<const int4 *>(a.slices) + s);
+        t.e = v.x;
+        t.slot = v.y;
+        t.n = v.z;
+        t.shared = v.w != 0;
     }
-    return false;
+    t.npad = (t.n + 15) & ~15;
+    return t;
 }
 
-// silu(g) * u in fp32 with CUDA's expf and an IEEE division.
+// silu(g) * u in fp32 with CUDA's expf and its approximate division (2 ulp; a denominator past
+// 2^126 gives 0, where the quotient is below 2^-119).
 __device__ __forceinline__ float silu_mul(float g, float u) {
-    return __fdiv_rn(g, 1.0f + expf(-g)) * u;
+    return __fdividef(g, 1.0f + expf(-g)) * u;
 }
 
-// The row of x that slot s of a tile reads.
-__device__ __forceinline__ int token_of(const TcArgs &a, const Tile &t, int s) {
-    if (t.shared) return s - a.routed;
-    const int p = a.perm[s];
+// The row of x that a slot reads is its entry of perm over k; the shared expert's slots follow
+// the routed ones in token order.  The entry is loaded ahead of its use.
+__device__ __forceinline__ int slot_entry(const TcArgs &a, const Tile &t, int s) {
+    return t.shared ? (s - a.routed) * a.k : __ldg(a.perm + s);
+}
+__device__ __forceinline__ int entry_token(const TcArgs &a, int p) {
     if (p < 0 || p >= a.routed) {
         set_status(a.status, MOE_ERR_BOUNDS);
         return 0;
@@ -118,12 +126,11 @@ __device__ __forceinline__ int token_of(const TcArgs &a, const Tile &t, int s) {
 }
 
 struct Shared {
-    uint64_t full[kStages], empty[kStages], acc_full[kAccs], acc_empty[kAccs], sc_full[kScales],
-        sc_empty[kScales], done;
+    uint64_t full[kStages], empty[kStages], acc_full[kAccs], acc_empty[kAccs], done;
     uint32_t tmem;
     int abort;
-    alignas(16) float scale[kScales][2][kNT];
-    alignas(16) uint32_t amax[2][kNT][4];        // gate/up: per column and lane quarter, by tile parity
+    uint32_t amax[2][2][kMT];             // gate/up: by tile parity and column half, per token
+    float patch[kEpiWarps][32][kPatch + 1];
 };
 
 constexpr size_t kSmem = 1024 + (size_t)kStages * kStage + sizeof(Shared);
@@ -162,20 +169,32 @@ __device__ __forceinline__ bool waitw(Shared &S, uint64_t *bar, uint32_t parity,
 }
 
 template <int kMode>
-__device__ void produce(const TcArgs &a, Shared &S, uint8_t *ring, int nj, const CUtensorMap *w0,
+__device__ void produce(const TcArgs &a, Shared &S, uint8_t *ring, int tiles, const CUtensorMap *w0,
                         const CUtensorMap *w1, const CUtensorMap *x) {
     const int lane = threadIdx.x & 31;
-    Walk c;
-    Tile t;
     Pos p;
     int issued = 0;
     bool ok = true;
-    for (int i = blockIdx.x; ok && tile_at<kMode>(a, nj, c, i, t); i += gridDim.x) {
-        int y[4];
+    int i = blockIdx.x;
+    if (i >= tiles) return;
+    Tile next = tile_at<kMode>(a, i);
+    int entry[4] = {0, 0, 0, 0};
+    auto entries = [&] {
         if (kMode == kGateUp) {
 #pragma unroll
-            for (int j = 0; j < 4; j++) y[j] = token_of(a, t, t.slot + min(4 * lane + j, t.n - 1));
+            for (int j = 0; j < 4; j++)
+                entry[j] = slot_entry(a, next, next.slot + min(4 * lane + j, next.n - 1));
         }
+    };
+    entries();
+    for (; ok && i < tiles; i += gridDim.x) {
+        const Tile t = next;
+        int y[4];
+#pragma unroll
+        for (int j = 0; j < 4; j++) y[j] = kMode == kGateUp ? entry_token(a, entry[j]) : 0;
+        // the next tile's place and token rows arrive while this one's blocks are issued
+        const bool more = i + gridDim.x < tiles;
+        if (more) next = tile_at<kMode>(a, i + gridDim.x);
         for (int b = 0; b < a.nkb; b++) {
             if (!waitw(S, &S.empty[p.s], p.ph ^ 1u, a.status)) {
                 ok = false;
@@ -185,7 +204,7 @@ __device__ void produce(const TcArgs &a, Shared &S, uint8_t *ring, int nj, const
             uint64_t *bar = &S.full[p.s];
             if (lane == 0) {
                 mbar_arrive_expect_tx(bar, 2 * kOperand + (uint32_t)t.npad * kSBlk);
-                const int r0 = kMode == kGateUp ? t.rt * 128 : t.rt * 256;
+                const int r0 = kMode == kGateUp ? t.rt * 128 : t.rt * kNW;
                 tma_load_3d(st, w0, b * kSBlk, r0, t.e, bar);
                 tma_load_3d(st + kOperand, w1, b * kSBlk, kMode == kGateUp ? r0 : r0 + 128, t.e,
                             bar);
@@ -200,22 +219,20 @@ __device__ void produce(const TcArgs &a, Shared &S, uint8_t *ring, int nj, const
             }
             issued++;
             p.next(kStages);
+            if (b == 0 && more) entries();
         }
     }
     // leaving early: the copies in flight land before the CTA goes
     if (!ok) {
-        for (int i = max(0, issued - kStages); i < issued; i++)
-            mbar_wait_bounded(&S.full[i % kStages], (uint32_t)(i / kStages) & 1u, kWaitNs);
+        for (int j = max(0, issued - kStages); j < issued; j++)
+            mbar_wait_bounded(&S.full[j % kStages], (uint32_t)(j / kStages) & 1u, kWaitNs);
     }
 }
 
-template <int kMode>
-__device__ void multiply(const TcArgs &a, Shared &S, uint8_t *ring, int nj, uint32_t tmem) {
-    Walk c;
-    Tile t;
+__device__ void multiply(const TcArgs &a, Shared &S, uint8_t *ring, int tiles, uint32_t tmem) {
     Pos p, q;
-    for (int i = blockIdx.x; tile_at<kMode>(a, nj, c, i, t); i += gridDim.x) {
-        const uint32_t idesc = instr_desc(0, 128, t.npad);
+    constexpr uint32_t idesc = instr_desc(0, kMT, kNW);
+    for (int i = blockIdx.x; i < tiles; i += gridDim.x) {
         for (int b = 0; b < a.nkb; b++) {
             if (!wait1(S, &S.acc_empty[q.s], q.ph ^ 1u, a.status) ||
                 !wait1(S, &S.full[p.s], p.ph, a.status)) {
@@ -225,70 +242,15 @@ __device__ void multiply(const TcArgs &a, Shared &S, uint8_t *ring, int nj, uint
             }
             tc_fence_after();
             const uint32_t st = smem_u32(ring + (size_t)p.s * kStage);
-            const uint32_t d = tmem + (uint32_t)q.s * 256u;
-            const uint64_t x = smem_desc(st + 2 * kOperand, 1024, 2);
-            const uint64_t w0 = smem_desc(st, 1024, 2), w1 = smem_desc(st + kOperand, 1024, 2);
+            const uint32_t d = tmem + (uint32_t)(q.s * kNW);
+            const uint64_t x = smem_desc(st + 2 * kOperand, 1024, 2), w = smem_desc(st, 1024, 2);
 #pragma unroll
-            for (int j = 0; j < 4; j++) {    // 32 bytes of k a step: 2 units of 16 bytes
-                umma_f8(d, w0 + 2 * j, x + 2 * j, idesc, j > 0);
-                umma_f8(d + 128, w1 + 2 * j, x + 2 * j, idesc, j > 0);
-            }
+            for (int j = 0; j < 4; j++)      // 32 bytes of k a step: 2 units of 16 bytes
+                umma_f8(d, x + 2 * j, w + 2 * j, idesc, j > 0);
             umma_commit(&S.empty[p.s]);
             umma_commit(&S.acc_full[q.s]);
             p.next(kStages);
             q.next(kAccs);
-        }
-    }
-}
-
-template <int kMode>
-__device__ void scales(const TcArgs &a, Shared &S, int nj, int half) {
-    constexpr int kAhead = 4;           // blocks whose loads are issued together
-    const int lane = threadIdx.x & 31;
-    const int rb = (a.rows + kSBlk - 1) / kSBlk;
-    Walk c;
-    Tile t;
-    Pos p;
-    for (int i = blockIdx.x; tile_at<kMode>(a, nj, c, i, t); i += gridDim.x) {
-        const float *as[2];
-#pragma unroll
-        for (int j = 0; j < 2; j++) {
-            const int col = half * 64 + j * 32 + lane;
-            as[j] = col >= t.n ? nullptr
-                    : a.as + (kMode == kGateUp ? token_of(a, t, t.slot + col) : t.slot + col);
-        }
-        const float *s0 = a.ws0 + t.e * a.ws_expert, *s1;
-        if (kMode == kGateUp) {
-            s0 += (int64_t)t.rt * a.nkb;
-            s1 = a.ws1 + t.e * a.ws_expert + (int64_t)t.rt * a.nkb;
-        } else {
-            s0 += (int64_t)(2 * t.rt) * a.nkb;
-            s1 = 2 * t.rt + 1 < rb ? s0 + a.nkb : s0;      // past the last rows: not stored
-        }
-        for (int b0 = 0; b0 < a.nkb; b0 += kAhead) {
-            float v[kAhead][2], w[kAhead][2];
-#pragma unroll
-            for (int u = 0; u < kAhead; u++) {
-                const int b = b0 + u;
-                const bool in = b < a.nkb;
-                v[u][0] = in && as[0] ? __ldg(as[0] + b * a.ldas) : 0.f;
-                v[u][1] = in && as[1] ? __ldg(as[1] + b * a.ldas) : 0.f;
-                w[u][0] = in ? __ldg(s0 + b) : 0.f;
-                w[u][1] = in ? __ldg(s1 + b) : 0.f;
-            }
-#pragma unroll
-            for (int u = 0; u < kAhead; u++) {
-                if (b0 + u >= a.nkb) break;
-                if (!waitw(S, &S.sc_empty[p.s], p.ph ^ 1u, a.status)) return;
-                const int col = half * 64 + lane;
-                S.scale[p.s][0][col] = v[u][0] * w[u][0];
-                S.scale[p.s][0][col + 32] = v[u][1] * w[u][0];
-                S.scale[p.s][1][col] = v[u][0] * w[u][1];
-                S.scale[p.s][1][col + 32] = v[u][1] * w[u][1];
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&S.sc_full[p.s]);
-                p.next(kScales);
-            }
         }
     }
 }
@@ -300,39 +262,146 @@ __device__ __forceinline__ float2 pair(uint64_t v) {
 __device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi) {
     return (uint64_t)lo | ((uint64_t)hi << 32);
 }
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+    return pair(__float_as_uint(lo), __float_as_uint(hi));
+}
 // acc += r * s for 16 columns, two at a time.
-__device__ __forceinline__ void promote16(uint64_t *acc, const uint32_t (&r)[16], const float *s) {
+__device__ __forceinline__ void promote16(uint64_t *acc, const uint32_t (&r)[16], uint64_t s) {
 #pragma unroll
-    for (int i = 0; i < 16; i += 4) {
-        const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(s + i);
+    for (int i = 0; i < 16; i += 2)
         asm("fma.rn.f32x2 %0, %1, %2, %0;"
-            : "+l"(acc[i / 2]) : "l"(pair(r[i], r[i + 1])), "l"(v.x));
-        asm("fma.rn.f32x2 %0, %1, %2, %0;"
-            : "+l"(acc[i / 2 + 1]) : "l"(pair(r[i + 2], r[i + 3])), "l"(v.y));
+            : "+l"(acc[i / 2]) : "l"(pair(r[i], r[i + 1])), "l"(s));
+}
+
+// The stream of (tile, block) scales of one epilogue thread, running ahead of the epilogue: the
+// token's scale times the two operands' weight scales.
+struct Scale {
+    float v, w0, w1;
+};
+template <int kMode>
+struct ScaleStream {
+    int i, b, entry;
+    Tile t, next;
+    const float *as, *s0, *s1;
+
+    __device__ __forceinline__ void look(const TcArgs &a, int row) {
+        if (kMode == kGateUp) entry = slot_entry(a, next, next.slot + min(row, next.n - 1));
+    }
+    __device__ __forceinline__ void open(const TcArgs &a, int row) {
+        t = next;
+        as = row >= t.n ? nullptr
+                        : a.as + (kMode == kGateUp ? entry_token(a, entry) : t.slot + row);
+        s0 = a.ws0 + t.e * a.ws_expert;
+        if (kMode == kGateUp) {
+            s0 += (int64_t)t.rt * a.nkb;
+            s1 = a.ws1 + t.e * a.ws_expert + (int64_t)t.rt * a.nkb;
+        } else {
+            s0 += (int64_t)(2 * t.rt) * a.nkb;
+            s1 = t.rt * kNW + kSBlk < a.rows ? s0 + a.nkb : s0;    // past the last rows: not stored
+        }
+    }
+    __device__ __forceinline__ void start(const TcArgs &a, int row) {
+        i = blockIdx.x;
+        b = 0;
+        next = tile_at<kMode>(a, i);
+        look(a, row);
+        open(a, row);
+    }
+    __device__ __forceinline__ Scale load(const TcArgs &a, int tiles, int row) {
+        Scale c{0.f, 0.f, 0.f};
+        if (i >= tiles) return c;
+        if (as) {
+            c.v = __ldg(as);
+            as += a.ldas;
+        }
+        c.w0 = __ldg(s0 + b);
+        c.w1 = __ldg(s1 + b);
+        const bool more = i + (int)gridDim.x < tiles;
+        if (b == 0 && more) {
+            next = tile_at<kMode>(a, i + gridDim.x);
+            look(a, row);
+        }
+        if (++b == a.nkb) {
+            b = 0;
+            i += gridDim.x;
+            if (more) open(a, row);
+        }
+        return c;
+    }
+};
+
+__device__ __forceinline__ void store32B(void *p, const uint32_t (&v)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]),
+                 "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi, float *) { return 0u; }
+__device__ __forceinline__ uint32_t pack2(float lo, float hi, __nv_bfloat16 *) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi, __half *) {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+// 16 columns (8 pairs) of this lane's row at p, 32-byte aligned.
+template <typename T>
+__device__ __forceinline__ void store16(T *p, const uint64_t *acc) {
+    uint32_t v[8];
+    if (sizeof(T) == 4) {
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                v[2 * i] = (uint32_t)acc[4 * h + i];
+                v[2 * i + 1] = (uint32_t)(acc[4 * h + i] >> 32);
+            }
+            store32B(p + 8 * h, v);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            const float2 f = pair(acc[i]);
+            v[i] = pack2(f.x, f.y, (T *)nullptr);
+        }
+        store32B(p, v);
     }
 }
 
 template <int kMode, typename T>
-__device__ void finish(const TcArgs &a, Shared &S, int nj, uint32_t tmem) {
+__device__ void finish(const TcArgs &a, Shared &S, int tiles, uint32_t tmem) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int quad = warp & 3, half = (warp - kEpiWarp0) >> 2;
-    const int c0 = half * 64;
-    const uint32_t base = tmem + ((uint32_t)quad << 21) + (uint32_t)c0;   // lane quad * 32
-    Walk c;
-    Tile t;
-    Pos q, p;
+    const int row = quad * 32 + lane;
+    const uint32_t base = tmem + ((uint32_t)quad << 21) + (uint32_t)(half * 64);  // lane quad * 32
+    Pos q;
     uint32_t par = 0;
-    for (int i = blockIdx.x; tile_at<kMode>(a, nj, c, i, t); i += gridDim.x) {
+    int i = blockIdx.x;
+    if (i >= tiles) return;
+    ScaleStream<kMode> ss;
+    ss.start(a, row);
+    Tile next = ss.t;
+    Scale c[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; u++) c[u] = ss.load(a, tiles, row);
+    for (; i < tiles; i += gridDim.x) {
+        const Tile t = next;
+        if (i + (int)gridDim.x < tiles) next = tile_at<kMode>(a, i + gridDim.x);
         uint64_t acc[2][32];            // two columns each
 #pragma unroll
         for (int j = 0; j < 32; j++) acc[0][j] = acc[1][j] = 0u;
-        const bool busy = c0 < t.npad;
+        const bool busy = quad * 32 < t.n;
         for (int b = 0; b < a.nkb; b++) {
-            if (!waitw(S, &S.sc_full[p.s], p.ph, a.status)) return;
+            const float f0 = c[0].v * c[0].w0, f1 = c[0].v * c[0].w1;
+            const uint64_t s0 = pair(f0, f0), s1 = pair(f1, f1);
+#pragma unroll
+            for (int u = 0; u + 1 < kAhead; u++) c[u] = c[u + 1];
+            c[kAhead - 1] = ss.load(a, tiles, row);
             if (!waitw(S, &S.acc_full[q.s], q.ph, a.status)) return;
             if (busy) {
                 tc_fence_after();
-                const uint32_t d = base + (uint32_t)q.s * 256u;
+                const uint32_t d = base + (uint32_t)(q.s * kNW);
 #pragma unroll
                 for (int j = 0; j < 4; j++) {
                     uint32_t r0[16], r1[16];
@@ -340,82 +409,91 @@ __device__ void finish(const TcArgs &a, Shared &S, int nj, uint32_t tmem) {
                     tmem_ld16(d + 128 + 16 * j, r1);
                     tmem_ld_wait(r0);
                     reg_tie(r1);
-                    promote16(acc[0] + 8 * j, r0, S.scale[p.s][0] + c0 + 16 * j);
-                    promote16(acc[1] + 8 * j, r1, S.scale[p.s][1] + c0 + 16 * j);
+                    promote16(acc[0] + 8 * j, r0, s0);
+                    promote16(acc[1] + 8 * j, r1, s1);
                 }
                 tc_fence_before();
             }
             __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&S.acc_empty[q.s]);
-                mbar_arrive(&S.sc_empty[p.s]);
-            }
+            if (lane == 0) mbar_arrive(&S.acc_empty[q.s]);
             q.next(kAccs);
-            p.next(kScales);
         }
+        if (!busy) continue;
         if (kMode == kGateUp) {
-            // h, and its e4m3 form per token and 128 ffn values: the 128 lanes of the operand
-            const int f = t.rt * 128 + quad * 32 + lane;
-            uint32_t keep[2] = {0u, 0u};
+            // h, and its e4m3 form per token and 128 ffn values: this thread's 64 and the other
+            // column half's
+            uint32_t m = 0u;
 #pragma unroll
             for (int j = 0; j < 32; j++) {
                 const float2 g = pair(acc[0][j]), u = pair(acc[1][j]);
                 const float h0 = silu_mul(g.x, u.x), h1 = silu_mul(g.y, u.y);
-                acc[0][j] = pair(__float_as_uint(h0), __float_as_uint(h1));
-                const uint32_t m0 =
-                    __reduce_max_sync(0xffffffffu, __float_as_uint(h0) & 0x7fffffffu);
-                const uint32_t m1 =
-                    __reduce_max_sync(0xffffffffu, __float_as_uint(h1) & 0x7fffffffu);
-                if (lane == ((2 * j) & 31)) keep[j >> 4] = m0;
-                if (lane == ((2 * j + 1) & 31)) keep[j >> 4] = m1;
+                acc[0][j] = pair(h0, h1);
+                m = max(m, max(__float_as_uint(h0) & 0x7fffffffu, __float_as_uint(h1) & 0x7fffffffu));
             }
-            S.amax[par][c0 + lane][quad] = keep[0];
-            S.amax[par][c0 + 32 + lane][quad] = keep[1];
-            named_barrier(1 + half, 128);
-            uint8_t *hq = a.hq + ((int64_t)t.slot + c0) * a.rows + f;
-            float *hs = a.hs + t.rt * a.slots + t.slot + c0;
-#pragma unroll
-            for (int j = 0; j < 64; j += 2) {
-                if (c0 + j < t.n) {
-                    float sc[2], inv[2];
-#pragma unroll
-                    for (int u = 0; u < 2; u++) {
-                        const uint4 m = *reinterpret_cast<const uint4 *>(S.amax[par][c0 + j + u]);
-                        const uint32_t mx = max(max(m.x, m.y), max(m.z, m.w));
-                        const bool fin = mx < 0x7f800000u;
-                        sc[u] = fin ? __fdiv_rn(__uint_as_float(mx), kE4M3Max) : 0.f;
-                        inv[u] = sc[u] > 0.f ? __frcp_rn(sc[u]) : 0.f;
-                        if (!fin && c0 + j + u < t.n && quad == 0 && lane == 0)
-                            set_status(a.status, MOE_ERR_NONFINITE);
-                    }
-                    const float2 h = pair(acc[0][j / 2]);
-                    const uint32_t v = cvt_e4m3x2(sc[0] > 0.f ? h.x * inv[0] : 0.f,
-                                                  sc[1] > 0.f ? h.y * inv[1] : 0.f);
-                    const bool two = c0 + j + 1 < t.n;
-                    if (f < a.rows) {
-                        hq[0] = (uint8_t)v;
-                        if (two) hq[a.rows] = (uint8_t)(v >> 8);
-                    }
-                    if (quad == 0 && lane == 0) {
-                        hs[j] = sc[0];
-                        if (two) hs[j + 1] = sc[1];
-                    }
-                }
-                hq += 2 * (int64_t)a.rows;
-            }
+            S.amax[par][half][row] = m;
+            named_barrier(1 + quad, 64);
+            m = max(m, S.amax[par][half ^ 1][row]);
             par ^= 1u;
+            if (row < t.n) {
+                const bool fin = m < 0x7f800000u;
+                const float sc = fin ? __fdiv_rn(__uint_as_float(m), kE4M3Max) : 0.f;
+                // h / sc as (h * pre) * (1 / (sc * pre)): pre keeps the reciprocal of a tiny scale finite
+                const float pre = sc < 0x1p-100f ? 0x1p100f : 1.0f;
+                const float inv = sc > 0.f ? __frcp_rn(sc * pre) : 0.f;
+                const int64_t slot = (int64_t)t.slot + row;
+                if (half == 0) {
+                    a.hs[t.rt * a.slots + slot] = sc;
+                    if (!fin) set_status(a.status, MOE_ERR_NONFINITE);
+                }
+                const int f = t.rt * 128 + half * 64;
+                uint8_t *hq = a.hq + slot * a.rows + f;
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    uint32_t v[4];
+#pragma unroll
+                    for (int u = 0; u < 4; u++) {
+                        const float2 x = pair(acc[0][8 * j + 2 * u]);
+                        const float2 y = pair(acc[0][8 * j + 2 * u + 1]);
+                        v[u] = cvt_e4m3x2(x.x * pre * inv, x.y * pre * inv) |
+                               (cvt_e4m3x2(y.x * pre * inv, y.y * pre * inv) << 16);
+                        if (!fin) v[u] = 0u;
+                    }
+                    if (f + 16 * j < a.rows)
+                        *reinterpret_cast<uint4 *>(hq + 16 * j) = make_uint4(v[0], v[1], v[2], v[3]);
+                }
+            }
         } else {
+            T *out = static_cast<T *>(a.out) + ((int64_t)t.slot + row) * a.ldo;
 #pragma unroll
             for (int u = 0; u < 2; u++) {
-                const int r = t.rt * 256 + u * 128 + quad * 32 + lane;
-                T *out = static_cast<T *>(a.out) + ((int64_t)t.slot + c0) * a.ldo + r;
-                if (r < a.rows) {
+                const int r0 = t.rt * kNW + u * 128 + half * 64;
+                if (a.vec) {
+                    // 32 bytes of a row per lane and store
 #pragma unroll
-                    for (int j = 0; j < 32; j++) {
-                        const float2 v = pair(acc[u][j]);
-                        if (c0 + 2 * j < t.n) out[0] = from_f32<T>(v.x);
-                        if (c0 + 2 * j + 1 < t.n) out[a.ldo] = from_f32<T>(v.y);
-                        out += 2 * a.ldo;
+                    for (int j = 0; j < 4; j++)
+                        if (row < t.n && r0 + 16 * j < a.rows)
+                            store16(out + r0 + 16 * j, acc[u] + 8 * j);
+                } else {
+                    // rows of any alignment: 16 columns at a time through shared memory, so that
+                    // a warp writes runs of a row
+                    float (&P)[32][kPatch + 1] = S.patch[warp - kEpiWarp0];
+#pragma unroll
+                    for (int j = 0; j < 4; j++) {
+#pragma unroll
+                        for (int x = 0; x < 8; x++) {
+                            const float2 v = pair(acc[u][8 * j + x]);
+                            P[lane][2 * x] = v.x;
+                            P[lane][2 * x + 1] = v.y;
+                        }
+                        __syncwarp();
+                        const int col = r0 + 16 * j + (lane & 15);
+                        const int first = quad * 32 + (lane >> 4);
+                        T *o = static_cast<T *>(a.out) + ((int64_t)t.slot + first) * a.ldo + col;
+                        if (col < a.rows) {
+                            for (int y = 0; y < 16 && first + 2 * y < t.n; y++, o += 2 * a.ldo)
+                                *o = from_f32<T>(P[(lane >> 4) + 2 * y][lane & 15]);
+                        }
+                        __syncwarp();
                     }
                 }
             }
@@ -441,10 +519,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&S.acc_full[i], 1);
             mbar_init(&S.acc_empty[i], kEpiWarps);
         }
-        for (int i = 0; i < kScales; i++) {
-            mbar_init(&S.sc_full[i], 2);
-            mbar_init(&S.sc_empty[i], kEpiWarps);
-        }
         mbar_init(&S.done, 1);
         S.abort = 0;
         fence_barrier_init();
@@ -457,18 +531,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = S.tmem;
-    const int nj = kMode == kDense ? 1 : *a.njobs;
+    const int tiles = (kMode == kDense ? (a.M + kMT - 1) / kMT : *a.nslices) * a.row_tiles;
     if (warp < kEpiWarp0) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRoleRegs));
         if (warp == 0)
-            produce<kMode>(a, S, ring, nj, &w0, &w1, &x);
-        else if (warp == 1) {
-            if ((threadIdx.x & 31) == 0) multiply<kMode>(a, S, ring, nj, tmem);
-        } else
-            scales<kMode>(a, S, nj, warp - 2);
+            produce<kMode>(a, S, ring, tiles, &w0, &w1, &x);
+        if (warp == 1) {
+            if ((threadIdx.x & 31) == 0) multiply(a, S, ring, tiles, tmem);
+        }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
-        finish<kMode, T>(a, S, nj, tmem);
+        finish<kMode, T>(a, S, tiles, tmem);
     }
     __syncwarp();
     tc_fence_before();
@@ -479,41 +552,34 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-// The experts' job list: one job per expert with tokens, the shared one last.  One CTA.
+// The runs of up to 128 slots of every expert with tokens, ascending, the shared one's last: the
+// tiles' token side.  One CTA.
 __global__ void __launch_bounds__(1024)
-    k_scaled_jobs(const int32_t *__restrict__ offsets, int E, int T, int k, int shared, Job *jobs,
-                  int32_t *njobs, uint32_t *status) {
-    __shared__ int s_warp[32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, A = T * k;
-    int base = 0;
-    for (int e0 = 0; e0 < E; e0 += 1024) {
-        const int e = e0 + threadIdx.x;
-        int n = 0, o = 0;
-        if (e < E) {
-            o = offsets[e];
-            const int o1 = offsets[e + 1];
-            n = o1 - o;
-            if (o < 0 || o1 > A || n < 0) {      // not what a router wrote
-                set_status(status, MOE_ERR_BOUNDS);
-                n = 0;
-            }
-        }
-        const unsigned m = __ballot_sync(0xffffffffu, n > 0);
-        if (lane == 0) s_warp[warp] = __popc(m);
-        __syncthreads();
-        int at = base, all = 0;
-        for (int w = 0; w < 32; w++) {
-            at += w < warp ? s_warp[w] : 0;
-            all += s_warp[w];
-        }
-        if (n > 0) jobs[at + __popc(m & ((1u << lane) - 1u))] = Job{e, o, n, 0};
-        base += all;
-        __syncthreads();
+    k_scaled_slices(const int32_t *__restrict__ offsets, int E, int T, int k, int shared,
+                    Job *slices, int32_t *nslices, uint32_t *status) {
+    __shared__ int s_first[kMaxE];
+    __shared__ int s_warp[33];
+    const int A = T * k;
+    for (int e = threadIdx.x; e < E; e += 1024) {
+        const int o = offsets[e], o1 = offsets[e + 1];
+        const bool fits = o >= 0 && o <= o1 && o1 <= A;      // else not what a router wrote
+        if (!fits) set_status(status, MOE_ERR_BOUNDS);
+        s_first[e] = fits ? (o1 - o + kMT - 1) / kMT : 0;
     }
-    if (threadIdx.x == 0) {
-        if (shared) jobs[base] = Job{E, A, T, 1};
-        *njobs = base + (shared ? 1 : 0);
+    __syncthreads();
+    // overlapping runs of damaged offsets could pass the list's end: those are left out too
+    const int most = A / kMT + min(E, A);
+    const int n = min(block_exclusive_scan<1024>(s_first, E, s_warp), most);
+    for (int e = threadIdx.x; e < E; e += 1024) {
+        const int o = offsets[e], o1 = offsets[e + 1];
+        if (!(o >= 0 && o <= o1 && o1 <= A)) continue;
+        for (int s = o, j = s_first[e]; s < o1 && j < most; s += kMT, j++)
+            slices[j] = Job{e, s, min(kMT, o1 - s), 0};
     }
+    const int ns = shared ? (T + kMT - 1) / kMT : 0;
+    for (int j = threadIdx.x; j < ns; j += 1024)
+        slices[n + j] = Job{E, A + j * kMT, min(kMT, T - j * kMT), 1};
+    if (threadIdx.x == 0) *nslices = n + ns;
 }
 
 // out[t] = sum_j w[t][j] y[slot of (t, j)] (+ gate[t] y[routed + t]): one CTA per token.
@@ -595,8 +661,8 @@ cudaError_t run_tc(const TcArgs &a, const CUtensorMap &w0, const CUtensorMap &w1
 size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 
 struct ExpertsWs {
-    size_t xq, xs, hq, hs, y, jobs, njobs, total;
-    int64_t slots;
+    size_t xq, xs, hq, hs, y, slices, nslices, total;
+    int64_t slots, most_slices;
 };
 
 ExpertsWs experts_ws(const moe_scaled_weights &w, int T, int k) {
@@ -613,8 +679,10 @@ ExpertsWs experts_ws(const moe_scaled_weights &w, int T, int k) {
     L.hq = take((size_t)L.slots * w.ffn);
     L.hs = take((size_t)sblocks(w.ffn) * L.slots * 4);
     L.y = take((size_t)L.slots * w.hidden * 4);
-    L.jobs = take(sizeof(Job) * ((size_t)std::min<int64_t>(w.n_experts, (int64_t)T * k) + 1));
-    L.njobs = take(4);
+    L.most_slices = (int64_t)T * k / kMT + std::min<int64_t>(w.n_experts, (int64_t)T * k) +
+                    (w.shared ? (T + kMT - 1) / kMT : 0);
+    L.slices = take(sizeof(Job) * (size_t)L.most_slices);
+    L.nslices = take(4);
     L.total = p;
     return L;
 }
@@ -623,26 +691,24 @@ cudaError_t experts_tc(const ScaledExpertsArgs &e, uint8_t *ws, cudaStream_t st)
     const moe_scaled_weights &w = e.w;
     const ExpertsWs L = experts_ws(w, e.T, e.k);
     const int n = w.n_experts + w.shared, H = w.hidden, F = w.ffn;
-    Job *jobs = reinterpret_cast<Job *>(ws + L.jobs);
-    int32_t *njobs = reinterpret_cast<int32_t *>(ws + L.njobs);
+    Job *slices = reinterpret_cast<Job *>(ws + L.slices);
+    int32_t *nslices = reinterpret_cast<int32_t *>(ws + L.nslices);
     float *xs = reinterpret_cast<float *>(ws + L.xs);
     CUtensorMap gate, up, down, x, h;
     if (!encode(&gate, w.d_gate, H, F, H, n, 128) || !encode(&up, w.d_up, H, F, H, n, 128) ||
         !encode(&down, w.d_down, F, H, F, n, 128) || !encode(&x, ws + L.xq, H, e.T, H, 0, 1) ||
         !encode(&h, ws + L.hq, F, L.slots, F, 0, 16))
         return cudaErrorInvalidValue;
-    k_scaled_jobs<<<1, 1024, 0, st>>>(e.offsets, w.n_experts, e.T, e.k, w.shared, jobs, njobs,
-                                      e.status);
+    k_scaled_slices<<<1, 1024, 0, st>>>(e.offsets, w.n_experts, e.T, e.k, w.shared, slices,
+                                        nslices, e.status);
     note_launches(1);
     cudaError_t err = cudaGetLastError();
     if (err != cudaSuccess) return err;
     err = launch_scaled_quantize(e.x, e.x_dt, e.T, H, H, ws + L.xq, H, xs, e.T, e.status, st);
     if (err != cudaSuccess) return err;
-    // an upper bound on the 128-token slices of all jobs
-    const int64_t slices = L.slots / kNT + std::min<int64_t>(w.n_experts, (int64_t)e.T * e.k) + 1;
     TcArgs a{};
-    a.jobs = jobs;
-    a.njobs = njobs;
+    a.slices = slices;
+    a.nslices = nslices;
     a.perm = e.perm;
     a.T = e.T;
     a.k = e.k;
@@ -659,17 +725,18 @@ cudaError_t experts_tc(const ScaledExpertsArgs &e, uint8_t *ws, cudaStream_t st)
     a.ws0 = w.d_gate_s;
     a.ws1 = w.d_up_s;
     a.ws_expert = (int64_t)sblocks(F) * sblocks(H);
-    err = run_tc<kGateUp, float>(a, gate, up, x, slices * a.row_tiles, st);
+    err = run_tc<kGateUp, float>(a, gate, up, x, L.most_slices * a.row_tiles, st);
     if (err != cudaSuccess) return err;
     a.nkb = sblocks(F);
     a.rows = H;
-    a.row_tiles = (H + 255) / 256;
+    a.row_tiles = (H + kNW - 1) / kNW;
     a.as = a.hs;
     a.ldas = L.slots;
     a.ws0 = w.d_down_s;
     a.out = ws + L.y;
     a.ldo = H;
-    err = run_tc<kDown, float>(a, down, down, h, slices * a.row_tiles, st);
+    a.vec = true;
+    err = run_tc<kDown, float>(a, down, down, h, L.most_slices * a.row_tiles, st);
     if (err != cudaSuccess) return err;
     return with_dtype(e.out_dt, [&](auto *tag) {
         using E = std::remove_pointer_t<decltype(tag)>;
@@ -689,15 +756,16 @@ cudaError_t matmul_tc(const ScaledMatmulArgs &m, cudaStream_t st) {
     TcArgs a{};
     a.nkb = sblocks(m.K);
     a.rows = m.N;
-    a.row_tiles = (m.N + 255) / 256;
+    a.row_tiles = (m.N + kNW - 1) / kNW;
     a.M = m.M;
     a.as = m.as;
     a.ldas = m.ldas;
     a.ws0 = m.bs;
     a.out = m.out;
     a.ldo = m.ldo;
+    a.vec = (uintptr_t)m.out % 32 == 0 && m.ldo * dtype_bytes(m.dt) % 32 == 0 && m.N % 16 == 0;
     a.status = m.status;
-    const int64_t tiles = (int64_t)((m.M + kNT - 1) / kNT) * a.row_tiles;
+    const int64_t tiles = (int64_t)((m.M + kMT - 1) / kMT) * a.row_tiles;
     if (tiles > INT32_MAX) return cudaErrorInvalidValue;
     return with_dtype(m.dt, [&](auto *tag) {
         using E = std::remove_pointer_t<decltype(tag)>;
