@@ -10,8 +10,7 @@
 //
 // Tile: 128 tokens (the MMA's M side) by 256 weight rows (N): rows of one matrix, or 128 gate rows
 // and the 128 up rows of the same ffn values.  Tokens sit on the M side so that a tensor-memory
-// lane is a token: an epilogue thread's scale is then one number per block and operand, held in
-// a register.  With the weights on the M side the scale changes from column to column and has to
+// lane is a token: an epilogue thread's scale is then one number per block and operand.  With the weights on the M side the scale changes from column to column and has to
 // be read from shared memory, two 16-byte loads per four elements; the loads, not the
 // additions, then bound the kernel (1380 clocks per block of 128 k against 512 of MMA).  An
 // expert with few tokens leaves rows of the MMA unused, which costs nothing that counts: it is
@@ -21,8 +20,9 @@
 //   warp 0        TMA producer: weight boxes of 128 rows x 128 bytes, token rows as boxes of 16
 //                 or, for routed tokens, gathered four at a time
 //   warp 1        tensor-memory allocation and the MMA issuer
-//   warps 4-11    epilogue: lane quarter (warp % 4), 64 columns of each 128-row operand; scales
-//                 are loaded four blocks ahead, across tiles
+//   warps 2-3     scales: as * bs of every token, block and operand, into a ring, loaded four
+//                 blocks ahead
+//   warps 4-11    epilogue: lane quarter (warp % 4), 64 columns of each 128-row operand
 // Every hand-off is an mbarrier and every wait is bounded (MOE_ERR_TIMEOUT in the status word).
 #include <algorithm>
 
@@ -44,13 +44,14 @@ constexpr uint32_t kOperand = 128 * kSBlk;     // bytes of 128 rows of one block
 constexpr uint32_t kStage = 3 * kOperand;      // the weights' two operands and the tokens
 constexpr int kStages = 4;
 constexpr int kAccs = 2;                       // accumulator buffers of 256 columns
+constexpr int kScales = 8;                     // depth of the scale ring
 constexpr int kAhead = 4;                      // blocks whose scales are loaded ahead
 constexpr int kPatch = 16;                     // columns per turn through shared memory (stores)
 constexpr uint32_t kTmemCols = 512;
 constexpr uint64_t kWaitNs = 2000000000ull;    // limit of every wait
-// Registers: 384 threads launch with 168 each (64512); the first warpgroup keeps 64 and the two
-// epilogue warpgroups take 216: 128 * 64 + 256 * 216 = 63488.
-constexpr int kLaunchRegs = 168, kRoleRegs = 64, kEpiRegs = 216;
+// Registers: 384 threads launch with 168 each (64512); the first warpgroup keeps 96 and the two
+// epilogue warpgroups take 200: 128 * 96 + 256 * 200 = 63488.
+constexpr int kLaunchRegs = 168, kRoleRegs = 96, kEpiRegs = 200;
 static_assert(sizeof(Job) == sizeof(int4), "a slice is loaded as one vector");
 static_assert(128 * kRoleRegs + 256 * kEpiRegs <= kThreads * kLaunchRegs, "register split");
 
@@ -126,9 +127,11 @@ __device__ __forceinline__ int entry_token(const TcArgs &a, int p) {
 }
 
 struct Shared {
-    uint64_t full[kStages], empty[kStages], acc_full[kAccs], acc_empty[kAccs], done;
+    uint64_t full[kStages], empty[kStages], acc_full[kAccs], acc_empty[kAccs], sc_full[kScales],
+        sc_empty[kScales], done;
     uint32_t tmem;
     int abort;
+    float2 scale[kScales][kMT];
     uint32_t amax[2][2][kMT];             // gate/up: by tile parity and column half, per token
     float patch[kEpiWarps][32][kPatch + 1];
 };
@@ -255,42 +258,33 @@ __device__ void multiply(const TcArgs &a, Shared &S, uint8_t *ring, int tiles, u
     }
 }
 
-// Running totals of two columns in one 64-bit register pair.
-__device__ __forceinline__ float2 pair(uint64_t v) {
-    return make_float2(__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32)));
-}
-__device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi) {
-    return (uint64_t)lo | ((uint64_t)hi << 32);
-}
-__device__ __forceinline__ uint64_t pair(float lo, float hi) {
-    return pair(__float_as_uint(lo), __float_as_uint(hi));
-}
-// acc += r * s for 16 columns, two at a time.
-__device__ __forceinline__ void promote16(uint64_t *acc, const uint32_t (&r)[16], uint64_t s) {
-#pragma unroll
-    for (int i = 0; i < 16; i += 2)
-        asm("fma.rn.f32x2 %0, %1, %2, %0;"
-            : "+l"(acc[i / 2]) : "l"(pair(r[i], r[i + 1])), "l"(s));
-}
-
-// The stream of (tile, block) scales of one epilogue thread, running ahead of the epilogue: the
-// token's scale times the two operands' weight scales.
-struct Scale {
-    float v, w0, w1;
-};
+// Warps 2 and 3: the scales of every tile and block, in the order the epilogue takes them: the
+// token's scale times the two operands' weight scales, one pair per token.  Loads run kAhead
+// blocks ahead of the ring's writes, across tiles.
 template <int kMode>
 struct ScaleStream {
-    int i, b, entry;
+    struct Set {
+        float v[2], w0, w1;
+    };
+    int i, b, entry[2];
     Tile t, next;
-    const float *as, *s0, *s1;
+    const float *as[2], *s0, *s1;
 
     __device__ __forceinline__ void look(const TcArgs &a, int row) {
-        if (kMode == kGateUp) entry = slot_entry(a, next, next.slot + min(row, next.n - 1));
+        if (kMode == kGateUp) {
+#pragma unroll
+            for (int j = 0; j < 2; j++)
+                entry[j] = slot_entry(a, next, next.slot + min(row + 32 * j, next.n - 1));
+        }
     }
     __device__ __forceinline__ void open(const TcArgs &a, int row) {
         t = next;
-        as = row >= t.n ? nullptr
-                        : a.as + (kMode == kGateUp ? entry_token(a, entry) : t.slot + row);
+#pragma unroll
+        for (int j = 0; j < 2; j++) {
+            const int r = row + 32 * j;
+            as[j] = r >= t.n ? nullptr
+                    : a.as + (kMode == kGateUp ? entry_token(a, entry[j]) : t.slot + r);
+        }
         s0 = a.ws0 + t.e * a.ws_expert;
         if (kMode == kGateUp) {
             s0 += (int64_t)t.rt * a.nkb;
@@ -307,12 +301,15 @@ struct ScaleStream {
         look(a, row);
         open(a, row);
     }
-    __device__ __forceinline__ Scale load(const TcArgs &a, int tiles, int row) {
-        Scale c{0.f, 0.f, 0.f};
-        if (i >= tiles) return c;
-        if (as) {
-            c.v = __ldg(as);
-            as += a.ldas;
+    __device__ __forceinline__ void load(const TcArgs &a, int tiles, int row, Set &c) {
+        if (i >= tiles) return;
+#pragma unroll
+        for (int j = 0; j < 2; j++) {
+            c.v[j] = 0.f;
+            if (as[j]) {
+                c.v[j] = __ldg(as[j]);
+                as[j] += a.ldas;
+            }
         }
         c.w0 = __ldg(s0 + b);
         c.w1 = __ldg(s1 + b);
@@ -326,9 +323,53 @@ struct ScaleStream {
             i += gridDim.x;
             if (more) open(a, row);
         }
-        return c;
     }
 };
+
+template <int kMode>
+__device__ void scales(const TcArgs &a, Shared &S, int tiles, int which) {
+    const int lane = threadIdx.x & 31, row = which * 64 + lane;
+    if ((int)blockIdx.x >= tiles) return;
+    ScaleStream<kMode> ss;
+    typename ScaleStream<kMode>::Set c[kAhead];
+    ss.start(a, row);
+#pragma unroll
+    for (int u = 0; u < kAhead; u++) ss.load(a, tiles, row, c[u]);
+    const int mine = (tiles - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
+    const int64_t total = (int64_t)mine * a.nkb;
+    Pos p;
+    for (int64_t b0 = 0; b0 < total; b0 += kAhead) {
+#pragma unroll
+        for (int u = 0; u < kAhead; u++) {
+            if (b0 + u >= total) break;
+            if (!waitw(S, &S.sc_empty[p.s], p.ph ^ 1u, a.status)) return;
+            S.scale[p.s][row] = make_float2(c[u].v[0] * c[u].w0, c[u].v[0] * c[u].w1);
+            S.scale[p.s][row + 32] = make_float2(c[u].v[1] * c[u].w0, c[u].v[1] * c[u].w1);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&S.sc_full[p.s]);
+            p.next(kScales);
+            ss.load(a, tiles, row, c[u]);
+        }
+    }
+}
+
+// Running totals of two columns in one 64-bit register pair.
+__device__ __forceinline__ float2 pair(uint64_t v) {
+    return make_float2(__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32)));
+}
+__device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi) {
+    return (uint64_t)lo | ((uint64_t)hi << 32);
+}
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+    return pair(__float_as_uint(lo), __float_as_uint(hi));
+}
+// acc += r * s for 32 columns, two at a time.
+__device__ __forceinline__ void promote32(uint64_t *acc, const uint32_t (&r)[32], uint64_t s) {
+#pragma unroll
+    for (int i = 0; i < 32; i += 2)
+        asm("fma.rn.f32x2 %0, %1, %2, %0;"
+            : "+l"(acc[i / 2]) : "l"(pair(r[i], r[i + 1])), "l"(s));
+}
 
 __device__ __forceinline__ void store32B(void *p, const uint32_t (&v)[8]) {
     asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]),
@@ -375,16 +416,11 @@ __device__ void finish(const TcArgs &a, Shared &S, int tiles, uint32_t tmem) {
     const int quad = warp & 3, half = (warp - kEpiWarp0) >> 2;
     const int row = quad * 32 + lane;
     const uint32_t base = tmem + ((uint32_t)quad << 21) + (uint32_t)(half * 64);  // lane quad * 32
-    Pos q;
+    Pos q, p;
     uint32_t par = 0;
     int i = blockIdx.x;
     if (i >= tiles) return;
-    ScaleStream<kMode> ss;
-    ss.start(a, row);
-    Tile next = ss.t;
-    Scale c[kAhead];
-#pragma unroll
-    for (int u = 0; u < kAhead; u++) c[u] = ss.load(a, tiles, row);
+    Tile next = tile_at<kMode>(a, i);
     for (; i < tiles; i += gridDim.x) {
         const Tile t = next;
         if (i + (int)gridDim.x < tiles) next = tile_at<kMode>(a, i + gridDim.x);
@@ -393,30 +429,32 @@ __device__ void finish(const TcArgs &a, Shared &S, int tiles, uint32_t tmem) {
         for (int j = 0; j < 32; j++) acc[0][j] = acc[1][j] = 0u;
         const bool busy = quad * 32 < t.n;
         for (int b = 0; b < a.nkb; b++) {
-            const float f0 = c[0].v * c[0].w0, f1 = c[0].v * c[0].w1;
-            const uint64_t s0 = pair(f0, f0), s1 = pair(f1, f1);
-#pragma unroll
-            for (int u = 0; u + 1 < kAhead; u++) c[u] = c[u + 1];
-            c[kAhead - 1] = ss.load(a, tiles, row);
+            if (!waitw(S, &S.sc_full[p.s], p.ph, a.status)) return;
+            const float2 f = S.scale[p.s][row];
             if (!waitw(S, &S.acc_full[q.s], q.ph, a.status)) return;
             if (busy) {
                 tc_fence_after();
                 const uint32_t d = base + (uint32_t)(q.s * kNW);
+                const uint64_t s0 = pair(f.x, f.x), s1 = pair(f.y, f.y);
 #pragma unroll
-                for (int j = 0; j < 4; j++) {
-                    uint32_t r0[16], r1[16];
-                    tmem_ld16(d + 16 * j, r0);
-                    tmem_ld16(d + 128 + 16 * j, r1);
+                for (int j = 0; j < 2; j++) {
+                    uint32_t r0[32], r1[32];
+                    tmem_ld32(d + 32 * j, r0);
+                    tmem_ld32(d + 128 + 32 * j, r1);
                     tmem_ld_wait(r0);
                     reg_tie(r1);
-                    promote16(acc[0] + 8 * j, r0, s0);
-                    promote16(acc[1] + 8 * j, r1, s1);
+                    promote32(acc[0] + 16 * j, r0, s0);
+                    promote32(acc[1] + 16 * j, r1, s1);
                 }
                 tc_fence_before();
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(&S.acc_empty[q.s]);
+            if (lane == 0) {
+                mbar_arrive(&S.acc_empty[q.s]);
+                mbar_arrive(&S.sc_empty[p.s]);
+            }
             q.next(kAccs);
+            p.next(kScales);
         }
         if (!busy) continue;
         if (kMode == kGateUp) {
@@ -519,6 +557,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&S.acc_full[i], 1);
             mbar_init(&S.acc_empty[i], kEpiWarps);
         }
+        for (int i = 0; i < kScales; i++) {
+            mbar_init(&S.sc_full[i], 2);
+            mbar_init(&S.sc_empty[i], kEpiWarps);
+        }
         mbar_init(&S.done, 1);
         S.abort = 0;
         fence_barrier_init();
@@ -539,6 +581,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (warp == 1) {
             if ((threadIdx.x & 31) == 0) multiply(a, S, ring, tiles, tmem);
         }
+        if (warp >= 2) scales<kMode>(a, S, tiles, warp - 2);
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
         finish<kMode, T>(a, S, tiles, tmem);
