@@ -10,18 +10,23 @@
 //
 // Tile: 128 tokens (the MMA's M side) by 256 weight rows (N): rows of one matrix, or 128 gate rows
 // and the 128 up rows of the same ffn values.  Tokens sit on the M side so that a tensor-memory
-// lane is a token: an epilogue thread's scale is then one number per block and operand.  With the weights on the M side the scale changes from column to column and has to
-// be read from shared memory, two 16-byte loads per four elements; the loads, not the
-// additions, then bound the kernel (1380 clocks per block of 128 k against 512 of MMA).  An
-// expert with few tokens leaves rows of the MMA unused, which costs nothing that counts: it is
-// bound by its weights' bytes.  One persistent CTA per SM.
+// lane is a token: an epilogue thread's scale is then one number per block and operand.  With the
+// weights on the M side the scale changes from column to column and has to be read from shared
+// memory, two 16-byte loads per four elements; the loads, not the additions, then bound the
+// kernel (1380 clocks per block of 128 k against 512 of MMA).  An expert with few tokens leaves
+// rows of the MMA unused, which costs nothing that counts: it is bound by its weights' bytes.
+//
+// One persistent CTA per SM, or a pair of CTAs (cta_group::2) per tile of 256 tokens: each CTA
+// then loads its own 128 token rows and half of the weight rows, 32 KB per block of k instead of
+// 48 KB, because a single CTA's tile is bound by what L2 can deliver to an SM.
 //
 // Roles (384 threads; registers move from the first four warps to the epilogue):
 //   warp 0        TMA producer: weight boxes of 128 rows x 128 bytes, token rows as boxes of 16
-//                 or, for routed tokens, gathered four at a time
-//   warp 1        tensor-memory allocation and the MMA issuer
+//   warp 1        tensor-memory allocation and the MMA issuer; in the second CTA of a pair it
+//                 passes "stage full" on to the first
 //   warps 2-3     scales: as * bs of every token, block and operand, into a ring, loaded four
-//                 blocks ahead
+//                 blocks ahead; gate/up: also the routed token rows, gathered with 16-byte
+//                 cp.async (a TMA gather of four rows costs about 70 clocks, 32 of them a block)
 //   warps 4-11    epilogue: lane quarter (warp % 4), 64 columns of each 128-row operand
 // Every hand-off is an mbarrier and every wait is bounded (MOE_ERR_TIMEOUT in the status word).
 #include <algorithm>
@@ -41,8 +46,13 @@ constexpr int kNW = 256;                       // weight rows of a tile (gate/up
 constexpr int kEpiWarp0 = 4, kEpiWarps = 8;
 constexpr int kThreads = (kEpiWarp0 + kEpiWarps) * 32;
 constexpr uint32_t kOperand = 128 * kSBlk;     // bytes of 128 rows of one block
-constexpr uint32_t kStage = 3 * kOperand;      // the weights' two operands and the tokens
-constexpr int kStages = 4;
+constexpr uint32_t kRing = 12 * kOperand;      // shared memory of all stages
+// A stage holds the weights (two operands, or this CTA's one of a pair) and 128 token rows.
+constexpr uint32_t weight_bytes(int pair) { return (uint32_t)(3 - pair) * kOperand; }
+constexpr uint32_t stage_bytes(int pair) { return weight_bytes(pair) + kOperand; }
+constexpr int stages(int pair) { return (int)(kRing / stage_bytes(pair)); }
+constexpr int kMaxStages = 6;
+static_assert(stages(1) == 4 && stages(2) == kMaxStages, "stages");
 constexpr int kAccs = 2;                       // accumulator buffers of 256 columns
 constexpr int kScales = 8;                     // depth of the scale ring
 constexpr int kAhead = 4;                      // blocks whose scales are loaded ahead
@@ -65,7 +75,9 @@ struct TcArgs {
     const Job *slices;           // experts: runs of up to 128 slots (k_scaled_slices)
     const int32_t *nslices;
     const int32_t *perm;
-    int T, k, routed;            // routed = T * k
+    const uint8_t *xq;           // gate/up: the token rows [T][x_cols]
+    int x_cols;
+    int k, routed;               // routed = T * k
     const float *as;
     int64_t ldas;
     const float *ws0, *ws1;      // weight scales [expert][row blocks][nkb]; ws1: up
@@ -80,21 +92,22 @@ struct TcArgs {
 };
 
 struct Tile {
-    int e, rt, slot, n, npad;
+    int e, rt, slot, n;
     bool shared;
 };
 
-// Tile i: row tiles innermost, so that the CTAs that run at the same time share an expert's
-// weights (its slices follow one another) and a slice's tokens.
-template <int kMode>
-__device__ __forceinline__ Tile tile_at(const TcArgs &a, int i) {
+// Tile i as CTA `rank` of its kPair CTAs sees it (its own 128 tokens; n may be 0 or less in the
+// second).  Row tiles are innermost, so that the CTAs that run at the same time share an
+// expert's weights (its slices follow one another) and a slice's tokens.
+template <int kMode, int kPair>
+__device__ __forceinline__ Tile tile_at(const TcArgs &a, int i, int rank) {
     Tile t;
     const int s = i / a.row_tiles;
     t.rt = i - s * a.row_tiles;
     if (kMode == kDense) {
         t.e = 0;
-        t.slot = s * kMT;
-        t.n = min(kMT, a.M - t.slot);
+        t.slot = s * (kPair * kMT);
+        t.n = min(kPair * kMT, a.M - t.slot);
         t.shared = false;
     } else {
         const int4 v = __ldg(reinterpret_cast<const int4 *>(a.slices) + s);
@@ -103,8 +116,18 @@ __device__ __forceinline__ Tile tile_at(const TcArgs &a, int i) {
         t.n = v.z;
         t.shared = v.w != 0;
     }
-    t.npad = (t.n + 15) & ~15;
+    t.slot += rank * kMT;
+    t.n = min(kMT, t.n - rank * kMT);
     return t;
+}
+// Tiles go round the clusters (single CTAs or pairs).
+template <int kPair>
+__device__ __forceinline__ int first_tile() { return (int)blockIdx.x / kPair; }
+template <int kPair>
+__device__ __forceinline__ int tile_step() { return (int)gridDim.x / kPair; }
+template <int kPair>
+__device__ __forceinline__ int tiles_of_cta(int tiles) {
+    return max(0, tiles - first_tile<kPair>() + tile_step<kPair>() - 1) / tile_step<kPair>();
 }
 
 // silu(g) * u in fp32 with CUDA's expf and its approximate division (2 ulp; a denominator past
@@ -127,16 +150,17 @@ __device__ __forceinline__ int entry_token(const TcArgs &a, int p) {
 }
 
 struct Shared {
-    uint64_t full[kStages], empty[kStages], acc_full[kAccs], acc_empty[kAccs], sc_full[kScales],
-        sc_empty[kScales], done;
+    uint64_t full[kMaxStages], empty[kMaxStages], peer[kMaxStages], acc_full[kAccs],
+        acc_empty[kAccs], sc_full[kScales], sc_empty[kScales], done;
     uint32_t tmem;
     int abort;
+    int token[kMT];                       // gate/up: the tile's token rows
     float2 scale[kScales][kMT];
     uint32_t amax[2][2][kMT];             // gate/up: by tile parity and column half, per token
     float patch[kEpiWarps][32][kPatch + 1];
 };
 
-constexpr size_t kSmem = 1024 + (size_t)kStages * kStage + sizeof(Shared);
+constexpr size_t kSmem = 1024 + (size_t)kRing + sizeof(Shared);
 static_assert(kSmem <= 232448, "shared memory");
 
 struct Pos {                          // ring position
@@ -150,131 +174,148 @@ struct Pos {                          // ring position
     }
 };
 
-__device__ __forceinline__ bool wait_slow(uint64_t *bar, uint32_t parity, int *abort,
-                                       uint32_t *status) {
+// Bounded wait; false once this CTA gives up.
+__device__ __forceinline__ bool wait1(Shared &S, uint64_t *bar, uint32_t parity, uint32_t *st) {
+    if (mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = globaltimer();
     while (!mbar_try_wait(bar, parity)) {
-        if (*(volatile int *)abort) return false;
+        if (*(volatile int *)&S.abort) return false;
         if (globaltimer() - t0 > kWaitNs) {
-            *(volatile int *)abort = 1;
-            set_status(status, MOE_ERR_TIMEOUT);
+            *(volatile int *)&S.abort = 1;
+            set_status(st, MOE_ERR_TIMEOUT);
             return false;
         }
     }
     return true;
-}
-__device__ __forceinline__ bool wait1(Shared &S, uint64_t *bar, uint32_t parity, uint32_t *st) {
-    return mbar_try_wait(bar, parity) || wait_slow(bar, parity, &S.abort, st);
 }
 // The same for a whole warp, with one answer.
 __device__ __forceinline__ bool waitw(Shared &S, uint64_t *bar, uint32_t parity, uint32_t *st) {
     return __all_sync(0xffffffffu, wait1(S, bar, parity, st));
 }
 
-template <int kMode>
-__device__ void produce(const TcArgs &a, Shared &S, uint8_t *ring, int tiles, const CUtensorMap *w0,
-                        const CUtensorMap *w1, const CUtensorMap *x) {
+template <int kMode, int kPair>
+__device__ void produce(const TcArgs &a, Shared &S, uint8_t *ring, int tiles, int rank,
+                        const CUtensorMap *w0, const CUtensorMap *w1, const CUtensorMap *x) {
     const int lane = threadIdx.x & 31;
+    const int mine = tiles_of_cta<kPair>(tiles);
     Pos p;
     int issued = 0;
+    if (mine == 0) return;
+    Tile next = tile_at<kMode, kPair>(a, first_tile<kPair>(), rank);
     bool ok = true;
-    int i = blockIdx.x;
-    if (i >= tiles) return;
-    Tile next = tile_at<kMode>(a, i);
-    int entry[4] = {0, 0, 0, 0};
-    auto entries = [&] {
-        if (kMode == kGateUp) {
-#pragma unroll
-            for (int j = 0; j < 4; j++)
-                entry[j] = slot_entry(a, next, next.slot + min(4 * lane + j, next.n - 1));
-        }
-    };
-    entries();
-    for (; ok && i < tiles; i += gridDim.x) {
+    for (int m = 0; ok && m < mine; m++) {
         const Tile t = next;
-        int y[4];
-#pragma unroll
-        for (int j = 0; j < 4; j++) y[j] = kMode == kGateUp ? entry_token(a, entry[j]) : 0;
-        // the next tile's place and token rows arrive while this one's blocks are issued
-        const bool more = i + gridDim.x < tiles;
-        if (more) next = tile_at<kMode>(a, i + gridDim.x);
+        const int npad = kMode == kGateUp ? 0 : max(0, (t.n + 15) & ~15);
+        // the next tile's place arrives while this one's blocks are issued
+        if (m + 1 < mine)
+            next = tile_at<kMode, kPair>(a, first_tile<kPair>() + (m + 1) * tile_step<kPair>(), rank);
         for (int b = 0; b < a.nkb; b++) {
             if (!waitw(S, &S.empty[p.s], p.ph ^ 1u, a.status)) {
                 ok = false;
                 break;
             }
-            uint8_t *st = ring + (size_t)p.s * kStage;
+            uint8_t *st = ring + (size_t)p.s * stage_bytes(kPair);
             uint64_t *bar = &S.full[p.s];
             if (lane == 0) {
-                mbar_arrive_expect_tx(bar, 2 * kOperand + (uint32_t)t.npad * kSBlk);
+                mbar_arrive_expect_tx(bar, weight_bytes(kPair) + (uint32_t)npad * kSBlk);
                 const int r0 = kMode == kGateUp ? t.rt * 128 : t.rt * kNW;
-                tma_load_3d(st, w0, b * kSBlk, r0, t.e, bar);
-                tma_load_3d(st + kOperand, w1, b * kSBlk, kMode == kGateUp ? r0 : r0 + 128, t.e,
-                            bar);
+                const int r1 = kMode == kGateUp ? r0 : r0 + 128;
+                if (kPair == 1 || rank == 0) tma_load_3d(st, w0, b * kSBlk, r0, t.e, bar);
+                if (kPair == 1)
+                    tma_load_3d(st + kOperand, w1, b * kSBlk, r1, t.e, bar);
+                else if (rank == 1)
+                    tma_load_3d(st, w1, b * kSBlk, r1, t.e, bar);
             }
             __syncwarp();
-            uint8_t *xs = st + 2 * kOperand;
-            if (kMode == kGateUp) {
-                if (4 * lane < t.npad)
-                    tma_gather4(xs + lane * 4 * kSBlk, x, b * kSBlk, y[0], y[1], y[2], y[3], bar);
-            } else if (16 * lane < t.npad) {
-                tma_load_2d(xs + lane * 16 * kSBlk, x, b * kSBlk, t.slot + 16 * lane, bar);
-            }
+            if (kMode != kGateUp && 16 * lane < npad)
+                tma_load_2d(st + weight_bytes(kPair) + lane * 16 * kSBlk, x, b * kSBlk,
+                            t.slot + 16 * lane, bar);
             issued++;
-            p.next(kStages);
-            if (b == 0 && more) entries();
+            p.next(stages(kPair));
         }
     }
-    // leaving early: the copies in flight land before the CTA goes
-    if (!ok) {
-        for (int j = max(0, issued - kStages); j < issued; j++)
-            mbar_wait_bounded(&S.full[j % kStages], (uint32_t)(j / kStages) & 1u, kWaitNs);
+    // leaving early, the copies in flight land before the CTA goes; else the stages' last uses
+    // are over (a pair's commits reach both CTAs)
+    for (int j = max(0, issued - stages(kPair)); j < issued; j++) {
+        const int s = j % stages(kPair);
+        const uint32_t ph = (uint32_t)(j / stages(kPair)) & 1u;
+        if (ok)
+            wait1(S, &S.empty[s], ph, a.status);
+        else
+            mbar_wait_bounded(&S.full[s], ph, kWaitNs);
     }
 }
 
+// One thread of a single CTA or of a pair's first.
+template <int kMode, int kPair>
 __device__ void multiply(const TcArgs &a, Shared &S, uint8_t *ring, int tiles, uint32_t tmem) {
+    constexpr uint32_t idesc = instr_desc(0, kPair * kMT, kNW);
+    const int64_t total = (int64_t)tiles_of_cta<kPair>(tiles) * a.nkb;
     Pos p, q;
-    constexpr uint32_t idesc = instr_desc(0, kMT, kNW);
-    for (int i = blockIdx.x; i < tiles; i += gridDim.x) {
-        for (int b = 0; b < a.nkb; b++) {
-            if (!wait1(S, &S.acc_empty[q.s], q.ph ^ 1u, a.status) ||
-                !wait1(S, &S.full[p.s], p.ph, a.status)) {
-                umma_commit(&S.done);
-                mbar_wait_bounded(&S.done, 0, kWaitNs);
-                return;
-            }
-            tc_fence_after();
-            const uint32_t st = smem_u32(ring + (size_t)p.s * kStage);
-            const uint32_t d = tmem + (uint32_t)(q.s * kNW);
-            const uint64_t x = smem_desc(st + 2 * kOperand, 1024, 2), w = smem_desc(st, 1024, 2);
+    for (int64_t i = 0; i < total; i++) {
+        if (!wait1(S, &S.acc_empty[q.s], q.ph ^ 1u, a.status) ||
+            !wait1(S, &S.full[p.s], p.ph, a.status) ||
+            (kPair == 2 && !wait1(S, &S.peer[p.s], p.ph, a.status))) {
+            kPair == 2 ? umma_commit_pair(&S.done) : umma_commit(&S.done);
+            mbar_wait_bounded(&S.done, 0, kWaitNs);
+            return;
+        }
+        // gathered rows were written by ordinary copies: seen by their arrivals, and made visible
+        // to the tensor core here
+        if (kMode == kGateUp) fence_proxy_async_smem();
+        tc_fence_after();
+        const uint32_t st = smem_u32(ring + (size_t)p.s * stage_bytes(kPair));
+        const uint32_t d = tmem + (uint32_t)(q.s * kNW);
+        const uint64_t x = smem_desc(st + weight_bytes(kPair), 1024, 2), w = smem_desc(st, 1024, 2);
 #pragma unroll
-            for (int j = 0; j < 4; j++)      // 32 bytes of k a step: 2 units of 16 bytes
+        for (int j = 0; j < 4; j++) {        // 32 bytes of k a step: 2 units of 16 bytes
+            if (kPair == 2)
+                umma_f8_pair(d, x + 2 * j, w + 2 * j, idesc, j > 0);
+            else
                 umma_f8(d, x + 2 * j, w + 2 * j, idesc, j > 0);
+        }
+        if (kPair == 2) {
+            umma_commit_both(&S.empty[p.s]);
+            umma_commit_both(&S.acc_full[q.s]);
+        } else {
             umma_commit(&S.empty[p.s]);
             umma_commit(&S.acc_full[q.s]);
-            p.next(kStages);
-            q.next(kAccs);
         }
+        p.next(stages(kPair));
+        q.next(kAccs);
     }
 }
 
-// Warps 2 and 3: the scales of every tile and block, in the order the epilogue takes them: the
-// token's scale times the two operands' weight scales, one pair per token.  Loads run kAhead
-// blocks ahead of the ring's writes, across tiles.
-template <int kMode>
+// One thread of a pair's second CTA: its full stages are announced to the first.
+__device__ void announce(const TcArgs &a, Shared &S, int tiles) {
+    const int64_t total = (int64_t)tiles_of_cta<2>(tiles) * a.nkb;
+    Pos p;
+    for (int64_t i = 0; i < total; i++) {
+        if (!wait1(S, &S.full[p.s], p.ph, a.status)) return;
+        fence_proxy_async_smem();
+        mbar_arrive_at(&S.peer[p.s], 0);
+        p.next(stages(2));
+    }
+}
+
+// The scales of one thread's two tokens, in the order the epilogue takes them, and the tokens
+// themselves.
+template <int kMode, int kPair>
 struct ScaleStream {
     struct Set {
         float v[2], w0, w1;
     };
-    int i, b, entry[2];
+    int m, b, entry[2];
     Tile t, next;
     const float *as[2], *s0, *s1;
 
     __device__ __forceinline__ void look(const TcArgs &a, int row) {
         if (kMode == kGateUp) {
 #pragma unroll
-            for (int j = 0; j < 2; j++)
-                entry[j] = slot_entry(a, next, next.slot + min(row + 32 * j, next.n - 1));
+            for (int j = 0; j < 2; j++) {
+                const int r = row + 32 * j;
+                entry[j] = r < next.n ? slot_entry(a, next, next.slot + r) : 0;
+            }
         }
     }
     __device__ __forceinline__ void open(const TcArgs &a, int row) {
@@ -294,15 +335,15 @@ struct ScaleStream {
             s1 = t.rt * kNW + kSBlk < a.rows ? s0 + a.nkb : s0;    // past the last rows: not stored
         }
     }
-    __device__ __forceinline__ void start(const TcArgs &a, int row) {
-        i = blockIdx.x;
+    __device__ __forceinline__ void start(const TcArgs &a, int row, int rank) {
+        m = 0;
         b = 0;
-        next = tile_at<kMode>(a, i);
+        next = tile_at<kMode, kPair>(a, first_tile<kPair>(), rank);
         look(a, row);
         open(a, row);
     }
-    __device__ __forceinline__ void load(const TcArgs &a, int tiles, int row, Set &c) {
-        if (i >= tiles) return;
+    __device__ __forceinline__ void load(const TcArgs &a, int mine, int row, int rank, Set &c) {
+        if (m >= mine) return;
 #pragma unroll
         for (int j = 0; j < 2; j++) {
             c.v[j] = 0.f;
@@ -313,42 +354,114 @@ struct ScaleStream {
         }
         c.w0 = __ldg(s0 + b);
         c.w1 = __ldg(s1 + b);
-        const bool more = i + (int)gridDim.x < tiles;
+        const bool more = m + 1 < mine;
         if (b == 0 && more) {
-            next = tile_at<kMode>(a, i + gridDim.x);
+            next = tile_at<kMode, kPair>(a, first_tile<kPair>() + (m + 1) * tile_step<kPair>(), rank);
             look(a, row);
         }
         if (++b == a.nkb) {
             b = 0;
-            i += gridDim.x;
+            m++;
             if (more) open(a, row);
         }
     }
 };
 
-template <int kMode>
-__device__ void scales(const TcArgs &a, Shared &S, int tiles, int which) {
-    const int lane = threadIdx.x & 31, row = which * 64 + lane;
-    if ((int)blockIdx.x >= tiles) return;
-    ScaleStream<kMode> ss;
-    typename ScaleStream<kMode>::Set c[kAhead];
-    ss.start(a, row);
+// Routed token rows of a warp's 64 tokens: eight lanes per row, four rows per step.  The loop
+// stays rolled and the tokens in shared memory: unrolled into the scales' loop it ran at 200
+// clocks a copy, waiting for instructions.
+template <int kPair>
+struct Gather {
+    int m, b, n, entry[2];
+    Pos p;
+
+    // perm's entries of tile m, to be used when it opens
+    __device__ __forceinline__ int look(const TcArgs &a, int first, int rank) {
+        const int lane = threadIdx.x & 31;
+        const Tile t = tile_at<kGateUp, kPair>(a, first_tile<kPair>() + m * tile_step<kPair>(), rank);
 #pragma unroll
-    for (int u = 0; u < kAhead; u++) ss.load(a, tiles, row, c[u]);
-    const int mine = (tiles - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
+        for (int j = 0; j < 2; j++) {
+            const int r = first + 32 * j + lane;
+            entry[j] = r < t.n ? slot_entry(a, t, t.slot + r) : 0;
+        }
+        return t.n;
+    }
+    int n_next;
+    __device__ __forceinline__ void open(const TcArgs &a, Shared &S, int mine, int first, int rank) {
+        const int lane = threadIdx.x & 31;
+        n = n_next;
+        __syncwarp();
+        S.token[first + lane] = entry_token(a, entry[0]);
+        S.token[first + 32 + lane] = entry_token(a, entry[1]);
+        __syncwarp();
+        if (++m < mine) n_next = look(a, first, rank);
+    }
+    __device__ __forceinline__ void start(const TcArgs &a, Shared &S, int mine, int first, int rank) {
+        m = b = 0;
+        n_next = look(a, first, rank);
+        open(a, S, mine, first, rank);
+    }
+    // issue the next block; false when a wait gave up
+    __device__ __forceinline__ bool step(const TcArgs &a, Shared &S, uint8_t *ring, int mine,
+                                         int first, int rank) {
+        const int lane = threadIdx.x & 31;
+        if (!waitw(S, &S.empty[p.s], p.ph ^ 1u, a.status)) return false;
+        uint8_t *xs = ring + (size_t)p.s * stage_bytes(kPair) + weight_bytes(kPair);
+        const int c = lane & 7, col = b * kSBlk + 16 * c;
+        const bool in = col < a.x_cols;
+        const uint8_t *src = a.xq + (in ? col : 0);
+        const int last = min(n, first + 64);
+#pragma unroll 4
+        for (int r = first + (lane >> 3); r < last; r += 4)
+            cp_async16_if(xs + r * kSBlk + ((c ^ (r & 7)) << 4),
+                          src + (int64_t)S.token[r] * a.x_cols, in);
+        cp_async_arrive(&S.full[p.s]);
+        p.next(stages(kPair));
+        if (++b == a.nkb) {
+            b = 0;
+            if (m < mine) open(a, S, mine, first, rank);
+        }
+        return true;
+    }
+};
+
+template <int kMode, int kPair>
+__device__ void feed(const TcArgs &a, Shared &S, uint8_t *ring, int tiles, int rank, int which) {
+    const int lane = threadIdx.x & 31, row = which * 64 + lane;
+    const int mine = tiles_of_cta<kPair>(tiles);
+    if (mine == 0) return;
+    Gather<kPair> g;
+    if (kMode == kGateUp) g.start(a, S, mine, which * 64, rank);
+    ScaleStream<kMode, kPair> ss;
+    typename ScaleStream<kMode, kPair>::Set c[kAhead];
+    ss.start(a, row, rank);
+#pragma unroll
+    for (int u = 0; u < kAhead; u++) ss.load(a, mine, row, rank, c[u]);
     const int64_t total = (int64_t)mine * a.nkb;
     Pos p;
     for (int64_t b0 = 0; b0 < total; b0 += kAhead) {
+        if (kMode == kGateUp) {
+#pragma unroll 1
+            for (int u = 0; u < kAhead && b0 + u < total; u++) {
+                if (!g.step(a, S, ring, mine, which * 64, rank)) {
+                    cp_async_wait_all();
+                    return;
+                }
+            }
+        }
 #pragma unroll
         for (int u = 0; u < kAhead; u++) {
             if (b0 + u >= total) break;
-            if (!waitw(S, &S.sc_empty[p.s], p.ph ^ 1u, a.status)) return;
+            if (!waitw(S, &S.sc_empty[p.s], p.ph ^ 1u, a.status)) {
+                if (kMode == kGateUp) cp_async_wait_all();
+                return;
+            }
             S.scale[p.s][row] = make_float2(c[u].v[0] * c[u].w0, c[u].v[0] * c[u].w1);
             S.scale[p.s][row + 32] = make_float2(c[u].v[1] * c[u].w0, c[u].v[1] * c[u].w1);
             __syncwarp();
             if (lane == 0) mbar_arrive(&S.sc_full[p.s]);
             p.next(kScales);
-            ss.load(a, tiles, row, c[u]);
+            ss.load(a, mine, row, rank, c[u]);
         }
     }
 }
@@ -410,20 +523,21 @@ __device__ __forceinline__ void store16(T *p, const uint64_t *acc) {
     }
 }
 
-template <int kMode, typename T>
-__device__ void finish(const TcArgs &a, Shared &S, int tiles, uint32_t tmem) {
+template <int kMode, int kPair, typename T>
+__device__ void finish(const TcArgs &a, Shared &S, int tiles, int rank, uint32_t tmem) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int quad = warp & 3, half = (warp - kEpiWarp0) >> 2;
     const int row = quad * 32 + lane;
     const uint32_t base = tmem + ((uint32_t)quad << 21) + (uint32_t)(half * 64);  // lane quad * 32
     Pos q, p;
     uint32_t par = 0;
-    int i = blockIdx.x;
-    if (i >= tiles) return;
-    Tile next = tile_at<kMode>(a, i);
-    for (; i < tiles; i += gridDim.x) {
+    const int mine = tiles_of_cta<kPair>(tiles);
+    if (mine == 0) return;
+    Tile next = tile_at<kMode, kPair>(a, first_tile<kPair>(), rank);
+    for (int m = 0; m < mine; m++) {
         const Tile t = next;
-        if (i + (int)gridDim.x < tiles) next = tile_at<kMode>(a, i + gridDim.x);
+        if (m + 1 < mine)
+            next = tile_at<kMode, kPair>(a, first_tile<kPair>() + (m + 1) * tile_step<kPair>(), rank);
         uint64_t acc[2][32];            // two columns each
 #pragma unroll
         for (int j = 0; j < 32; j++) acc[0][j] = acc[1][j] = 0u;
@@ -450,7 +564,10 @@ __device__ void finish(const TcArgs &a, Shared &S, int tiles, uint32_t tmem) {
             }
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive(&S.acc_empty[q.s]);
+                if (kPair == 2)
+                    mbar_arrive_at(&S.acc_empty[q.s], 0);
+                else
+                    mbar_arrive(&S.acc_empty[q.s]);
                 mbar_arrive(&S.sc_empty[p.s]);
             }
             q.next(kAccs);
@@ -460,21 +577,21 @@ __device__ void finish(const TcArgs &a, Shared &S, int tiles, uint32_t tmem) {
         if (kMode == kGateUp) {
             // h, and its e4m3 form per token and 128 ffn values: this thread's 64 and the other
             // column half's
-            uint32_t m = 0u;
+            uint32_t mx = 0u;
 #pragma unroll
             for (int j = 0; j < 32; j++) {
                 const float2 g = pair(acc[0][j]), u = pair(acc[1][j]);
                 const float h0 = silu_mul(g.x, u.x), h1 = silu_mul(g.y, u.y);
                 acc[0][j] = pair(h0, h1);
-                m = max(m, max(__float_as_uint(h0) & 0x7fffffffu, __float_as_uint(h1) & 0x7fffffffu));
+                mx = max(mx, max(__float_as_uint(h0) & 0x7fffffffu, __float_as_uint(h1) & 0x7fffffffu));
             }
-            S.amax[par][half][row] = m;
+            S.amax[par][half][row] = mx;
             named_barrier(1 + quad, 64);
-            m = max(m, S.amax[par][half ^ 1][row]);
+            mx = max(mx, S.amax[par][half ^ 1][row]);
             par ^= 1u;
             if (row < t.n) {
-                const bool fin = m < 0x7f800000u;
-                const float sc = fin ? __fdiv_rn(__uint_as_float(m), kE4M3Max) : 0.f;
+                const bool fin = mx < 0x7f800000u;
+                const float sc = fin ? __fdiv_rn(__uint_as_float(mx), kE4M3Max) : 0.f;
                 // h / sc as (h * pre) * (1 / (sc * pre)): pre keeps the reciprocal of a tiny scale finite
                 const float pre = sc < 0x1p-100f ? 0x1p100f : 1.0f;
                 const float inv = sc > 0.f ? __frcp_rn(sc * pre) : 0.f;
@@ -539,23 +656,25 @@ __device__ void finish(const TcArgs &a, Shared &S, int tiles, uint32_t tmem) {
     }
 }
 
-template <int kMode, typename T>
+template <int kMode, int kPair, typename T>
 __global__ void __launch_bounds__(kThreads, 1)
     k_scaled_tc(const TcArgs a, const __grid_constant__ CUtensorMap w0,
                 const __grid_constant__ CUtensorMap w1, const __grid_constant__ CUtensorMap x) {
     extern __shared__ uint8_t raw[];
-    uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) &
-                                                ~uintptr_t(1023));
-    Shared &S = *reinterpret_cast<Shared *>(ring + (size_t)kStages * kStage);
+    // the same offset in both CTAs of a pair: dynamic shared memory starts at one address
+    uint8_t *ring = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+    Shared &S = *reinterpret_cast<Shared *>(ring + (size_t)kRing);
     const int warp = threadIdx.x >> 5;
+    const int rank = kPair == 2 ? (int)cluster_rank() : 0;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kStages; i++) {
-            mbar_init(&S.full[i], 1);
+        for (int i = 0; i < stages(kPair); i++) {
+            mbar_init(&S.full[i], kMode == kGateUp ? 1 + 64 : 1);   // the gathering threads
             mbar_init(&S.empty[i], 1);
+            mbar_init(&S.peer[i], 1);
         }
         for (int i = 0; i < kAccs; i++) {
             mbar_init(&S.acc_full[i], 1);
-            mbar_init(&S.acc_empty[i], kEpiWarps);
+            mbar_init(&S.acc_empty[i], kPair * kEpiWarps);
         }
         for (int i = 0; i < kScales; i++) {
             mbar_init(&S.sc_full[i], 2);
@@ -566,40 +685,58 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_barrier_init();
     }
     if (warp == 1) {
-        tmem_alloc(&S.tmem, kTmemCols);
-        tmem_relinquish();
+        if (kPair == 2) {
+            tmem_alloc2(&S.tmem, kTmemCols);
+            tmem_relinquish2();
+        } else {
+            tmem_alloc(&S.tmem, kTmemCols);
+            tmem_relinquish();
+        }
     }
     tc_fence_before();
     __syncthreads();
+    if (kPair == 2) cluster_sync();
     tc_fence_after();
     const uint32_t tmem = S.tmem;
-    const int tiles = (kMode == kDense ? (a.M + kMT - 1) / kMT : *a.nslices) * a.row_tiles;
+    constexpr int kSlice = kPair * kMT;
+    const int tiles = (kMode == kDense ? (a.M + kSlice - 1) / kSlice : *a.nslices) * a.row_tiles;
     if (warp < kEpiWarp0) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRoleRegs));
-        if (warp == 0)
-            produce<kMode>(a, S, ring, tiles, &w0, &w1, &x);
-        if (warp == 1) {
-            if ((threadIdx.x & 31) == 0) multiply(a, S, ring, tiles, tmem);
+        if (warp == 0) {
+            produce<kMode, kPair>(a, S, ring, tiles, rank, &w0, &w1, &x);
+        } else if (warp == 1) {
+            if ((threadIdx.x & 31) == 0) {
+                if (rank == 0)
+                    multiply<kMode, kPair>(a, S, ring, tiles, tmem);
+                else
+                    announce(a, S, tiles);
+            }
+        } else {
+            feed<kMode, kPair>(a, S, ring, tiles, rank, warp - 2);
         }
-        if (warp >= 2) scales<kMode>(a, S, tiles, warp - 2);
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
-        finish<kMode, T>(a, S, tiles, tmem);
+        finish<kMode, kPair, T>(a, S, tiles, rank, tmem);
     }
     __syncwarp();
     tc_fence_before();
     __syncthreads();
+    // neither CTA of a pair leaves while the other's MMAs, commits or arrivals may reach it
+    if (kPair == 2) cluster_sync();
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem, kTmemCols);
+        if (kPair == 2)
+            tmem_dealloc2(tmem, kTmemCols);
+        else
+            tmem_dealloc(tmem, kTmemCols);
     }
 }
 
-// The runs of up to 128 slots of every expert with tokens, ascending, the shared one's last: the
+// The runs of up to `run` slots of every expert with tokens, ascending, the shared one's last: the
 // tiles' token side.  One CTA.
 __global__ void __launch_bounds__(1024)
     k_scaled_slices(const int32_t *__restrict__ offsets, int E, int T, int k, int shared,
-                    Job *slices, int32_t *nslices, uint32_t *status) {
+                    int run, Job *slices, int32_t *nslices, uint32_t *status) {
     __shared__ int s_first[kMaxE];
     __shared__ int s_warp[33];
     const int A = T * k;
@@ -607,21 +744,21 @@ __global__ void __launch_bounds__(1024)
         const int o = offsets[e], o1 = offsets[e + 1];
         const bool fits = o >= 0 && o <= o1 && o1 <= A;      // else not what a router wrote
         if (!fits) set_status(status, MOE_ERR_BOUNDS);
-        s_first[e] = fits ? (o1 - o + kMT - 1) / kMT : 0;
+        s_first[e] = fits ? (o1 - o + run - 1) / run : 0;
     }
     __syncthreads();
     // overlapping runs of damaged offsets could pass the list's end: those are left out too
-    const int most = A / kMT + min(E, A);
+    const int most = A / run + min(E, A);
     const int n = min(block_exclusive_scan<1024>(s_first, E, s_warp), most);
     for (int e = threadIdx.x; e < E; e += 1024) {
         const int o = offsets[e], o1 = offsets[e + 1];
         if (!(o >= 0 && o <= o1 && o1 <= A)) continue;
-        for (int s = o, j = s_first[e]; s < o1 && j < most; s += kMT, j++)
-            slices[j] = Job{e, s, min(kMT, o1 - s), 0};
+        for (int s = o, j = s_first[e]; s < o1 && j < most; s += run, j++)
+            slices[j] = Job{e, s, min(run, o1 - s), 0};
     }
-    const int ns = shared ? (T + kMT - 1) / kMT : 0;
+    const int ns = shared ? (T + run - 1) / run : 0;
     for (int j = threadIdx.x; j < ns; j += 1024)
-        slices[n + j] = Job{E, A + j * kMT, min(kMT, T - j * kMT), 1};
+        slices[n + j] = Job{E, A + j * run, min(run, T - j * run), 1};
     if (threadIdx.x == 0) *nslices = n + ns;
 }
 
@@ -682,10 +819,10 @@ bool encode(CUtensorMap *m, const void *base, int cols, int64_t rows, int64_t st
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int kMode, typename T>
+template <int kMode, int kPair, typename T>
 cudaError_t run_tc(const TcArgs &a, const CUtensorMap &w0, const CUtensorMap &w1,
                    const CUtensorMap &x, int64_t most_tiles, cudaStream_t st) {
-    auto kernel = k_scaled_tc<kMode, T>;
+    auto kernel = k_scaled_tc<kMode, kPair, T>;
     // the register split needs every register of the launch it was made for
     static const bool fits = [&] {
         cudaFuncAttributes at{};
@@ -695,10 +832,30 @@ cudaError_t run_tc(const TcArgs &a, const CUtensorMap &w0, const CUtensorMap &w1
     cudaError_t err = ensure_smem(kernel, kSmem);
     if (err != cudaSuccess) return err;
     const int sms = sm_count();
-    if (sms <= 0) return cudaErrorInvalidDevice;
-    kernel<<<(unsigned)std::min<int64_t>(sms, most_tiles), kThreads, kSmem, st>>>(a, w0, w1, x);
+    if (sms < kPair) return cudaErrorInvalidDevice;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(std::min<int64_t>(sms / kPair, most_tiles) * kPair));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kPair;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = kPair == 2 ? 1 : 0;
+    err = cudaLaunchKernelEx(&cfg, kernel, a, w0, w1, x);
+    if (err != cudaSuccess) return err;
     note_launches(1);
     return cudaGetLastError();
+}
+
+// Pairs of CTAs or single ones.
+template <int kMode, typename T>
+cudaError_t run_tc(bool pair, const TcArgs &a, const CUtensorMap &w0, const CUtensorMap &w1,
+                   const CUtensorMap &x, int64_t most_tiles, cudaStream_t st) {
+    return pair ? run_tc<kMode, 2, T>(a, w0, w1, x, most_tiles, st)
+                : run_tc<kMode, 1, T>(a, w0, w1, x, most_tiles, st);
 }
 
 size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
@@ -730,6 +887,11 @@ ExpertsWs experts_ws(const moe_scaled_weights &w, int T, int k) {
     return L;
 }
 
+bool use_pair(int M) { return M > kMT; }
+bool use_pair_experts(const moe_scaled_weights &w, int T, int k) {
+    return (int64_t)T * k > (int64_t)kMT * w.n_experts;
+}
+
 cudaError_t experts_tc(const ScaledExpertsArgs &e, uint8_t *ws, cudaStream_t st) {
     const moe_scaled_weights &w = e.w;
     const ExpertsWs L = experts_ws(w, e.T, e.k);
@@ -737,13 +899,14 @@ cudaError_t experts_tc(const ScaledExpertsArgs &e, uint8_t *ws, cudaStream_t st)
     Job *slices = reinterpret_cast<Job *>(ws + L.slices);
     int32_t *nslices = reinterpret_cast<int32_t *>(ws + L.nslices);
     float *xs = reinterpret_cast<float *>(ws + L.xs);
-    CUtensorMap gate, up, down, x, h;
+    CUtensorMap gate, up, down, h;
     if (!encode(&gate, w.d_gate, H, F, H, n, 128) || !encode(&up, w.d_up, H, F, H, n, 128) ||
-        !encode(&down, w.d_down, F, H, F, n, 128) || !encode(&x, ws + L.xq, H, e.T, H, 0, 1) ||
+        !encode(&down, w.d_down, F, H, F, n, 128) ||
         !encode(&h, ws + L.hq, F, L.slots, F, 0, 16))
         return cudaErrorInvalidValue;
-    k_scaled_slices<<<1, 1024, 0, st>>>(e.offsets, w.n_experts, e.T, e.k, w.shared, slices,
-                                        nslices, e.status);
+    const bool pair = use_pair_experts(w, e.T, e.k);
+    k_scaled_slices<<<1, 1024, 0, st>>>(e.offsets, w.n_experts, e.T, e.k, w.shared,
+                                        pair ? 2 * kMT : kMT, slices, nslices, e.status);
     note_launches(1);
     cudaError_t err = cudaGetLastError();
     if (err != cudaSuccess) return err;
@@ -753,7 +916,8 @@ cudaError_t experts_tc(const ScaledExpertsArgs &e, uint8_t *ws, cudaStream_t st)
     a.slices = slices;
     a.nslices = nslices;
     a.perm = e.perm;
-    a.T = e.T;
+    a.xq = ws + L.xq;
+    a.x_cols = H;
     a.k = e.k;
     a.routed = e.T * e.k;
     a.status = e.status;
@@ -768,7 +932,7 @@ cudaError_t experts_tc(const ScaledExpertsArgs &e, uint8_t *ws, cudaStream_t st)
     a.ws0 = w.d_gate_s;
     a.ws1 = w.d_up_s;
     a.ws_expert = (int64_t)sblocks(F) * sblocks(H);
-    err = run_tc<kGateUp, float>(a, gate, up, x, L.most_slices * a.row_tiles, st);
+    err = run_tc<kGateUp, float>(pair, a, gate, up, h, L.most_slices * a.row_tiles, st);
     if (err != cudaSuccess) return err;
     a.nkb = sblocks(F);
     a.rows = H;
@@ -779,7 +943,7 @@ cudaError_t experts_tc(const ScaledExpertsArgs &e, uint8_t *ws, cudaStream_t st)
     a.out = ws + L.y;
     a.ldo = H;
     a.vec = true;
-    err = run_tc<kDown, float>(a, down, down, h, L.most_slices * a.row_tiles, st);
+    err = run_tc<kDown, float>(pair, a, down, down, h, L.most_slices * a.row_tiles, st);
     if (err != cudaSuccess) return err;
     return with_dtype(e.out_dt, [&](auto *tag) {
         using E = std::remove_pointer_t<decltype(tag)>;
@@ -808,11 +972,13 @@ cudaError_t matmul_tc(const ScaledMatmulArgs &m, cudaStream_t st) {
     a.ldo = m.ldo;
     a.vec = (uintptr_t)m.out % 32 == 0 && m.ldo * dtype_bytes(m.dt) % 32 == 0 && m.N % 16 == 0;
     a.status = m.status;
-    const int64_t tiles = (int64_t)((m.M + kMT - 1) / kMT) * a.row_tiles;
+    const bool pair = use_pair(m.M);
+    const int slice = pair ? 2 * kMT : kMT;
+    const int64_t tiles = (int64_t)((m.M + slice - 1) / slice) * a.row_tiles;
     if (tiles > INT32_MAX) return cudaErrorInvalidValue;
     return with_dtype(m.dt, [&](auto *tag) {
         using E = std::remove_pointer_t<decltype(tag)>;
-        return run_tc<kDense, E>(a, b, b, x, tiles, st);
+        return run_tc<kDense, E>(pair, a, b, b, x, tiles, st);
     });
 }
 

@@ -315,7 +315,8 @@ def run_experts(torch, layer, x, ids, w, gate, out_dtype):
     (1, 8, 2, 256, 128, False), (1, 6, 6, 144, 48, True), (2, 16, 4, 512, 640, True),
     (3, 40, 5, 384, 144, True), (8, 5, 3, 272, 272, False), (9, 8, 2, 256, 128, False),
     (16, 4, 4, 400, 80, True), (33, 24, 3, 144, 400, True), (150, 3, 2, 640, 256, True),
-    (130, 64, 1, 256, 16, False), (300, 2, 1, 16, 128, True)])
+    (130, 64, 1, 256, 16, False), (300, 2, 1, 16, 128, True),
+    (600, 3, 2, 272, 144, True), (700, 4, 1, 128, 656, False)])
 def test_experts(torch, moe, xt, ot, T, E, k, H, F, shared):
     rng = np.random.default_rng(T * 1009 + E * 31 + H + F)
     W, layer = make_layer(torch, moe, rng, E, H, F, k, shared, T)
