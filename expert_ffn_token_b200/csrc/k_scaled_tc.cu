@@ -20,14 +20,16 @@
 // then loads its own 128 token rows and half of the weight rows, 32 KB per block of k instead of
 // 48 KB, because a single CTA's tile is bound by what L2 can deliver to an SM.
 //
-// Roles (384 threads; registers move from the first four warps to the epilogue):
+// Roles (640 threads; registers move from the first four warps to the epilogue):
 //   warp 0        TMA producer: weight boxes of 128 rows x 128 bytes, token rows as boxes of 16
 //   warp 1        tensor-memory allocation and the MMA issuer; in the second CTA of a pair it
 //                 passes "stage full" on to the first
-//   warps 2-3     scales: as * bs of every token, block and operand, into a ring, loaded four
-//                 blocks ahead; gate/up: also the routed token rows, gathered with 16-byte
-//                 cp.async (a TMA gather of four rows costs about 70 clocks, 32 of them a block)
-//   warps 4-11    epilogue: lane quarter (warp % 4), 64 columns of each 128-row operand
+//   warp 2        the scales of every block, copied into a ring four blocks a hand-over
+//   warp 3        gate/up: the routed token rows, gathered with 16-byte cp.async (a TMA gather of
+//                 four rows costs about 70 clocks, 32 of them a block)
+//   warps 4-19    epilogue: lane quarter (warp % 4), 32 columns of each 128-row operand.  Four warps
+//                 a scheduler, because a block is a chain of hand-overs and tensor-memory loads
+//                 that one warp cannot hide: with two, a block took 1250 clocks, 300 of them work
 // Every hand-off is an mbarrier and every wait is bounded (MOE_ERR_TIMEOUT in the status word).
 #include <algorithm>
 
@@ -43,7 +45,7 @@ using namespace ptx;
 
 constexpr int kMT = 128;                       // most tokens of a tile
 constexpr int kNW = 256;                       // weight rows of a tile (gate/up: 128 + 128)
-constexpr int kEpiWarp0 = 4, kEpiWarps = 8;
+constexpr int kEpiWarp0 = 4, kEpiWarps = 16;
 constexpr int kThreads = (kEpiWarp0 + kEpiWarps) * 32;
 constexpr uint32_t kOperand = 128 * kSBlk;     // bytes of 128 rows of one block
 constexpr uint32_t kRing = 12 * kOperand;      // shared memory of all stages
@@ -54,16 +56,17 @@ constexpr int stages(int pair) { return (int)(kRing / stage_bytes(pair)); }
 constexpr int kMaxStages = 6;
 static_assert(stages(1) == 4 && stages(2) == kMaxStages, "stages");
 constexpr int kAccs = 2;                       // accumulator buffers of 256 columns
-constexpr int kScales = 8;                     // depth of the scale ring
-constexpr int kAhead = 4;                      // blocks whose scales are loaded ahead
-constexpr int kPatch = 16;                     // columns per turn through shared memory (stores)
+constexpr int kBand = 8;                       // row tiles of a band (dense)
+constexpr int kGroup = 4;                      // blocks whose scales are handed over together
+constexpr int kScales = 4;                     // depth of the scale ring, in groups
+constexpr int kPatch = 8;                      // columns per turn through shared memory (stores)
 constexpr uint32_t kTmemCols = 512;
 constexpr uint64_t kWaitNs = 2000000000ull;    // limit of every wait
-// Registers: 384 threads launch with 168 each (64512); the first warpgroup keeps 96 and the two
-// epilogue warpgroups take 200: 128 * 96 + 256 * 200 = 63488.
-constexpr int kLaunchRegs = 168, kRoleRegs = 96, kEpiRegs = 200;
+// Registers: 640 threads launch with 96 each (61440); the first warpgroup keeps 64 and the four
+// epilogue warpgroups take 104: 128 * 64 + 512 * 104 = 61440.
+constexpr int kLaunchRegs = 96, kRoleRegs = 64, kEpiRegs = 104;
 static_assert(sizeof(Job) == sizeof(int4), "a slice is loaded as one vector");
-static_assert(128 * kRoleRegs + 256 * kEpiRegs <= kThreads * kLaunchRegs, "register split");
+static_assert(128 * kRoleRegs + 512 * kEpiRegs <= kThreads * kLaunchRegs, "register split");
 
 enum Mode { kGateUp, kDown, kDense };
 
@@ -97,14 +100,20 @@ struct Tile {
 };
 
 // Tile i as CTA `rank` of its kPair CTAs sees it (its own 128 tokens; n may be 0 or less in the
-// second).  Row tiles are innermost, so that the CTAs that run at the same time share an
-// expert's weights (its slices follow one another) and a slice's tokens.
+// second).  Experts: row tiles are innermost, so that the CTAs that run at the same time share
+// an expert's weights (its slices follow one another) and a slice's tokens.
 template <int kMode, int kPair>
 __device__ __forceinline__ Tile tile_at(const TcArgs &a, int i, int rank) {
     Tile t;
-    const int s = i / a.row_tiles;
+    int s = i / a.row_tiles;
     t.rt = i - s * a.row_tiles;
     if (kMode == kDense) {
+        // bands of kBand row tiles, so that the tiles in flight cover a compact part of both sides
+        const int ns = (a.M + kPair * kMT - 1) / (kPair * kMT);
+        const int band = i / (kBand * ns), in = i - band * (kBand * ns);
+        const int width = min(kBand, a.row_tiles - band * kBand);
+        s = in / width;
+        t.rt = band * kBand + in - s * width;
         t.e = 0;
         t.slot = s * (kPair * kMT);
         t.n = min(kPair * kMT, a.M - t.slot);
@@ -155,8 +164,9 @@ struct Shared {
     uint32_t tmem;
     int abort;
     int token[kMT];                       // gate/up: the tile's token rows
-    float2 scale[kScales][kMT];
-    uint32_t amax[2][2][kMT];             // gate/up: by tile parity and column half, per token
+    float as[kScales][kGroup][kMT];       // per block: the tokens' scales
+    float2 ws[kScales][kGroup];           // and the two operands' weight scales
+    uint32_t amax[2][4][kMT];             // gate/up: by tile parity and column quarter, per token
     float patch[kEpiWarps][32][kPatch + 1];
 };
 
@@ -174,13 +184,17 @@ struct Pos {                          // ring position
     }
 };
 
-// Bounded wait; false once this CTA gives up.
+// Bounded wait; false once this CTA gives up.  The clock and the abort flag are looked at once in
+// 64 tries: reading the global timer between tries would delay the wake-up.
 __device__ __forceinline__ bool wait1(Shared &S, uint64_t *bar, uint32_t parity, uint32_t *st) {
-    if (mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = globaltimer();
-    while (!mbar_try_wait(bar, parity)) {
+    uint64_t t0 = 0;
+#pragma unroll 1
+    for (uint32_t i = 0; !mbar_try_wait(bar, parity); i++) {
+        if ((i & 63u) != 63u) continue;
         if (*(volatile int *)&S.abort) return false;
-        if (globaltimer() - t0 > kWaitNs) {
+        const uint64_t t = globaltimer();
+        if (t0 == 0) t0 = t;
+        if (t - t0 > kWaitNs) {
             *(volatile int *)&S.abort = 1;
             set_status(st, MOE_ERR_TIMEOUT);
             return false;
@@ -195,7 +209,8 @@ __device__ __forceinline__ bool waitw(Shared &S, uint64_t *bar, uint32_t parity,
 
 template <int kMode, int kPair>
 __device__ void produce(const TcArgs &a, Shared &S, uint8_t *ring, int tiles, int rank,
-                        const CUtensorMap *w0, const CUtensorMap *w1, const CUtensorMap *x) {
+                        const CUtensorMap *w0, const CUtensorMap *w1, const CUtensorMap *x,
+                        const CUtensorMap *x16) {
     const int lane = threadIdx.x & 31;
     const int mine = tiles_of_cta<kPair>(tiles);
     Pos p;
@@ -205,7 +220,10 @@ __device__ void produce(const TcArgs &a, Shared &S, uint8_t *ring, int tiles, in
     bool ok = true;
     for (int m = 0; ok && m < mine; m++) {
         const Tile t = next;
-        const int npad = kMode == kGateUp ? 0 : max(0, (t.n + 15) & ~15);
+        // more than half a tile of tokens comes as one box of 128 rows (those past the slice, if
+        // they exist, are read and not used): every box costs the copy engine time of its own
+        const bool whole = kMode != kGateUp && t.n > kMT / 2;
+        const int npad = kMode == kGateUp ? 0 : whole ? kMT : max(0, (t.n + 15) & ~15);
         // the next tile's place arrives while this one's blocks are issued
         if (m + 1 < mine)
             next = tile_at<kMode, kPair>(a, first_tile<kPair>() + (m + 1) * tile_step<kPair>(), rank);
@@ -221,14 +239,13 @@ __device__ void produce(const TcArgs &a, Shared &S, uint8_t *ring, int tiles, in
                 const int r0 = kMode == kGateUp ? t.rt * 128 : t.rt * kNW;
                 const int r1 = kMode == kGateUp ? r0 : r0 + 128;
                 if (kPair == 1 || rank == 0) tma_load_3d(st, w0, b * kSBlk, r0, t.e, bar);
-                if (kPair == 1)
-                    tma_load_3d(st + kOperand, w1, b * kSBlk, r1, t.e, bar);
-                else if (rank == 1)
-                    tma_load_3d(st, w1, b * kSBlk, r1, t.e, bar);
+                if (kPair == 1) tma_load_3d(st + kOperand, w1, b * kSBlk, r1, t.e, bar);
+                if (kPair == 2 && rank == 1) tma_load_3d(st, w1, b * kSBlk, r1, t.e, bar);
+                if (whole) tma_load_2d(st + weight_bytes(kPair), x, b * kSBlk, t.slot, bar);
             }
             __syncwarp();
-            if (kMode != kGateUp && 16 * lane < npad)
-                tma_load_2d(st + weight_bytes(kPair) + lane * 16 * kSBlk, x, b * kSBlk,
+            if (!whole && 16 * lane < npad)
+                tma_load_2d(st + weight_bytes(kPair) + lane * 16 * kSBlk, x16, b * kSBlk,
                             t.slot + 16 * lane, bar);
             issued++;
             p.next(stages(kPair));
@@ -246,41 +263,42 @@ __device__ void produce(const TcArgs &a, Shared &S, uint8_t *ring, int tiles, in
     }
 }
 
-// One thread of a single CTA or of a pair's first.
+// The MMA issuer: warp 1 of a single CTA or of a pair's first.  The whole warp walks the loop and
+// one elected lane issues, so that the descriptors stay in uniform registers.
 template <int kMode, int kPair>
 __device__ void multiply(const TcArgs &a, Shared &S, uint8_t *ring, int tiles, uint32_t tmem) {
     constexpr uint32_t idesc = instr_desc(0, kPair * kMT, kNW);
     const int64_t total = (int64_t)tiles_of_cta<kPair>(tiles) * a.nkb;
     Pos p, q;
     for (int64_t i = 0; i < total; i++) {
-        if (!wait1(S, &S.acc_empty[q.s], q.ph ^ 1u, a.status) ||
-            !wait1(S, &S.full[p.s], p.ph, a.status) ||
-            (kPair == 2 && !wait1(S, &S.peer[p.s], p.ph, a.status))) {
-            kPair == 2 ? umma_commit_pair(&S.done) : umma_commit(&S.done);
-            mbar_wait_bounded(&S.done, 0, kWaitNs);
+        if (!waitw(S, &S.full[p.s], p.ph, a.status) ||
+            (kPair == 2 && !waitw(S, &S.peer[p.s], p.ph, a.status)) ||
+            !waitw(S, &S.acc_empty[q.s], q.ph ^ 1u, a.status)) {
+            if (elect_one()) {
+                kPair == 2 ? umma_commit_pair(&S.done) : umma_commit(&S.done);
+                mbar_wait_bounded(&S.done, 0, kWaitNs);
+            }
             return;
         }
         // gathered rows were written by ordinary copies: seen by their arrivals, and made visible
         // to the tensor core here
         if (kMode == kGateUp) fence_proxy_async_smem();
         tc_fence_after();
-        const uint32_t st = smem_u32(ring + (size_t)p.s * stage_bytes(kPair));
-        const uint32_t d = tmem + (uint32_t)(q.s * kNW);
+        const uint32_t st = smem_u32(ring) + (uint32_t)p.s * stage_bytes(kPair);
         const uint64_t x = smem_desc(st + weight_bytes(kPair), 1024, 2), w = smem_desc(st, 1024, 2);
+        const uint32_t d = tmem + (uint32_t)(q.s * kNW);
+        if (elect_one()) {
 #pragma unroll
-        for (int j = 0; j < 4; j++) {        // 32 bytes of k a step: 2 units of 16 bytes
-            if (kPair == 2)
-                umma_f8_pair(d, x + 2 * j, w + 2 * j, idesc, j > 0);
-            else
-                umma_f8(d, x + 2 * j, w + 2 * j, idesc, j > 0);
+            for (int j = 0; j < 4; j++) {        // 32 bytes of k a step: 2 units of 16 bytes
+                if (kPair == 2)
+                    umma_f8_pair(d, x + 2 * j, w + 2 * j, idesc, j > 0);
+                else
+                    umma_f8(d, x + 2 * j, w + 2 * j, idesc, j > 0);
+            }
+            kPair == 2 ? umma_commit_both(&S.acc_full[q.s]) : umma_commit(&S.acc_full[q.s]);
+            kPair == 2 ? umma_commit_both(&S.empty[p.s]) : umma_commit(&S.empty[p.s]);
         }
-        if (kPair == 2) {
-            umma_commit_both(&S.empty[p.s]);
-            umma_commit_both(&S.acc_full[q.s]);
-        } else {
-            umma_commit(&S.empty[p.s]);
-            umma_commit(&S.acc_full[q.s]);
-        }
+        __syncwarp();
         p.next(stages(kPair));
         q.next(kAccs);
     }
@@ -298,35 +316,34 @@ __device__ void announce(const TcArgs &a, Shared &S, int tiles) {
     }
 }
 
-// The scales of one thread's two tokens, in the order the epilogue takes them, and the tokens
-// themselves.
+// Warp 2: the scales of every block, in the order the epilogue takes them, copied into the ring.
 template <int kMode, int kPair>
-struct ScaleStream {
-    struct Set {
-        float v[2], w0, w1;
-    };
-    int m, b, entry[2];
-    Tile t, next;
-    const float *as[2], *s0, *s1;
-
-    __device__ __forceinline__ void look(const TcArgs &a, int row) {
+__device__ void scales(const TcArgs &a, Shared &S, int tiles, int rank) {
+    const int lane = threadIdx.x & 31;
+    const int mine = tiles_of_cta<kPair>(tiles);
+    if (mine == 0) return;
+    Pos p;
+    int u = 0;                              // block within the group
+    int entry[4];
+    Tile next = tile_at<kMode, kPair>(a, first_tile<kPair>(), rank);
+    auto look = [&] {
         if (kMode == kGateUp) {
 #pragma unroll
-            for (int j = 0; j < 2; j++) {
-                const int r = row + 32 * j;
+            for (int j = 0; j < 4; j++) {
+                const int r = lane + 32 * j;
                 entry[j] = r < next.n ? slot_entry(a, next, next.slot + r) : 0;
             }
         }
-    }
-    __device__ __forceinline__ void open(const TcArgs &a, int row) {
-        t = next;
+    };
+    look();
+    for (int m = 0; m < mine; m++) {
+        const Tile t = next;
+        const float *as = a.as + (kMode == kGateUp ? 0 : (int64_t)t.slot + lane);
+        int off[4];
 #pragma unroll
-        for (int j = 0; j < 2; j++) {
-            const int r = row + 32 * j;
-            as[j] = r >= t.n ? nullptr
-                    : a.as + (kMode == kGateUp ? entry_token(a, entry[j]) : t.slot + r);
-        }
-        s0 = a.ws0 + t.e * a.ws_expert;
+        for (int j = 0; j < 4; j++)
+            off[j] = kMode == kGateUp ? entry_token(a, entry[j]) : 32 * j;
+        const float *s0 = a.ws0 + t.e * a.ws_expert, *s1;
         if (kMode == kGateUp) {
             s0 += (int64_t)t.rt * a.nkb;
             s1 = a.ws1 + t.e * a.ws_expert + (int64_t)t.rt * a.nkb;
@@ -334,154 +351,88 @@ struct ScaleStream {
             s0 += (int64_t)(2 * t.rt) * a.nkb;
             s1 = t.rt * kNW + kSBlk < a.rows ? s0 + a.nkb : s0;    // past the last rows: not stored
         }
-    }
-    __device__ __forceinline__ void start(const TcArgs &a, int row, int rank) {
-        m = 0;
-        b = 0;
-        next = tile_at<kMode, kPair>(a, first_tile<kPair>(), rank);
-        look(a, row);
-        open(a, row);
-    }
-    __device__ __forceinline__ void load(const TcArgs &a, int mine, int row, int rank, Set &c) {
-        if (m >= mine) return;
-#pragma unroll
-        for (int j = 0; j < 2; j++) {
-            c.v[j] = 0.f;
-            if (as[j]) {
-                c.v[j] = __ldg(as[j]);
-                as[j] += a.ldas;
-            }
-        }
-        c.w0 = __ldg(s0 + b);
-        c.w1 = __ldg(s1 + b);
-        const bool more = m + 1 < mine;
-        if (b == 0 && more) {
+        const float *mine_ws = lane == 0 ? s0 : s1;
+        // the next tile's entries arrive while this one's scales are copied
+        if (m + 1 < mine) {
             next = tile_at<kMode, kPair>(a, first_tile<kPair>() + (m + 1) * tile_step<kPair>(), rank);
-            look(a, row);
+            look();
         }
-        if (++b == a.nkb) {
-            b = 0;
-            m++;
-            if (more) open(a, row);
-        }
-    }
-};
-
-// Routed token rows of a warp's 64 tokens: eight lanes per row, four rows per step.  The loop
-// stays rolled and the tokens in shared memory: unrolled into the scales' loop it ran at 200
-// clocks a copy, waiting for instructions.
-template <int kPair>
-struct Gather {
-    int m, b, n, entry[2];
-    Pos p;
-
-    // perm's entries of tile m, to be used when it opens
-    __device__ __forceinline__ int look(const TcArgs &a, int first, int rank) {
-        const int lane = threadIdx.x & 31;
-        const Tile t = tile_at<kGateUp, kPair>(a, first_tile<kPair>() + m * tile_step<kPair>(), rank);
-#pragma unroll
-        for (int j = 0; j < 2; j++) {
-            const int r = first + 32 * j + lane;
-            entry[j] = r < t.n ? slot_entry(a, t, t.slot + r) : 0;
-        }
-        return t.n;
-    }
-    int n_next;
-    __device__ __forceinline__ void open(const TcArgs &a, Shared &S, int mine, int first, int rank) {
-        const int lane = threadIdx.x & 31;
-        n = n_next;
-        __syncwarp();
-        S.token[first + lane] = entry_token(a, entry[0]);
-        S.token[first + 32 + lane] = entry_token(a, entry[1]);
-        __syncwarp();
-        if (++m < mine) n_next = look(a, first, rank);
-    }
-    __device__ __forceinline__ void start(const TcArgs &a, Shared &S, int mine, int first, int rank) {
-        m = b = 0;
-        n_next = look(a, first, rank);
-        open(a, S, mine, first, rank);
-    }
-    // issue the next block; false when a wait gave up
-    __device__ __forceinline__ bool step(const TcArgs &a, Shared &S, uint8_t *ring, int mine,
-                                         int first, int rank) {
-        const int lane = threadIdx.x & 31;
-        if (!waitw(S, &S.empty[p.s], p.ph ^ 1u, a.status)) return false;
-        uint8_t *xs = ring + (size_t)p.s * stage_bytes(kPair) + weight_bytes(kPair);
-        const int c = lane & 7, col = b * kSBlk + 16 * c;
-        const bool in = col < a.x_cols;
-        const uint8_t *src = a.xq + (in ? col : 0);
-        const int last = min(n, first + 64);
-#pragma unroll 4
-        for (int r = first + (lane >> 3); r < last; r += 4)
-            cp_async16_if(xs + r * kSBlk + ((c ^ (r & 7)) << 4),
-                          src + (int64_t)S.token[r] * a.x_cols, in);
-        cp_async_arrive(&S.full[p.s]);
-        p.next(stages(kPair));
-        if (++b == a.nkb) {
-            b = 0;
-            if (m < mine) open(a, S, mine, first, rank);
-        }
-        return true;
-    }
-};
-
-template <int kMode, int kPair>
-__device__ void feed(const TcArgs &a, Shared &S, uint8_t *ring, int tiles, int rank, int which) {
-    const int lane = threadIdx.x & 31, row = which * 64 + lane;
-    const int mine = tiles_of_cta<kPair>(tiles);
-    if (mine == 0) return;
-    Gather<kPair> g;
-    if (kMode == kGateUp) g.start(a, S, mine, which * 64, rank);
-    ScaleStream<kMode, kPair> ss;
-    typename ScaleStream<kMode, kPair>::Set c[kAhead];
-    ss.start(a, row, rank);
-#pragma unroll
-    for (int u = 0; u < kAhead; u++) ss.load(a, mine, row, rank, c[u]);
-    const int64_t total = (int64_t)mine * a.nkb;
-    Pos p;
-    for (int64_t b0 = 0; b0 < total; b0 += kAhead) {
-        if (kMode == kGateUp) {
 #pragma unroll 1
-            for (int u = 0; u < kAhead && b0 + u < total; u++) {
-                if (!g.step(a, S, ring, mine, which * 64, rank)) {
-                    cp_async_wait_all();
-                    return;
-                }
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < kAhead; u++) {
-            if (b0 + u >= total) break;
-            if (!waitw(S, &S.sc_empty[p.s], p.ph ^ 1u, a.status)) {
-                if (kMode == kGateUp) cp_async_wait_all();
+        for (int b = 0; b < a.nkb; b++) {
+            if (u == 0 && !waitw(S, &S.sc_empty[p.s], p.ph ^ 1u, a.status)) {
+                cp_async_wait_all();
                 return;
             }
-            S.scale[p.s][row] = make_float2(c[u].v[0] * c[u].w0, c[u].v[0] * c[u].w1);
-            S.scale[p.s][row + 32] = make_float2(c[u].v[1] * c[u].w0, c[u].v[1] * c[u].w1);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&S.sc_full[p.s]);
-            p.next(kScales);
-            ss.load(a, mine, row, rank, c[u]);
+#pragma unroll
+            for (int j = 0; j < 4; j++)
+                if (lane + 32 * j < t.n) cp_async4(&S.as[p.s][u][lane + 32 * j], as + off[j]);
+            if (lane < 2)
+                cp_async4(reinterpret_cast<float *>(&S.ws[p.s][u]) + lane, mine_ws + b);
+            as += a.ldas;
+            if (++u == kGroup) {
+                u = 0;
+                cp_async_arrive(&S.sc_full[p.s]);
+                p.next(kScales);
+            }
+        }
+    }
+    if (u) cp_async_arrive(&S.sc_full[p.s]);
+}
+
+// Warp 3, gate/up: the routed token rows, gathered: eight lanes per row, four rows per step.  The
+// loop stays short and the tokens in shared memory: unrolled, with the tokens in registers, it
+// ran at 200 clocks a copy, waiting for instructions.
+template <int kPair>
+__device__ void gather(const TcArgs &a, Shared &S, uint8_t *ring, int tiles, int rank) {
+    const int lane = threadIdx.x & 31;
+    const int mine = tiles_of_cta<kPair>(tiles);
+    if (mine == 0) return;
+    Pos p;
+    int entry[4];
+    Tile next = tile_at<kGateUp, kPair>(a, first_tile<kPair>(), rank);
+    auto look = [&] {
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            const int r = lane + 32 * j;
+            entry[j] = r < next.n ? slot_entry(a, next, next.slot + r) : 0;
+        }
+    };
+    look();
+    for (int m = 0; m < mine; m++) {
+        const int n = next.n;
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 4; j++) S.token[lane + 32 * j] = entry_token(a, entry[j]);
+        __syncwarp();
+        if (m + 1 < mine) {
+            next = tile_at<kGateUp, kPair>(a, first_tile<kPair>() + (m + 1) * tile_step<kPair>(), rank);
+            look();
+        }
+#pragma unroll 1
+        for (int b = 0; b < a.nkb; b++) {
+            if (!waitw(S, &S.empty[p.s], p.ph ^ 1u, a.status)) {
+                cp_async_wait_all();
+                return;
+            }
+            uint8_t *xs = ring + (size_t)p.s * stage_bytes(kPair) + weight_bytes(kPair);
+            const int c = lane & 7, col = b * kSBlk + 16 * c;
+            const bool in = col < a.x_cols;
+            const uint8_t *src = a.xq + (in ? col : 0);
+#pragma unroll 4
+            for (int r = lane >> 3; r < n; r += 4)
+                cp_async16_if(xs + r * kSBlk + ((c ^ (r & 7)) << 4),
+                              src + (int64_t)S.token[r] * a.x_cols, in);
+            cp_async_arrive(&S.full[p.s]);
+            p.next(stages(kPair));
         }
     }
 }
 
-// Running totals of two columns in one 64-bit register pair.
-__device__ __forceinline__ float2 pair(uint64_t v) {
-    return make_float2(__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32)));
-}
-__device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi) {
-    return (uint64_t)lo | ((uint64_t)hi << 32);
-}
-__device__ __forceinline__ uint64_t pair(float lo, float hi) {
-    return pair(__float_as_uint(lo), __float_as_uint(hi));
-}
-// acc += r * s for 32 columns, two at a time.
-__device__ __forceinline__ void promote32(uint64_t *acc, const uint32_t (&r)[32], uint64_t s) {
+// acc += r * s for 16 columns.  (Packed two-element multiply-adds need the loaded registers in
+// pairs; the moves that pairs them cost more than the halved instruction count gains.)
+__device__ __forceinline__ void promote16(float *acc, const uint32_t (&r)[16], float s) {
 #pragma unroll
-    for (int i = 0; i < 32; i += 2)
-        asm("fma.rn.f32x2 %0, %1, %2, %0;"
-            : "+l"(acc[i / 2]) : "l"(pair(r[i], r[i + 1])), "l"(s));
+    for (int i = 0; i < 16; i++) acc[i] = fmaf(__uint_as_float(r[i]), s, acc[i]);
 }
 
 __device__ __forceinline__ void store32B(void *p, const uint32_t (&v)[8]) {
@@ -499,26 +450,20 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi, __half *) {
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
-// 16 columns (8 pairs) of this lane's row at p, 32-byte aligned.
+// 16 columns of this lane's row at p, 32-byte aligned.
 template <typename T>
-__device__ __forceinline__ void store16(T *p, const uint64_t *acc) {
+__device__ __forceinline__ void store16(T *p, const float *acc) {
     uint32_t v[8];
     if (sizeof(T) == 4) {
 #pragma unroll
         for (int h = 0; h < 2; h++) {
 #pragma unroll
-            for (int i = 0; i < 4; i++) {
-                v[2 * i] = (uint32_t)acc[4 * h + i];
-                v[2 * i + 1] = (uint32_t)(acc[4 * h + i] >> 32);
-            }
+            for (int i = 0; i < 8; i++) v[i] = __float_as_uint(acc[8 * h + i]);
             store32B(p + 8 * h, v);
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; i++) {
-            const float2 f = pair(acc[i]);
-            v[i] = pack2(f.x, f.y, (T *)nullptr);
-        }
+        for (int i = 0; i < 8; i++) v[i] = pack2(acc[2 * i], acc[2 * i + 1], (T *)nullptr);
         store32B(p, v);
     }
 }
@@ -526,10 +471,11 @@ __device__ __forceinline__ void store16(T *p, const uint64_t *acc) {
 template <int kMode, int kPair, typename T>
 __device__ void finish(const TcArgs &a, Shared &S, int tiles, int rank, uint32_t tmem) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int quad = warp & 3, half = (warp - kEpiWarp0) >> 2;
+    const int quad = warp & 3, part = (warp - kEpiWarp0) >> 2;
     const int row = quad * 32 + lane;
-    const uint32_t base = tmem + ((uint32_t)quad << 21) + (uint32_t)(half * 64);  // lane quad * 32
+    const uint32_t base = tmem + ((uint32_t)quad << 21) + (uint32_t)(part * 32);  // lane quad * 32
     Pos q, p;
+    int u = 0;                          // block within the scale ring's group
     uint32_t par = 0;
     const int mine = tiles_of_cta<kPair>(tiles);
     if (mine == 0) return;
@@ -538,27 +484,29 @@ __device__ void finish(const TcArgs &a, Shared &S, int tiles, int rank, uint32_t
         const Tile t = next;
         if (m + 1 < mine)
             next = tile_at<kMode, kPair>(a, first_tile<kPair>() + (m + 1) * tile_step<kPair>(), rank);
-        uint64_t acc[2][32];            // two columns each
+        float acc[2][32];
 #pragma unroll
-        for (int j = 0; j < 32; j++) acc[0][j] = acc[1][j] = 0u;
+        for (int j = 0; j < 32; j++) acc[0][j] = acc[1][j] = 0.f;
         const bool busy = quad * 32 < t.n;
+#pragma unroll 1
         for (int b = 0; b < a.nkb; b++) {
-            if (!waitw(S, &S.sc_full[p.s], p.ph, a.status)) return;
-            const float2 f = S.scale[p.s][row];
+            if (u == 0 && !waitw(S, &S.sc_full[p.s], p.ph, a.status)) return;
+            const float v = S.as[p.s][u][row];
+            const float2 w = S.ws[p.s][u];
             if (!waitw(S, &S.acc_full[q.s], q.ph, a.status)) return;
             if (busy) {
+                const float f[2] = {v * w.x, v * w.y};
                 tc_fence_after();
                 const uint32_t d = base + (uint32_t)(q.s * kNW);
-                const uint64_t s0 = pair(f.x, f.x), s1 = pair(f.y, f.y);
 #pragma unroll
-                for (int j = 0; j < 2; j++) {
-                    uint32_t r0[32], r1[32];
-                    tmem_ld32(d + 32 * j, r0);
-                    tmem_ld32(d + 128 + 32 * j, r1);
-                    tmem_ld_wait(r0);
-                    reg_tie(r1);
-                    promote32(acc[0] + 16 * j, r0, s0);
-                    promote32(acc[1] + 16 * j, r1, s1);
+                for (int o = 0; o < 2; o++) {
+#pragma unroll
+                    for (int j = 0; j < 32; j += 16) {
+                        uint32_t r[16];
+                        tmem_ld16(d + o * 128 + j, r);
+                        tmem_ld_wait(r);
+                        promote16(acc[o] + j, r, f[o]);
+                    }
                 }
                 tc_fence_before();
             }
@@ -568,26 +516,28 @@ __device__ void finish(const TcArgs &a, Shared &S, int tiles, int rank, uint32_t
                     mbar_arrive_at(&S.acc_empty[q.s], 0);
                 else
                     mbar_arrive(&S.acc_empty[q.s]);
-                mbar_arrive(&S.sc_empty[p.s]);
             }
             q.next(kAccs);
-            p.next(kScales);
+            if (++u == kGroup) {
+                u = 0;
+                if (lane == 0) mbar_arrive(&S.sc_empty[p.s]);
+                p.next(kScales);
+            }
         }
         if (!busy) continue;
         if (kMode == kGateUp) {
-            // h, and its e4m3 form per token and 128 ffn values: this thread's 64 and the other
-            // column half's
+            // h, and its e4m3 form per token and 128 ffn values: this thread's 32 and those of the
+            // other three column quarters
             uint32_t mx = 0u;
 #pragma unroll
             for (int j = 0; j < 32; j++) {
-                const float2 g = pair(acc[0][j]), u = pair(acc[1][j]);
-                const float h0 = silu_mul(g.x, u.x), h1 = silu_mul(g.y, u.y);
-                acc[0][j] = pair(h0, h1);
-                mx = max(mx, max(__float_as_uint(h0) & 0x7fffffffu, __float_as_uint(h1) & 0x7fffffffu));
+                acc[0][j] = silu_mul(acc[0][j], acc[1][j]);
+                mx = max(mx, __float_as_uint(acc[0][j]) & 0x7fffffffu);
             }
-            S.amax[par][half][row] = mx;
-            named_barrier(1 + quad, 64);
-            mx = max(mx, S.amax[par][half ^ 1][row]);
+            S.amax[par][part][row] = mx;
+            named_barrier(1 + quad, 128);
+            mx = max(max(S.amax[par][0][row], S.amax[par][1][row]),
+                     max(S.amax[par][2][row], S.amax[par][3][row]));
             par ^= 1u;
             if (row < t.n) {
                 const bool fin = mx < 0x7f800000u;
@@ -596,21 +546,20 @@ __device__ void finish(const TcArgs &a, Shared &S, int tiles, int rank, uint32_t
                 const float pre = sc < 0x1p-100f ? 0x1p100f : 1.0f;
                 const float inv = sc > 0.f ? __frcp_rn(sc * pre) : 0.f;
                 const int64_t slot = (int64_t)t.slot + row;
-                if (half == 0) {
+                if (part == 0) {
                     a.hs[t.rt * a.slots + slot] = sc;
                     if (!fin) set_status(a.status, MOE_ERR_NONFINITE);
                 }
-                const int f = t.rt * 128 + half * 64;
+                const int f = t.rt * 128 + part * 32;
                 uint8_t *hq = a.hq + slot * a.rows + f;
 #pragma unroll
-                for (int j = 0; j < 4; j++) {
+                for (int j = 0; j < 2; j++) {
                     uint32_t v[4];
 #pragma unroll
                     for (int u = 0; u < 4; u++) {
-                        const float2 x = pair(acc[0][8 * j + 2 * u]);
-                        const float2 y = pair(acc[0][8 * j + 2 * u + 1]);
-                        v[u] = cvt_e4m3x2(x.x * pre * inv, x.y * pre * inv) |
-                               (cvt_e4m3x2(y.x * pre * inv, y.y * pre * inv) << 16);
+                        const float *x = acc[0] + 16 * j + 4 * u;
+                        v[u] = cvt_e4m3x2(x[0] * pre * inv, x[1] * pre * inv) |
+                               (cvt_e4m3x2(x[2] * pre * inv, x[3] * pre * inv) << 16);
                         if (!fin) v[u] = 0u;
                     }
                     if (f + 16 * j < a.rows)
@@ -621,32 +570,33 @@ __device__ void finish(const TcArgs &a, Shared &S, int tiles, int rank, uint32_t
             T *out = static_cast<T *>(a.out) + ((int64_t)t.slot + row) * a.ldo;
 #pragma unroll
             for (int u = 0; u < 2; u++) {
-                const int r0 = t.rt * kNW + u * 128 + half * 64;
+                const int r0 = t.rt * kNW + u * 128 + part * 32;
                 if (a.vec) {
                     // 32 bytes of a row per lane and store
 #pragma unroll
-                    for (int j = 0; j < 4; j++)
+                    for (int j = 0; j < 2; j++)
                         if (row < t.n && r0 + 16 * j < a.rows)
-                            store16(out + r0 + 16 * j, acc[u] + 8 * j);
+                            store16(out + r0 + 16 * j, acc[u] + 16 * j);
                 } else {
-                    // rows of any alignment: 16 columns at a time through shared memory, so that
-                    // a warp writes runs of a row
+                    // rows of any alignment: 8 columns at a time through shared memory, so that a
+                    // warp writes runs of a row
                     float (&P)[32][kPatch + 1] = S.patch[warp - kEpiWarp0];
 #pragma unroll
-                    for (int j = 0; j < 4; j++) {
+                    for (int j = 0; j < 32 / kPatch; j++) {
 #pragma unroll
-                        for (int x = 0; x < 8; x++) {
-                            const float2 v = pair(acc[u][8 * j + x]);
-                            P[lane][2 * x] = v.x;
-                            P[lane][2 * x + 1] = v.y;
-                        }
+                        for (int x = 0; x < kPatch; x++) P[lane][x] = acc[u][kPatch * j + x];
                         __syncwarp();
-                        const int col = r0 + 16 * j + (lane & 15);
-                        const int first = quad * 32 + (lane >> 4);
-                        T *o = static_cast<T *>(a.out) + ((int64_t)t.slot + first) * a.ldo + col;
+                        const int col = r0 + kPatch * j + lane % kPatch;
+                        const int first = lane / kPatch;
+                        T *o = static_cast<T *>(a.out) +
+                               ((int64_t)t.slot + quad * 32 + first) * a.ldo + col;
                         if (col < a.rows) {
-                            for (int y = 0; y < 16 && first + 2 * y < t.n; y++, o += 2 * a.ldo)
-                                *o = from_f32<T>(P[(lane >> 4) + 2 * y][lane & 15]);
+#pragma unroll
+                            for (int y = 0; y < 32; y += 32 / kPatch) {
+                                if (quad * 32 + first + y < t.n)
+                                    *o = from_f32<T>(P[first + y][lane % kPatch]);
+                                o += (32 / kPatch) * a.ldo;
+                            }
                         }
                         __syncwarp();
                     }
@@ -659,7 +609,8 @@ __device__ void finish(const TcArgs &a, Shared &S, int tiles, int rank, uint32_t
 template <int kMode, int kPair, typename T>
 __global__ void __launch_bounds__(kThreads, 1)
     k_scaled_tc(const TcArgs a, const __grid_constant__ CUtensorMap w0,
-                const __grid_constant__ CUtensorMap w1, const __grid_constant__ CUtensorMap x) {
+                const __grid_constant__ CUtensorMap w1, const __grid_constant__ CUtensorMap x,
+                const __grid_constant__ CUtensorMap x16) {
     extern __shared__ uint8_t raw[];
     // the same offset in both CTAs of a pair: dynamic shared memory starts at one address
     uint8_t *ring = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
@@ -668,7 +619,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int rank = kPair == 2 ? (int)cluster_rank() : 0;
     if (threadIdx.x == 0) {
         for (int i = 0; i < stages(kPair); i++) {
-            mbar_init(&S.full[i], kMode == kGateUp ? 1 + 64 : 1);   // the gathering threads
+            mbar_init(&S.full[i], kMode == kGateUp ? 1 + 32 : 1);   // and the gathering threads
             mbar_init(&S.empty[i], 1);
             mbar_init(&S.peer[i], 1);
         }
@@ -677,7 +628,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&S.acc_empty[i], kPair * kEpiWarps);
         }
         for (int i = 0; i < kScales; i++) {
-            mbar_init(&S.sc_full[i], 2);
+            mbar_init(&S.sc_full[i], 32);
             mbar_init(&S.sc_empty[i], kEpiWarps);
         }
         mbar_init(&S.done, 1);
@@ -703,16 +654,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp < kEpiWarp0) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRoleRegs));
         if (warp == 0) {
-            produce<kMode, kPair>(a, S, ring, tiles, rank, &w0, &w1, &x);
+            produce<kMode, kPair>(a, S, ring, tiles, rank, &w0, &w1, &x, &x16);
         } else if (warp == 1) {
-            if ((threadIdx.x & 31) == 0) {
-                if (rank == 0)
-                    multiply<kMode, kPair>(a, S, ring, tiles, tmem);
-                else
-                    announce(a, S, tiles);
-            }
-        } else {
-            feed<kMode, kPair>(a, S, ring, tiles, rank, warp - 2);
+            if (rank == 0)
+                multiply<kMode, kPair>(a, S, ring, tiles, tmem);
+            else if ((threadIdx.x & 31) == 0)
+                announce(a, S, tiles);
+        } else if (warp == 2) {
+            scales<kMode, kPair>(a, S, tiles, rank);
+        } else if (kMode == kGateUp) {
+            gather<kPair>(a, S, ring, tiles, rank);
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
@@ -821,7 +772,8 @@ bool encode(CUtensorMap *m, const void *base, int cols, int64_t rows, int64_t st
 
 template <int kMode, int kPair, typename T>
 cudaError_t run_tc(const TcArgs &a, const CUtensorMap &w0, const CUtensorMap &w1,
-                   const CUtensorMap &x, int64_t most_tiles, cudaStream_t st) {
+                   const CUtensorMap &x, const CUtensorMap &x16, int64_t most_tiles,
+                   cudaStream_t st) {
     auto kernel = k_scaled_tc<kMode, kPair, T>;
     // the register split needs every register of the launch it was made for
     static const bool fits = [&] {
@@ -844,7 +796,7 @@ cudaError_t run_tc(const TcArgs &a, const CUtensorMap &w0, const CUtensorMap &w1
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = kPair == 2 ? 1 : 0;
-    err = cudaLaunchKernelEx(&cfg, kernel, a, w0, w1, x);
+    err = cudaLaunchKernelEx(&cfg, kernel, a, w0, w1, x, x16);
     if (err != cudaSuccess) return err;
     note_launches(1);
     return cudaGetLastError();
@@ -853,9 +805,10 @@ cudaError_t run_tc(const TcArgs &a, const CUtensorMap &w0, const CUtensorMap &w1
 // Pairs of CTAs or single ones.
 template <int kMode, typename T>
 cudaError_t run_tc(bool pair, const TcArgs &a, const CUtensorMap &w0, const CUtensorMap &w1,
-                   const CUtensorMap &x, int64_t most_tiles, cudaStream_t st) {
-    return pair ? run_tc<kMode, 2, T>(a, w0, w1, x, most_tiles, st)
-                : run_tc<kMode, 1, T>(a, w0, w1, x, most_tiles, st);
+                   const CUtensorMap &x, const CUtensorMap &x16, int64_t most_tiles,
+                   cudaStream_t st) {
+    return pair ? run_tc<kMode, 2, T>(a, w0, w1, x, x16, most_tiles, st)
+                : run_tc<kMode, 1, T>(a, w0, w1, x, x16, most_tiles, st);
 }
 
 size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
@@ -889,7 +842,7 @@ ExpertsWs experts_ws(const moe_scaled_weights &w, int T, int k) {
 
 bool use_pair(int M) { return M > kMT; }
 bool use_pair_experts(const moe_scaled_weights &w, int T, int k) {
-    return (int64_t)T * k > (int64_t)kMT * w.n_experts;
+    return (int64_t)T * k > 4 * (int64_t)kMT * w.n_experts;
 }
 
 cudaError_t experts_tc(const ScaledExpertsArgs &e, uint8_t *ws, cudaStream_t st) {
@@ -899,12 +852,13 @@ cudaError_t experts_tc(const ScaledExpertsArgs &e, uint8_t *ws, cudaStream_t st)
     Job *slices = reinterpret_cast<Job *>(ws + L.slices);
     int32_t *nslices = reinterpret_cast<int32_t *>(ws + L.nslices);
     float *xs = reinterpret_cast<float *>(ws + L.xs);
-    CUtensorMap gate, up, down, h;
+    CUtensorMap gate, up, down, h, h16;
+    const bool pair = use_pair_experts(w, e.T, e.k);
     if (!encode(&gate, w.d_gate, H, F, H, n, 128) || !encode(&up, w.d_up, H, F, H, n, 128) ||
         !encode(&down, w.d_down, F, H, F, n, 128) ||
-        !encode(&h, ws + L.hq, F, L.slots, F, 0, 16))
+        !encode(&h, ws + L.hq, F, L.slots, F, 0, 128) ||
+        !encode(&h16, ws + L.hq, F, L.slots, F, 0, 16))
         return cudaErrorInvalidValue;
-    const bool pair = use_pair_experts(w, e.T, e.k);
     k_scaled_slices<<<1, 1024, 0, st>>>(e.offsets, w.n_experts, e.T, e.k, w.shared,
                                         pair ? 2 * kMT : kMT, slices, nslices, e.status);
     note_launches(1);
@@ -932,7 +886,7 @@ cudaError_t experts_tc(const ScaledExpertsArgs &e, uint8_t *ws, cudaStream_t st)
     a.ws0 = w.d_gate_s;
     a.ws1 = w.d_up_s;
     a.ws_expert = (int64_t)sblocks(F) * sblocks(H);
-    err = run_tc<kGateUp, float>(pair, a, gate, up, h, L.most_slices * a.row_tiles, st);
+    err = run_tc<kGateUp, float>(pair, a, gate, up, h, h16, L.most_slices * a.row_tiles, st);
     if (err != cudaSuccess) return err;
     a.nkb = sblocks(F);
     a.rows = H;
@@ -943,7 +897,7 @@ cudaError_t experts_tc(const ScaledExpertsArgs &e, uint8_t *ws, cudaStream_t st)
     a.out = ws + L.y;
     a.ldo = H;
     a.vec = true;
-    err = run_tc<kDown, float>(pair, a, down, down, h, L.most_slices * a.row_tiles, st);
+    err = run_tc<kDown, float>(pair, a, down, down, h, h16, L.most_slices * a.row_tiles, st);
     if (err != cudaSuccess) return err;
     return with_dtype(e.out_dt, [&](auto *tag) {
         using E = std::remove_pointer_t<decltype(tag)>;
@@ -957,8 +911,10 @@ cudaError_t experts_tc(const ScaledExpertsArgs &e, uint8_t *ws, cudaStream_t st)
 }
 
 cudaError_t matmul_tc(const ScaledMatmulArgs &m, cudaStream_t st) {
-    CUtensorMap b, x;
-    if (!encode(&b, m.b, m.K, m.N, m.ldb, 1, 128) || !encode(&x, m.a, m.K, m.M, m.lda, 0, 16))
+    CUtensorMap b, x, x16;
+    const bool pair = use_pair(m.M);
+    if (!encode(&b, m.b, m.K, m.N, m.ldb, 1, 128) || !encode(&x, m.a, m.K, m.M, m.lda, 0, 128) ||
+        !encode(&x16, m.a, m.K, m.M, m.lda, 0, 16))
         return cudaErrorInvalidValue;
     TcArgs a{};
     a.nkb = sblocks(m.K);
@@ -972,13 +928,12 @@ cudaError_t matmul_tc(const ScaledMatmulArgs &m, cudaStream_t st) {
     a.ldo = m.ldo;
     a.vec = (uintptr_t)m.out % 32 == 0 && m.ldo * dtype_bytes(m.dt) % 32 == 0 && m.N % 16 == 0;
     a.status = m.status;
-    const bool pair = use_pair(m.M);
     const int slice = pair ? 2 * kMT : kMT;
     const int64_t tiles = (int64_t)((m.M + slice - 1) / slice) * a.row_tiles;
     if (tiles > INT32_MAX) return cudaErrorInvalidValue;
     return with_dtype(m.dt, [&](auto *tag) {
         using E = std::remove_pointer_t<decltype(tag)>;
-        return run_tc<kDense, E>(pair, a, b, b, x, tiles, st);
+        return run_tc<kDense, E>(pair, a, b, b, x, x16, tiles, st);
     });
 }
 
