@@ -10,20 +10,37 @@ namespace moe {
 namespace {
 
 constexpr int kRows = 4;       // rows per warp
+constexpr int kThreads = 256;
+
+// Where the bytes and scales of row t go: row t itself, or every slot of token t.
+struct Rows {
+    uint8_t *q;
+    int64_t ldq;
+    float *s;
+    int64_t lds;
+    __device__ __forceinline__ int count() const { return 1; }
+    __device__ __forceinline__ int64_t row(int64_t t, int, uint32_t *) const { return t; }
+};
+struct Slots {
+    uint8_t *q;
+    int64_t ldq;
+    float *s;
+    int64_t lds;
+    const int32_t *inv_perm;
+    int k, routed, shared;
+    __device__ __forceinline__ int count() const { return k + shared; }
+    __device__ __forceinline__ int64_t row(int64_t t, int j, uint32_t *status) const {
+        if (j == k) return routed + t;
+        const int p = __ldg(inv_perm + t * k + j);
+        if (p >= 0 && p < routed) return p;
+        set_status(status, MOE_ERR_BOUNDS);
+        return -1;
+    }
+};
 
 template <typename T, bool kVec>
-__global__ void __launch_bounds__(256)
-    k_scaled_quantize(const T *__restrict__ x, int rows, int K, int64_t ldx, uint8_t *__restrict__ q,
-                      int64_t ldq, float *__restrict__ s, int64_t lds, uint32_t *status) {
-    const int lane = threadIdx.x & 31;
-    const int nb = sblocks(K);
-    const int64_t unit = (int64_t)blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5);
-    const int64_t rt = unit / nb;
-    const int b = (int)(unit - rt * nb);
-    const int64_t t0 = rt * kRows;
-    if (t0 >= rows) return;
-    const int c = b * kSBlk + lane * 4;
-    float4 v[kRows];
+__device__ __forceinline__ void load_rows(const T *x, int64_t t0, int c, int rows, int K,
+                                          int64_t ldx, float4 (&v)[kRows]) {
 #pragma unroll
     for (int i = 0; i < kRows; i++) {
         v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -38,26 +55,79 @@ __global__ void __launch_bounds__(256)
             if (c + 3 < K) v[i].w = to_f32(p[3]);
         }
     }
-    float mine = 0.f;
-    bool bad = false;
+}
+
+template <typename T, bool kVec, typename To>
+__global__ void __launch_bounds__(kThreads)
+    k_scaled_quantize(const T *__restrict__ x, int rows, int K, int64_t ldx, const To to,
+                      uint32_t *status) {
+    const int lane = threadIdx.x & 31;
+    const int nb = sblocks(K);
+    const int64_t unit = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+    const int64_t rt = unit / nb;
+    const int b = (int)(unit - rt * nb);
+    const int64_t t0 = rt * kRows;
+    if (t0 >= rows) return;
+    const int c = b * kSBlk + lane * 4;
+    float4 v[kRows];
+    load_rows<T, kVec>(x, t0, c, rows, K, ldx, v);
+    // the largest magnitudes as integers (a NaN or an infinity has the largest bit patterns);
+    // lane i takes row i's scale and reciprocal, one division for the four
+    uint32_t top = 0;
 #pragma unroll
     for (int i = 0; i < kRows; i++) {
-        float sc;
-        bool fin;
-        const uint32_t p = quant_block(v[i], &sc, &fin);
-        if (lane == i) mine = sc;
-        bad = bad || !fin;
-        if (t0 + i >= rows) continue;
-        uint8_t *o = q + (t0 + i) * ldq + c;
-        if (c + 3 < K) {
-            *reinterpret_cast<uint32_t *>(o) = p;
-        } else {
-            for (int j = 0; j < 3; j++)
-                if (c + j < K) o[j] = (uint8_t)(p >> (8 * j));
+        const uint32_t m = __reduce_max_sync(0xffffffffu, abs_bits(v[i]));
+        if (lane == i) top = m;
+    }
+    const bool bad = top >= 0x7f800000u;
+    const float sc = bad ? 0.f : __fdiv_rn(__uint_as_float(top), kE4M3Max);
+    const float inv = sc > 0.f ? __frcp_rn(sc) : 0.f;
+    if (bad) set_status(status, MOE_ERR_NONFINITE);
+    uint32_t p[kRows];
+#pragma unroll
+    for (int i = 0; i < kRows; i++) {
+        const float s = __shfl_sync(0xffffffffu, sc, i), r = __shfl_sync(0xffffffffu, inv, i);
+        p[i] = s > 0.f ? quant4(v[i], s, r) : 0u;
+    }
+    for (int j = 0; j < to.count(); j++) {
+        int64_t at = -1;
+        if (lane < kRows && t0 + lane < rows) {
+            at = to.row(t0 + lane, j, status);
+            if (at >= 0) to.s[b * to.lds + at] = sc;
+        }
+#pragma unroll
+        for (int i = 0; i < kRows; i++) {
+            const int64_t r = __shfl_sync(0xffffffffu, at, i);
+            if (r < 0) continue;
+            uint8_t *o = to.q + r * to.ldq + c;
+            if (c + 3 < K) {
+                *reinterpret_cast<uint32_t *>(o) = p[i];
+            } else {
+                for (int n = 0; n < 3; n++)
+                    if (c + n < K) o[n] = (uint8_t)(p[i] >> (8 * n));
+            }
         }
     }
-    if (lane < kRows && t0 + lane < rows) s[b * lds + t0 + lane] = mine;
-    if (bad && lane == 0) set_status(status, MOE_ERR_NONFINITE);
+}
+
+template <typename To>
+cudaError_t run(const void *x, int dt, int T, int K, int64_t ldx, const To &to, uint32_t *status,
+                cudaStream_t st) {
+    if (T <= 0) return cudaSuccess;
+    const int64_t units = (int64_t)((T + kRows - 1) / kRows) * sblocks(K);
+    const unsigned grid = (unsigned)((units + kThreads / 32 - 1) / (kThreads / 32));
+    return with_dtype(dt, [&](auto *tag) {
+        using E = std::remove_pointer_t<decltype(tag)>;
+        const E *p = static_cast<const E *>(x);
+        // vector loads where every lane's four elements start on their natural boundary
+        const bool vec = ((uintptr_t)x % (4 * sizeof(E))) == 0 && ldx % 4 == 0 && K % 4 == 0;
+        if (vec)
+            k_scaled_quantize<E, true, To><<<grid, kThreads, 0, st>>>(p, T, K, ldx, to, status);
+        else
+            k_scaled_quantize<E, false, To><<<grid, kThreads, 0, st>>>(p, T, K, ldx, to, status);
+        note_launches(1);
+        return cudaGetLastError();
+    });
 }
 
 }  // namespace
@@ -65,21 +135,14 @@ __global__ void __launch_bounds__(256)
 cudaError_t launch_scaled_quantize(const void *x, int dt, int T, int K, int64_t ldx, uint8_t *q,
                                    int64_t ldq, float *s, int64_t lds, uint32_t *status,
                                    cudaStream_t st) {
-    if (T <= 0) return cudaSuccess;
-    const int64_t units = (int64_t)((T + kRows - 1) / kRows) * sblocks(K);
-    const unsigned grid = (unsigned)((units + 7) / 8);
-    return with_dtype(dt, [&](auto *tag) {
-        using E = std::remove_pointer_t<decltype(tag)>;
-        const E *p = static_cast<const E *>(x);
-        // vector loads where every lane's four elements start on their natural boundary
-        const bool vec = ((uintptr_t)x % (4 * sizeof(E))) == 0 && ldx % 4 == 0 && K % 4 == 0;
-        if (vec)
-            k_scaled_quantize<E, true><<<grid, 256, 0, st>>>(p, T, K, ldx, q, ldq, s, lds, status);
-        else
-            k_scaled_quantize<E, false><<<grid, 256, 0, st>>>(p, T, K, ldx, q, ldq, s, lds, status);
-        note_launches(1);
-        return cudaGetLastError();
-    });
+    return run(x, dt, T, K, ldx, Rows{q, ldq, s, lds}, status, st);
+}
+
+cudaError_t launch_scaled_spread(const ScaledExpertsArgs &e, uint8_t *q, float *s, cudaStream_t st) {
+    const int A = e.T * e.k;
+    const Slots to{q, e.w.hidden, s, (int64_t)A + (e.w.shared ? e.T : 0), e.inv_perm, e.k, A,
+                   e.w.shared};
+    return run(e.x, e.x_dt, e.T, e.w.hidden, e.w.hidden, to, e.status, st);
 }
 
 }  // namespace moe

@@ -25,13 +25,17 @@
 //   warp 1        tensor-memory allocation and the MMA issuer; in the second CTA of a pair it
 //                 passes "stage full" on to the first
 //   warp 2        the scales of every block, copied into a ring four blocks a hand-over
-//   warp 3        gate/up: the routed token rows, gathered with 16-byte cp.async (a TMA gather of
-//                 four rows costs about 70 clocks, 32 of them a block)
 //   warps 4-19    epilogue: lane quarter (warp % 4), 32 columns of each 128-row operand.  Four warps
 //                 a scheduler, because a block is a chain of hand-overs and tensor-memory loads
 //                 that one warp cannot hide: with two, a block took 1250 clocks, 300 of them work
 // Every hand-off is an mbarrier and every wait is bounded (MOE_ERR_TIMEOUT in the status word).
+//
+// The experts' layer quantises x straight into slot order, once per routed expert, so that every
+// tile's token rows are neighbours.  Gathering them in this kernel cost more: a TMA gather of
+// four rows takes about 70 clocks and a block needs 32, and one warp's 16-byte cp.async copies
+// took 1.4 us a block where the loads of neighbouring rows take 0.5 us.
 #include <algorithm>
+#include <cmath>
 
 #include "route_dev.cuh"
 #include "scaled.cuh"
@@ -77,10 +81,6 @@ struct TcArgs {
     int M;                       // dense: rows of a
     const Job *slices;           // experts: runs of up to 128 slots (k_scaled_slices)
     const int32_t *nslices;
-    const int32_t *perm;
-    const uint8_t *xq;           // gate/up: the token rows [T][x_cols]
-    int x_cols;
-    int k, routed;               // routed = T * k
     const float *as;
     int64_t ldas;
     const float *ws0, *ws1;      // weight scales [expert][row blocks][nkb]; ws1: up
@@ -88,6 +88,8 @@ struct TcArgs {
     uint8_t *hq;                 // gate/up: [slots][rows] and scales [row blocks][slots]
     float *hs;
     int64_t slots;
+    float *ys;                   // down to fp16: powers of two [slots][row blocks]
+    int y_exp;                   // and the exponent that keeps a sum of nkb blocks finite
     void *out;
     int64_t ldo;
     bool vec;                    // out rows are 32-byte aligned and rows a multiple of 16
@@ -96,7 +98,6 @@ struct TcArgs {
 
 struct Tile {
     int e, rt, slot, n;
-    bool shared;
 };
 
 // Tile i as CTA `rank` of its kPair CTAs sees it (its own 128 tokens; n may be 0 or less in the
@@ -117,13 +118,11 @@ __device__ __forceinline__ Tile tile_at(const TcArgs &a, int i, int rank) {
         t.e = 0;
         t.slot = s * (kPair * kMT);
         t.n = min(kPair * kMT, a.M - t.slot);
-        t.shared = false;
     } else {
         const int4 v = __ldg(reinterpret_cast<const int4 *>(a.slices) + s);
         t.e = v.x;
         t.slot = v.y;
         t.n = v.z;
-        t.shared = v.w != 0;
     }
     t.slot += rank * kMT;
     t.n = min(kMT, t.n - rank * kMT);
@@ -145,25 +144,11 @@ __device__ __forceinline__ float silu_mul(float g, float u) {
     return __fdividef(g, 1.0f + expf(-g)) * u;
 }
 
-// The row of x that a slot reads is its entry of perm over k; the shared expert's slots follow
-// the routed ones in token order.  The entry is loaded ahead of its use.
-__device__ __forceinline__ int slot_entry(const TcArgs &a, const Tile &t, int s) {
-    return t.shared ? (s - a.routed) * a.k : __ldg(a.perm + s);
-}
-__device__ __forceinline__ int entry_token(const TcArgs &a, int p) {
-    if (p < 0 || p >= a.routed) {
-        set_status(a.status, MOE_ERR_BOUNDS);
-        return 0;
-    }
-    return p / a.k;
-}
-
 struct Shared {
     uint64_t full[kMaxStages], empty[kMaxStages], peer[kMaxStages], acc_full[kAccs],
         acc_empty[kAccs], sc_full[kScales], sc_empty[kScales], done;
     uint32_t tmem;
     int abort;
-    int token[kMT];                       // gate/up: the tile's token rows
     float as[kScales][kGroup][kMT];       // per block: the tokens' scales
     float2 ws[kScales][kGroup];           // and the two operands' weight scales
     uint32_t amax[2][4][kMT];             // gate/up: by tile parity and column quarter, per token
@@ -222,8 +207,8 @@ __device__ void produce(const TcArgs &a, Shared &S, uint8_t *ring, int tiles, in
         const Tile t = next;
         // more than half a tile of tokens comes as one box of 128 rows (those past the slice, if
         // they exist, are read and not used): every box costs the copy engine time of its own
-        const bool whole = kMode != kGateUp && t.n > kMT / 2;
-        const int npad = kMode == kGateUp ? 0 : whole ? kMT : max(0, (t.n + 15) & ~15);
+        const bool whole = t.n > kMT / 2;
+        const int npad = whole ? kMT : max(0, (t.n + 15) & ~15);
         // the next tile's place arrives while this one's blocks are issued
         if (m + 1 < mine)
             next = tile_at<kMode, kPair>(a, first_tile<kPair>() + (m + 1) * tile_step<kPair>(), rank);
@@ -265,7 +250,7 @@ __device__ void produce(const TcArgs &a, Shared &S, uint8_t *ring, int tiles, in
 
 // The MMA issuer: warp 1 of a single CTA or of a pair's first.  The whole warp walks the loop and
 // one elected lane issues, so that the descriptors stay in uniform registers.
-template <int kMode, int kPair>
+template <int kPair>
 __device__ void multiply(const TcArgs &a, Shared &S, uint8_t *ring, int tiles, uint32_t tmem) {
     constexpr uint32_t idesc = instr_desc(0, kPair * kMT, kNW);
     const int64_t total = (int64_t)tiles_of_cta<kPair>(tiles) * a.nkb;
@@ -280,9 +265,6 @@ __device__ void multiply(const TcArgs &a, Shared &S, uint8_t *ring, int tiles, u
             }
             return;
         }
-        // gathered rows were written by ordinary copies: seen by their arrivals, and made visible
-        // to the tensor core here
-        if (kMode == kGateUp) fence_proxy_async_smem();
         tc_fence_after();
         const uint32_t st = smem_u32(ring) + (uint32_t)p.s * stage_bytes(kPair);
         const uint64_t x = smem_desc(st + weight_bytes(kPair), 1024, 2), w = smem_desc(st, 1024, 2);
@@ -324,25 +306,10 @@ __device__ void scales(const TcArgs &a, Shared &S, int tiles, int rank) {
     if (mine == 0) return;
     Pos p;
     int u = 0;                              // block within the group
-    int entry[4];
     Tile next = tile_at<kMode, kPair>(a, first_tile<kPair>(), rank);
-    auto look = [&] {
-        if (kMode == kGateUp) {
-#pragma unroll
-            for (int j = 0; j < 4; j++) {
-                const int r = lane + 32 * j;
-                entry[j] = r < next.n ? slot_entry(a, next, next.slot + r) : 0;
-            }
-        }
-    };
-    look();
     for (int m = 0; m < mine; m++) {
         const Tile t = next;
-        const float *as = a.as + (kMode == kGateUp ? 0 : (int64_t)t.slot + lane);
-        int off[4];
-#pragma unroll
-        for (int j = 0; j < 4; j++)
-            off[j] = kMode == kGateUp ? entry_token(a, entry[j]) : 32 * j;
+        const float *as = a.as + t.slot + lane;
         const float *s0 = a.ws0 + t.e * a.ws_expert, *s1;
         if (kMode == kGateUp) {
             s0 += (int64_t)t.rt * a.nkb;
@@ -352,11 +319,8 @@ __device__ void scales(const TcArgs &a, Shared &S, int tiles, int rank) {
             s1 = t.rt * kNW + kSBlk < a.rows ? s0 + a.nkb : s0;    // past the last rows: not stored
         }
         const float *mine_ws = lane == 0 ? s0 : s1;
-        // the next tile's entries arrive while this one's scales are copied
-        if (m + 1 < mine) {
+        if (m + 1 < mine)
             next = tile_at<kMode, kPair>(a, first_tile<kPair>() + (m + 1) * tile_step<kPair>(), rank);
-            look();
-        }
 #pragma unroll 1
         for (int b = 0; b < a.nkb; b++) {
             if (u == 0 && !waitw(S, &S.sc_empty[p.s], p.ph ^ 1u, a.status)) {
@@ -365,7 +329,7 @@ __device__ void scales(const TcArgs &a, Shared &S, int tiles, int rank) {
             }
 #pragma unroll
             for (int j = 0; j < 4; j++)
-                if (lane + 32 * j < t.n) cp_async4(&S.as[p.s][u][lane + 32 * j], as + off[j]);
+                if (lane + 32 * j < t.n) cp_async4(&S.as[p.s][u][lane + 32 * j], as + 32 * j);
             if (lane < 2)
                 cp_async4(reinterpret_cast<float *>(&S.ws[p.s][u]) + lane, mine_ws + b);
             as += a.ldas;
@@ -377,55 +341,6 @@ __device__ void scales(const TcArgs &a, Shared &S, int tiles, int rank) {
         }
     }
     if (u) cp_async_arrive(&S.sc_full[p.s]);
-}
-
-// Warp 3, gate/up: the routed token rows, gathered: eight lanes per row, four rows per step.  The
-// loop stays short and the tokens in shared memory: unrolled, with the tokens in registers, it
-// ran at 200 clocks a copy, waiting for instructions.
-template <int kPair>
-__device__ void gather(const TcArgs &a, Shared &S, uint8_t *ring, int tiles, int rank) {
-    const int lane = threadIdx.x & 31;
-    const int mine = tiles_of_cta<kPair>(tiles);
-    if (mine == 0) return;
-    Pos p;
-    int entry[4];
-    Tile next = tile_at<kGateUp, kPair>(a, first_tile<kPair>(), rank);
-    auto look = [&] {
-#pragma unroll
-        for (int j = 0; j < 4; j++) {
-            const int r = lane + 32 * j;
-            entry[j] = r < next.n ? slot_entry(a, next, next.slot + r) : 0;
-        }
-    };
-    look();
-    for (int m = 0; m < mine; m++) {
-        const int n = next.n;
-        __syncwarp();
-#pragma unroll
-        for (int j = 0; j < 4; j++) S.token[lane + 32 * j] = entry_token(a, entry[j]);
-        __syncwarp();
-        if (m + 1 < mine) {
-            next = tile_at<kGateUp, kPair>(a, first_tile<kPair>() + (m + 1) * tile_step<kPair>(), rank);
-            look();
-        }
-#pragma unroll 1
-        for (int b = 0; b < a.nkb; b++) {
-            if (!waitw(S, &S.empty[p.s], p.ph ^ 1u, a.status)) {
-                cp_async_wait_all();
-                return;
-            }
-            uint8_t *xs = ring + (size_t)p.s * stage_bytes(kPair) + weight_bytes(kPair);
-            const int c = lane & 7, col = b * kSBlk + 16 * c;
-            const bool in = col < a.x_cols;
-            const uint8_t *src = a.xq + (in ? col : 0);
-#pragma unroll 4
-            for (int r = lane >> 3; r < n; r += 4)
-                cp_async16_if(xs + r * kSBlk + ((c ^ (r & 7)) << 4),
-                              src + (int64_t)S.token[r] * a.x_cols, in);
-            cp_async_arrive(&S.full[p.s]);
-            p.next(stages(kPair));
-        }
-    }
 }
 
 // acc += r * s for 16 columns.  (Packed two-element multiply-adds need the loaded registers in
@@ -473,6 +388,7 @@ __device__ void finish(const TcArgs &a, Shared &S, int tiles, int rank, uint32_t
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int quad = warp & 3, part = (warp - kEpiWarp0) >> 2;
     const int row = quad * 32 + lane;
+    constexpr bool kHalfY = kMode == kDown && sizeof(T) == 2;
     const uint32_t base = tmem + ((uint32_t)quad << 21) + (uint32_t)(part * 32);  // lane quad * 32
     Pos q, p;
     int u = 0;                          // block within the scale ring's group
@@ -488,6 +404,7 @@ __device__ void finish(const TcArgs &a, Shared &S, int tiles, int rank, uint32_t
 #pragma unroll
         for (int j = 0; j < 32; j++) acc[0][j] = acc[1][j] = 0.f;
         const bool busy = quad * 32 < t.n;
+        float top[2] = {0.f, 0.f};           // the largest scale of each operand's blocks
 #pragma unroll 1
         for (int b = 0; b < a.nkb; b++) {
             if (u == 0 && !waitw(S, &S.sc_full[p.s], p.ph, a.status)) return;
@@ -496,6 +413,10 @@ __device__ void finish(const TcArgs &a, Shared &S, int tiles, int rank, uint32_t
             if (!waitw(S, &S.acc_full[q.s], q.ph, a.status)) return;
             if (busy) {
                 const float f[2] = {v * w.x, v * w.y};
+                if (kHalfY) {
+                    top[0] = fmaxf(top[0], fabsf(f[0]));
+                    top[1] = fmaxf(top[1], fabsf(f[1]));
+                }
                 tc_fence_after();
                 const uint32_t d = base + (uint32_t)(q.s * kNW);
 #pragma unroll
@@ -571,6 +492,19 @@ __device__ void finish(const TcArgs &a, Shared &S, int tiles, int rank, uint32_t
 #pragma unroll
             for (int u = 0; u < 2; u++) {
                 const int r0 = t.rt * kNW + u * 128 + part * 32;
+                if (kHalfY) {
+                    // y as fp16 times a power of two per token and 128 rows: a block's sum is at
+                    // most 128 * 448^2 times its scale, so the power follows from the largest
+                    // scale, the same in every column part
+                    const int e = (int)(__float_as_uint(top[u]) >> 23) - 126 + a.y_exp;
+                    const int x = min(max(e, -126), 126);
+                    const float inv = __uint_as_float((uint32_t)(127 - x) << 23);
+                    if (part == 0 && row < t.n && r0 < a.rows)
+                        a.ys[((int64_t)t.slot + row) * ((a.rows + 127) / 128) + 2 * t.rt + u] =
+                            __uint_as_float((uint32_t)(127 + x) << 23);
+#pragma unroll
+                    for (int j = 0; j < 32; j++) acc[u][j] *= inv;
+                }
                 if (a.vec) {
                     // 32 bytes of a row per lane and store
 #pragma unroll
@@ -619,7 +553,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int rank = kPair == 2 ? (int)cluster_rank() : 0;
     if (threadIdx.x == 0) {
         for (int i = 0; i < stages(kPair); i++) {
-            mbar_init(&S.full[i], kMode == kGateUp ? 1 + 32 : 1);   // and the gathering threads
+            mbar_init(&S.full[i], 1);
             mbar_init(&S.empty[i], 1);
             mbar_init(&S.peer[i], 1);
         }
@@ -657,13 +591,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             produce<kMode, kPair>(a, S, ring, tiles, rank, &w0, &w1, &x, &x16);
         } else if (warp == 1) {
             if (rank == 0)
-                multiply<kMode, kPair>(a, S, ring, tiles, tmem);
+                multiply<kPair>(a, S, ring, tiles, tmem);
             else if ((threadIdx.x & 31) == 0)
                 announce(a, S, tiles);
         } else if (warp == 2) {
             scales<kMode, kPair>(a, S, tiles, rank);
-        } else if (kMode == kGateUp) {
-            gather<kPair>(a, S, ring, tiles, rank);
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
@@ -713,44 +645,82 @@ __global__ void __launch_bounds__(1024)
     if (threadIdx.x == 0) *nslices = n + ns;
 }
 
-// out[t] = sum_j w[t][j] y[slot of (t, j)] (+ gate[t] y[routed + t]): one CTA per token.
-template <typename T>
+// Eight values of y at column 8 c of a slot's row, with their power of two when y is fp16.
+__device__ __forceinline__ void load_y(const float *y, const float *, int64_t slot, int H, int c,
+                                       float (&v)[8]) {
+    const float4 *p = reinterpret_cast<const float4 *>(y + slot * H) + 2 * c;
+    const float4 a = __ldg(p), b = __ldg(p + 1);
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+    v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+__device__ __forceinline__ void load_y(const __half *y, const float *ys, int64_t slot, int H, int c,
+                                       float (&v)[8]) {
+    const uint4 r = __ldg(reinterpret_cast<const uint4 *>(y + slot * H) + c);
+    const float s = __ldg(ys + slot * ((H + 127) / 128) + c / 16);
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
+        v[2 * i] = f.x * s;
+        v[2 * i + 1] = f.y * s;
+    }
+}
+
+// out[t] = sum_j w[t][j] y[slot of (t, j)] (+ gate[t] y[routed + t]), in the order of j.  A warp
+// takes 256 columns of a token, eight per lane; reads y once: bound by memory.
+template <typename Y, typename T>
 __global__ void __launch_bounds__(256)
-    k_scaled_combine(const float *__restrict__ y, const int32_t *__restrict__ inv_perm,
-                     const int32_t *__restrict__ ids, const float *__restrict__ w,
-                     const float *__restrict__ gate, int tokens, int k, int E, int shared, int H,
-                     T *__restrict__ out, uint32_t *status) {
-    __shared__ int s_slot[kMaxK + 1];
-    __shared__ float s_w[kMaxK + 1];
-    const int t = blockIdx.x, A = tokens * k;
-    if ((int)threadIdx.x < k) {
-        const int s = inv_perm[t * k + threadIdx.x], e = ids[t * k + threadIdx.x];
+    k_scaled_combine(const Y *__restrict__ y, const float *__restrict__ ys,
+                     const int32_t *__restrict__ inv_perm, const int32_t *__restrict__ ids,
+                     const float *__restrict__ w, const float *__restrict__ gate, int tokens,
+                     int k, int E, int shared, int H, T *__restrict__ out, uint32_t *status) {
+    const int lane = threadIdx.x & 31;
+    const int per = (H / 8 + 31) / 32;
+    const int64_t unit = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int64_t t = unit / per;
+    if (t >= tokens) return;
+    const int c = (int)(unit - t * per) * 32 + lane;
+    const int A = tokens * k;
+    // lane j holds pair j's slot and weight
+    int slot = -1;
+    float wt = 0.f;
+    if (lane < k) {
+        const int s = __ldg(inv_perm + t * k + lane), e = __ldg(ids + t * k + lane);
         const bool in = s >= 0 && s < A && e >= 0 && e < E;
         if (!in) set_status(status, MOE_ERR_BOUNDS);
-        s_slot[threadIdx.x] = in ? s : -1;
-        s_w[threadIdx.x] = w[t * k + threadIdx.x];
+        slot = in ? s : -1;
+        wt = __ldg(w + t * k + lane);
     }
-    if (threadIdx.x == 0) {
-        s_slot[k] = shared ? A + t : -1;
-        s_w[k] = shared ? (gate ? gate[t] : 1.0f) : 0.f;
+    float acc[8];
+#pragma unroll
+    for (int i = 0; i < 8; i++) acc[i] = 0.f;
+    const bool in = 8 * c < H;
+#pragma unroll 4
+    for (int j = 0; j < k; j++) {
+        const int s = __shfl_sync(kFull, slot, j);
+        const float f = __shfl_sync(kFull, wt, j);
+        if (s < 0 || !in) continue;
+        float v[8];
+        load_y(y, ys, s, H, c, v);
+#pragma unroll
+        for (int i = 0; i < 8; i++) acc[i] = fmaf(f, v[i], acc[i]);
     }
-    __syncthreads();
-    for (int c = threadIdx.x; c < H / 4; c += blockDim.x) {
-        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int j = 0; j <= k; j++) {
-            if (s_slot[j] < 0) continue;
-            const float4 v = __ldg(reinterpret_cast<const float4 *>(y + (int64_t)s_slot[j] * H) + c);
-            const float f = s_w[j];
-            s.x = fmaf(f, v.x, s.x);
-            s.y = fmaf(f, v.y, s.y);
-            s.z = fmaf(f, v.z, s.z);
-            s.w = fmaf(f, v.w, s.w);
-        }
-        T *o = out + (int64_t)t * H + 4 * c;
-        o[0] = from_f32<T>(s.x);
-        o[1] = from_f32<T>(s.y);
-        o[2] = from_f32<T>(s.z);
-        o[3] = from_f32<T>(s.w);
+    if (!in) return;
+    if (shared) {
+        const float f = gate ? __ldg(gate + t) : 1.0f;
+        float v[8];
+        load_y(y, ys, (int64_t)A + t, H, c, v);
+#pragma unroll
+        for (int i = 0; i < 8; i++) acc[i] = fmaf(f, v[i], acc[i]);
+    }
+    T *o = out + t * H + 8 * c;
+    if (sizeof(T) == 4) {
+        reinterpret_cast<float4 *>(o)[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+        reinterpret_cast<float4 *>(o)[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+    } else {
+        *reinterpret_cast<uint4 *>(o) =
+            make_uint4(pack2(acc[0], acc[1], (T *)nullptr), pack2(acc[2], acc[3], (T *)nullptr),
+                       pack2(acc[4], acc[5], (T *)nullptr), pack2(acc[6], acc[7], (T *)nullptr));
     }
 }
 
@@ -814,10 +784,11 @@ cudaError_t run_tc(bool pair, const TcArgs &a, const CUtensorMap &w0, const CUte
 size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 
 struct ExpertsWs {
-    size_t xq, xs, hq, hs, y, slices, nslices, total;
+    size_t xq, xs, hq, hs, y, ys, slices, nslices, total;
     int64_t slots, most_slices;
 };
 
+// y is sized for fp32; with a 16-bit output it is fp16.
 ExpertsWs experts_ws(const moe_scaled_weights &w, int T, int k) {
     ExpertsWs L{};
     size_t p = 0;
@@ -827,11 +798,12 @@ ExpertsWs experts_ws(const moe_scaled_weights &w, int T, int k) {
         return o;
     };
     L.slots = (int64_t)T * k + (w.shared ? T : 0);
-    L.xq = take((size_t)T * w.hidden);
-    L.xs = take((size_t)sblocks(w.hidden) * T * 4);
+    L.xq = take((size_t)L.slots * w.hidden);
+    L.xs = take((size_t)sblocks(w.hidden) * L.slots * 4);
     L.hq = take((size_t)L.slots * w.ffn);
     L.hs = take((size_t)sblocks(w.ffn) * L.slots * 4);
     L.y = take((size_t)L.slots * w.hidden * 4);
+    L.ys = take((size_t)L.slots * sblocks(w.hidden) * 4);
     L.most_slices = (int64_t)T * k / kMT + std::min<int64_t>(w.n_experts, (int64_t)T * k) +
                     (w.shared ? (T + kMT - 1) / kMT : 0);
     L.slices = take(sizeof(Job) * (size_t)L.most_slices);
@@ -845,6 +817,20 @@ bool use_pair_experts(const moe_scaled_weights &w, int T, int k) {
     return (int64_t)T * k > 4 * (int64_t)kMT * w.n_experts;
 }
 
+template <typename Y>
+cudaError_t run_combine(const ScaledExpertsArgs &e, const void *y, const float *ys, cudaStream_t st) {
+    const moe_scaled_weights &w = e.w;
+    const int64_t units = (int64_t)e.T * ((w.hidden / 8 + 31) / 32);
+    return with_dtype(e.out_dt, [&](auto *tag) {
+        using E = std::remove_pointer_t<decltype(tag)>;
+        k_scaled_combine<Y, E><<<(unsigned)((units + 7) / 8), 256, 0, st>>>(
+            static_cast<const Y *>(y), ys, e.inv_perm, e.ids, e.rw, e.gate, e.T, e.k, w.n_experts,
+            w.shared, w.hidden, static_cast<E *>(e.out), e.status);
+        note_launches(1);
+        return cudaGetLastError();
+    });
+}
+
 cudaError_t experts_tc(const ScaledExpertsArgs &e, uint8_t *ws, cudaStream_t st) {
     const moe_scaled_weights &w = e.w;
     const ExpertsWs L = experts_ws(w, e.T, e.k);
@@ -852,28 +838,26 @@ cudaError_t experts_tc(const ScaledExpertsArgs &e, uint8_t *ws, cudaStream_t st)
     Job *slices = reinterpret_cast<Job *>(ws + L.slices);
     int32_t *nslices = reinterpret_cast<int32_t *>(ws + L.nslices);
     float *xs = reinterpret_cast<float *>(ws + L.xs);
-    CUtensorMap gate, up, down, h, h16;
-    const bool pair = use_pair_experts(w, e.T, e.k);
+    float *ys = reinterpret_cast<float *>(ws + L.ys);
+    CUtensorMap gate, up, down, x, x16, h, h16;
     if (!encode(&gate, w.d_gate, H, F, H, n, 128) || !encode(&up, w.d_up, H, F, H, n, 128) ||
         !encode(&down, w.d_down, F, H, F, n, 128) ||
+        !encode(&x, ws + L.xq, H, L.slots, H, 0, 128) ||
+        !encode(&x16, ws + L.xq, H, L.slots, H, 0, 16) ||
         !encode(&h, ws + L.hq, F, L.slots, F, 0, 128) ||
         !encode(&h16, ws + L.hq, F, L.slots, F, 0, 16))
         return cudaErrorInvalidValue;
+    const bool pair = use_pair_experts(w, e.T, e.k);
     k_scaled_slices<<<1, 1024, 0, st>>>(e.offsets, w.n_experts, e.T, e.k, w.shared,
                                         pair ? 2 * kMT : kMT, slices, nslices, e.status);
     note_launches(1);
     cudaError_t err = cudaGetLastError();
     if (err != cudaSuccess) return err;
-    err = launch_scaled_quantize(e.x, e.x_dt, e.T, H, H, ws + L.xq, H, xs, e.T, e.status, st);
+    err = launch_scaled_spread(e, ws + L.xq, xs, st);
     if (err != cudaSuccess) return err;
     TcArgs a{};
     a.slices = slices;
     a.nslices = nslices;
-    a.perm = e.perm;
-    a.xq = ws + L.xq;
-    a.x_cols = H;
-    a.k = e.k;
-    a.routed = e.T * e.k;
     a.status = e.status;
     a.slots = L.slots;
     a.hq = ws + L.hq;
@@ -882,32 +866,30 @@ cudaError_t experts_tc(const ScaledExpertsArgs &e, uint8_t *ws, cudaStream_t st)
     a.rows = F;
     a.row_tiles = sblocks(F);
     a.as = xs;
-    a.ldas = e.T;
+    a.ldas = L.slots;
     a.ws0 = w.d_gate_s;
     a.ws1 = w.d_up_s;
     a.ws_expert = (int64_t)sblocks(F) * sblocks(H);
-    err = run_tc<kGateUp, float>(pair, a, gate, up, h, h16, L.most_slices * a.row_tiles, st);
+    err = run_tc<kGateUp, float>(pair, a, gate, up, x, x16, L.most_slices * a.row_tiles, st);
     if (err != cudaSuccess) return err;
     a.nkb = sblocks(F);
     a.rows = H;
     a.row_tiles = (H + kNW - 1) / kNW;
     a.as = a.hs;
-    a.ldas = L.slots;
     a.ws0 = w.d_down_s;
     a.out = ws + L.y;
     a.ldo = H;
     a.vec = true;
-    err = run_tc<kDown, float>(pair, a, down, down, h, h16, L.most_slices * a.row_tiles, st);
-    if (err != cudaSuccess) return err;
-    return with_dtype(e.out_dt, [&](auto *tag) {
-        using E = std::remove_pointer_t<decltype(tag)>;
-        k_scaled_combine<E><<<e.T, 256, 0, st>>>(reinterpret_cast<const float *>(ws + L.y),
-                                                 e.inv_perm, e.ids, e.rw, e.gate, e.T, e.k,
-                                                 w.n_experts, w.shared, H,
-                                                 static_cast<E *>(e.out), e.status);
-        note_launches(1);
-        return cudaGetLastError();
-    });
+    const int64_t tiles = L.most_slices * a.row_tiles;
+    if (e.out_dt == MOE_DT_F32) {
+        err = run_tc<kDown, float>(pair, a, down, down, h, h16, tiles, st);
+        return err != cudaSuccess ? err : run_combine<float>(e, ws + L.y, nullptr, st);
+    }
+    a.ys = ys;
+    // 2^y_exp * 65504 >= nkb * 128 * 448^2
+    a.y_exp = (int)std::ceil(std::log2(a.nkb * (128.0 * 448.0 * 448.0) / 65504.0));
+    err = run_tc<kDown, __half>(pair, a, down, down, h, h16, tiles, st);
+    return err != cudaSuccess ? err : run_combine<__half>(e, ws + L.y, ys, st);
 }
 
 cudaError_t matmul_tc(const ScaledMatmulArgs &m, cudaStream_t st) {

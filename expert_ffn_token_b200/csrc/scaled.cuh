@@ -97,15 +97,17 @@ __device__ __forceinline__ uint32_t quant4(float4 v, float s, float inv) {
     return lo;
 }
 
+// The largest magnitude of four values, as the integer whose order it follows.
+__device__ __forceinline__ uint32_t abs_bits(float4 v) {
+    return max(max(__float_as_uint(v.x) & 0x7fffffffu, __float_as_uint(v.y) & 0x7fffffffu),
+               max(__float_as_uint(v.z) & 0x7fffffffu, __float_as_uint(v.w) & 0x7fffffffu));
+}
+
 // The block of 128 values that a warp holds, 4 per lane (0 past the row's end): the packed bytes
 // of the lane's values; *s receives the scale.  Returns the bytes; *finite is false (and bytes and
 // scale 0) when a value was not finite.
 __device__ __forceinline__ uint32_t quant_block(float4 v, float *s, bool *finite) {
-    constexpr unsigned all = 0xffffffffu;
-    // the largest magnitude as integers: a NaN or infinity has the largest bit patterns
-    const uint32_t m = max(max(__float_as_uint(v.x) & 0x7fffffffu, __float_as_uint(v.y) & 0x7fffffffu),
-                           max(__float_as_uint(v.z) & 0x7fffffffu, __float_as_uint(v.w) & 0x7fffffffu));
-    const uint32_t amax = __reduce_max_sync(all, m);
+    const uint32_t amax = __reduce_max_sync(0xffffffffu, abs_bits(v));
     const bool fin = amax < 0x7f800000u;
     const float sc = fin ? __fdiv_rn(__uint_as_float(amax), kE4M3Max) : 0.0f;
     *s = sc;
@@ -156,13 +158,15 @@ struct ScaledExpertsArgs {
     int T, k;
     const int32_t *ids;
     const float *rw;               // routing weights [T][k]
-    const int32_t *offsets, *perm, *inv_perm;
+    const int32_t *offsets, *inv_perm;
     const float *gate;             // [T] or null
     void *out;
     int out_dt;
     uint32_t *status;
     float *h;                      // small batches: h of (job, token) [jobs][8][ffn]
 };
+// x quantised into the slots of its tokens: q [slots][hidden], scales [blocks][slots].
+cudaError_t launch_scaled_spread(const ScaledExpertsArgs &e, uint8_t *q, float *s, cudaStream_t st);
 // The layer on the kernels that suit T, and the workspace they need for exactly T tokens.
 size_t scaled_experts_ws_bytes(const moe_scaled_weights &w, int T, int k);
 cudaError_t launch_scaled_experts(const ScaledExpertsArgs &a, void *ws, cudaStream_t st);

@@ -127,8 +127,7 @@ moe_status moe_scaled_experts_workspace_size(const moe_scaled_weights *host_weig
 
 moe_status moe_scaled_experts(const moe_scaled_weights *host_weights, const void *d_x,
                               int x_dtype, int T, int k, const int32_t *d_ids, const float *d_w,
-                              const int32_t *d_offsets, const int32_t *d_perm,
-                              const int32_t *d_inv_perm, const float *d_gate, void *d_out,
+                              const int32_t *d_offsets, const int32_t *d_inv_perm, const float *d_gate, void *d_out,
                               int out_dtype, uint32_t *d_status, void *d_ws, size_t ws_bytes,
                               void *stream) {
     const moe_status st = check_weights(host_weights);
@@ -136,7 +135,7 @@ moe_status moe_scaled_experts(const moe_scaled_weights *host_weights, const void
     const moe_scaled_weights &w = *host_weights;
     if (!w.d_gate || !w.d_up || !w.d_down || !w.d_gate_s || !w.d_up_s || !w.d_down_s)
         return MOE_ERR_INVALID_ARG;
-    if (!d_x || !d_ids || !d_w || !d_offsets || !d_perm || !d_inv_perm || !d_out || !d_ws)
+    if (!d_x || !d_ids || !d_w || !d_offsets || !d_inv_perm || !d_out || !d_ws)
         return MOE_ERR_INVALID_ARG;
     if (!dtype_ok(x_dtype) || !dtype_ok(out_dtype) || (d_gate && !w.shared))
         return MOE_ERR_INVALID_ARG;
@@ -144,7 +143,7 @@ moe_status moe_scaled_experts(const moe_scaled_weights *host_weights, const void
     if ((int64_t)T * (k + 1) > kScaledMaxSlots) return MOE_ERR_UNSUPPORTED;
     if (!aligned(w.d_gate, 16) || !aligned(w.d_up, 16) || !aligned(w.d_down, 16) ||
         !aligned(d_x, 16) || !aligned(d_out, 16) || !aligned(d_ws, 256) ||
-        !words({w.d_gate_s, w.d_up_s, w.d_down_s, d_ids, d_w, d_offsets, d_perm, d_inv_perm,
+        !words({w.d_gate_s, w.d_up_s, w.d_down_s, d_ids, d_w, d_offsets, d_inv_perm,
                 d_gate, d_status}))
         return MOE_ERR_ALIGNMENT;
     if (ws_bytes < scaled_experts_ws_bytes(w, T, k)) return MOE_ERR_WORKSPACE;
@@ -157,7 +156,6 @@ moe_status moe_scaled_experts(const moe_scaled_weights *host_weights, const void
     a.ids = d_ids;
     a.rw = d_w;
     a.offsets = d_offsets;
-    a.perm = d_perm;
     a.inv_perm = d_inv_perm;
     a.gate = d_gate;
     a.out = d_out;

@@ -129,8 +129,8 @@ _lib.moe_scaled_matmul_workspace_size.argtypes = [_I, _I, _I, ctypes.POINTER(_S)
 _lib.moe_scaled_matmul.argtypes = [_P, _L, _P, _L, _I, _I, _P, _L, _P, _I, _P, _I, _L, _P, _P,
                                    _S, _P]
 _lib.moe_scaled_experts_workspace_size.argtypes = [_P, _I, _I, ctypes.POINTER(_S)]
-_lib.moe_scaled_experts.argtypes = [_P, _P, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _I, _P, _P,
-                                    _S, _P]
+_lib.moe_scaled_experts.argtypes = [_P, _P, _I, _I, _I, _P, _P, _P, _P, _P, _P, _I, _P, _P, _S,
+                                    _P]
 _lib.moe_kernels_enqueued.argtypes = []
 _lib.moe_kernels_enqueued.restype = ctypes.c_uint64
 
@@ -361,11 +361,11 @@ def scaled_experts_workspace_size(weights: ScaledWeights, max_tokens: int, k: in
 
 
 def scaled_experts(weights: ScaledWeights, d_x: int, x_dtype: int, T: int, k: int, d_ids: int,
-                   d_w: int, d_offsets: int, d_perm: int, d_inv_perm: int, d_gate, d_out: int,
-                   out_dtype: int, d_status, d_ws: int, ws_bytes: int, stream=None) -> None:
+                   d_w: int, d_offsets: int, d_inv_perm: int, d_gate, d_out: int, out_dtype: int,
+                   d_status, d_ws: int, ws_bytes: int, stream=None) -> None:
     _check(_lib.moe_scaled_experts(ctypes.addressof(weights), d_x, x_dtype, T, k, d_ids, d_w,
-                                   d_offsets, d_perm, d_inv_perm, d_gate, d_out, out_dtype,
-                                   d_status, d_ws, ws_bytes, stream), "moe_scaled_experts")
+                                   d_offsets, d_inv_perm, d_gate, d_out, out_dtype, d_status,
+                                   d_ws, ws_bytes, stream), "moe_scaled_experts")
 
 
 # ------------------------------------------------------------------ torch convenience
@@ -485,7 +485,8 @@ class ScaledExperts:
         return ids, w, offsets, perm, inv
 
     def forward(self, x, ids, w, offsets, perm, inv_perm, gate=None, out=None):
-        """The experts' combined output [T][hidden] for tokens routed by route() or route_topk."""
+        """The experts' combined output [T][hidden] for tokens routed by route() or route_topk (perm,
+        the inverse of inv_perm, is not read)."""
         import torch
         T, k, E = x.shape[0], self.k, self.n_experts
         i32, f32 = torch.int32, torch.float32
@@ -493,7 +494,6 @@ class ScaledExperts:
         _contiguous(ids, "ids", (T, k), i32)
         _contiguous(w, "w", (T, k), f32)
         _contiguous(offsets, "offsets", (E + 1,), i32)
-        _contiguous(perm, "perm", (T * k,), i32)
         _contiguous(inv_perm, "inv_perm", (T * k,), i32)
         if gate is not None:
             _contiguous(gate, "gate", (T,), f32)
@@ -501,7 +501,7 @@ class ScaledExperts:
             out = torch.empty_like(x)
         _contiguous(out, "out", (T, self.hidden))
         scaled_experts(self.weights, x.data_ptr(), dtype_of(x), T, k, ids.data_ptr(),
-                       w.data_ptr(), offsets.data_ptr(), perm.data_ptr(), inv_perm.data_ptr(),
+                       w.data_ptr(), offsets.data_ptr(), inv_perm.data_ptr(),
                        None if gate is None else gate.data_ptr(), out.data_ptr(), dtype_of(out),
                        self.status_word.data_ptr(), self.ws.data_ptr(), self.ws_bytes, _stream())
         return out

@@ -403,11 +403,12 @@ typedef struct {
 } moe_scaled_weights;
 
 /* a4-a7 on scaled experts, for tokens routed by moe_route_scored or moe_route_topk (d_ids, d_w,
- * d_offsets, d_perm, d_inv_perm as written there for T, n_experts, k):
+ * d_offsets, d_inv_perm as written there for T, n_experts, k):
  *   x^ = d_x [T][hidden] as moe_scaled_quantize stores it, g = W_gate x^, u = W_up x^,
  *   h = g / (1 + exp(-g)) * u in fp32, h^ = h quantised likewise per 128 values of ffn,
  *   y = W_down h^, d_out[t] = sum_j w[t][j] y[t][ids[t][j]] (+ gate[t] y[t][shared])
- * with d_x and d_out [T][hidden] contiguous of x_dtype and out_dtype, 16-byte aligned, d_gate
+ * (y in fp32, or, with a 16-bit out_dtype, in fp16 times a power of two per token and 128
+ * columns), with d_x and d_out [T][hidden] contiguous of x_dtype and out_dtype, 16-byte aligned, d_gate
  * fp32 [T] (NULL: 1; only with shared).  A routed id or a slot outside its range is skipped and
  * reported as MOE_ERR_BOUNDS in d_status (may be NULL), a non-finite block of x or h is taken as
  * zeros and reported as MOE_ERR_NONFINITE.  1 <= T <= the max_tokens the workspace was sized for
@@ -417,8 +418,8 @@ moe_status moe_scaled_experts_workspace_size(const moe_scaled_weights *host_weig
                                              int max_tokens, int k, size_t *bytes);
 moe_status moe_scaled_experts(const moe_scaled_weights *host_weights, const void *d_x,
                               int x_dtype, int T, int k, const int32_t *d_ids, const float *d_w,
-                              const int32_t *d_offsets, const int32_t *d_perm,
-                              const int32_t *d_inv_perm, const float *d_gate, void *d_out,
+                              const int32_t *d_offsets, const int32_t *d_inv_perm,
+                              const float *d_gate, void *d_out,
                               int out_dtype, uint32_t *d_status, void *d_ws, size_t ws_bytes,
                               void *stream);
 

@@ -80,14 +80,17 @@ def experts(x, ids, w, gate, W):
     """The experts' layer in 64 bits: x [T][H] (values as the operator reads them), ids, w [T][k],
     gate [T] or None, W: dict of (codes, scales) of gate, up, down, with `shared`.
 
-    Returns (out, tol): tol bounds what fp32 arithmetic may change.  g and u carry
+    Returns (out, tol, half): tol bounds what fp32 arithmetic may change, half what holding every
+    y in fp16 times a power of two per 128 columns adds (batches of more than 8 tokens with a
+    16-bit output): 2^-11 of |y|, and half of fp16's smallest step times the power, which is
+    less than four times what the largest possible sum asks for.  In tol, g and u carry
     product_error; h = silu(g) u inherits them (|silu'| <= 1.1) with a few fp32 roundings; a
     value of h whose quotient lies that close to a rounding boundary may take the neighbouring
     e4m3 value; y and the weighted sum round in fp32."""
     T, H = x.shape
     E = W["gate"][0].shape[0] - int(W["shared"])
     xq = wide_act(*quantize(x))
-    out, tol = np.zeros((T, H)), np.zeros((T, H))
+    out, tol, half = np.zeros((T, H)), np.zeros((T, H)), np.zeros((T, H))
     jobs = [(e, [(t, w[t, j]) for t in range(T) for j in range(ids.shape[1]) if ids[t, j] == e])
             for e in range(E)]
     if W["shared"]:
@@ -119,8 +122,11 @@ def experts(x, ids, w, gate, W):
         y, ya = matmul(hv, m["down"])
         ty = dv @ np.abs(m["down"]).T + ya * product_error(blocks(F))
         np.add.at(out, t, c * y)
+        top = (hs.T.astype(np.float64)[:, None, :] * W["down"][1][e].astype(np.float64)).max(2)
+        power = 4 * np.repeat(top, BLOCK, 1)[:, :H] * blocks(F) * 128 * 448.0 ** 2 / 65504
+        np.add.at(half, t, np.abs(c) * (np.abs(y) * 2.0 ** -11 + 2.0 ** -25 * power))
         np.add.at(tol, t, np.abs(c) * (ty + np.abs(y) * (ids.shape[1] + 3) * 2.0 ** -24))
-    return out, tol
+    return out, tol, half
 
 
 def random_weights(rng, n, rows, cols):

@@ -107,15 +107,14 @@ def test_scaled_experts_refuses(moe):
 
     need = moe.scaled_experts_workspace_size(weights(), 4, 2)
 
-    def call(w=None, x=FAKE, xdt=1, T=4, k=2, ids=FAKE, rw=FAKE, off=FAKE, perm=FAKE, inv=FAKE,
+    def call(w=None, x=FAKE, xdt=1, T=4, k=2, ids=FAKE, rw=FAKE, off=FAKE, inv=FAKE,
              gate=None, out=FAKE, odt=1, status=None, ws=FAKE, nbytes=need):
         w = weights() if w is None else w
-        return L.moe_scaled_experts(ctypes.addressof(w), x, xdt, T, k, ids, rw, off, perm, inv,
-                                    gate, out, odt, status, ws, nbytes, None)
+        return L.moe_scaled_experts(ctypes.addressof(w), x, xdt, T, k, ids, rw, off, inv, gate, out, odt, status, ws, nbytes, None)
 
     before = moe.kernels_enqueued()
     bad = moe.ERR_INVALID_ARG
-    for name in ("x", "ids", "rw", "off", "perm", "inv", "out", "ws"):
+    for name in ("x", "ids", "rw", "off", "inv", "out", "ws"):
         assert call(**{name: None}) == bad, name
     for name in ("d_gate", "d_up", "d_down", "d_gate_s", "d_up_s", "d_down_s"):
         assert call(w=weights(**{name: None})) == bad, name
