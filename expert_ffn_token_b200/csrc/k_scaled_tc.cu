@@ -16,14 +16,13 @@
 // kernel (1380 clocks per block of 128 k against 512 of MMA).  An expert with few tokens leaves
 // rows of the MMA unused, which costs nothing that counts: it is bound by its weights' bytes.
 //
-// One persistent CTA per SM, or a pair of CTAs (cta_group::2) per tile of 256 tokens: each CTA
-// then loads its own 128 token rows and half of the weight rows, 32 KB per block of k instead of
-// 48 KB, because a single CTA's tile is bound by what L2 can deliver to an SM.
+// One persistent CTA per SM.  Pairs of CTAs (cta_group::2, 256 tokens a tile) load a third less per
+// MMA, but the hand-overs between the two cost what the loads gain: 8192^3 547 us against 560 us,
+// 4096 x 1280 x 2560 37 against 35 us, 8192 routed tokens 1270 against 1006 us.  They are not used.
 //
 // Roles (640 threads; registers move from the first four warps to the epilogue):
 //   warp 0        TMA producer: weight boxes of 128 rows x 128 bytes, token rows as boxes of 16
-//   warp 1        tensor-memory allocation and the MMA issuer; in the second CTA of a pair it
-//                 passes "stage full" on to the first
+//   warp 1        tensor-memory allocation and the MMA issuer
 //   warp 2        the scales of every block, copied into a ring four blocks a hand-over
 //   warps 4-19    epilogue: lane quarter (warp % 4), 32 columns of each 128-row operand.  Four warps
 //                 a scheduler, because a block is a chain of hand-overs and tensor-memory loads
@@ -52,13 +51,9 @@ constexpr int kNW = 256;                       // weight rows of a tile (gate/up
 constexpr int kEpiWarp0 = 4, kEpiWarps = 16;
 constexpr int kThreads = (kEpiWarp0 + kEpiWarps) * 32;
 constexpr uint32_t kOperand = 128 * kSBlk;     // bytes of 128 rows of one block
-constexpr uint32_t kRing = 12 * kOperand;      // shared memory of all stages
-// A stage holds the weights (two operands, or this CTA's one of a pair) and 128 token rows.
-constexpr uint32_t weight_bytes(int pair) { return (uint32_t)(3 - pair) * kOperand; }
-constexpr uint32_t stage_bytes(int pair) { return weight_bytes(pair) + kOperand; }
-constexpr int stages(int pair) { return (int)(kRing / stage_bytes(pair)); }
-constexpr int kMaxStages = 6;
-static_assert(stages(1) == 4 && stages(2) == kMaxStages, "stages");
+constexpr uint32_t kWeights = 2 * kOperand;    // a stage: the weights' two operands
+constexpr uint32_t kStage = kWeights + kOperand;   // and the tokens
+constexpr int kStages = 4;
 constexpr int kAccs = 2;                       // accumulator buffers of 256 columns
 constexpr int kBand = 8;                       // row tiles of a band (dense)
 constexpr int kGroup = 4;                      // blocks whose scales are handed over together
@@ -100,42 +95,30 @@ struct Tile {
     int e, rt, slot, n;
 };
 
-// Tile i as CTA `rank` of its kPair CTAs sees it (its own 128 tokens; n may be 0 or less in the
-// second).  Experts: row tiles are innermost, so that the CTAs that run at the same time share
+// Tile i.  Experts: row tiles are innermost, so that the CTAs that run at the same time share
 // an expert's weights (its slices follow one another) and a slice's tokens.
-template <int kMode, int kPair>
-__device__ __forceinline__ Tile tile_at(const TcArgs &a, int i, int rank) {
+template <int kMode>
+__device__ __forceinline__ Tile tile_at(const TcArgs &a, int i) {
     Tile t;
     int s = i / a.row_tiles;
     t.rt = i - s * a.row_tiles;
     if (kMode == kDense) {
         // bands of kBand row tiles, so that the tiles in flight cover a compact part of both sides
-        const int ns = (a.M + kPair * kMT - 1) / (kPair * kMT);
+        const int ns = (a.M + kMT - 1) / kMT;
         const int band = i / (kBand * ns), in = i - band * (kBand * ns);
         const int width = min(kBand, a.row_tiles - band * kBand);
         s = in / width;
         t.rt = band * kBand + in - s * width;
         t.e = 0;
-        t.slot = s * (kPair * kMT);
-        t.n = min(kPair * kMT, a.M - t.slot);
+        t.slot = s * kMT;
+        t.n = min(kMT, a.M - t.slot);
     } else {
         const int4 v = __ldg(reinterpret_cast<const int4 *>(a.slices) + s);
         t.e = v.x;
         t.slot = v.y;
         t.n = v.z;
     }
-    t.slot += rank * kMT;
-    t.n = min(kMT, t.n - rank * kMT);
     return t;
-}
-// Tiles go round the clusters (single CTAs or pairs).
-template <int kPair>
-__device__ __forceinline__ int first_tile() { return (int)blockIdx.x / kPair; }
-template <int kPair>
-__device__ __forceinline__ int tile_step() { return (int)gridDim.x / kPair; }
-template <int kPair>
-__device__ __forceinline__ int tiles_of_cta(int tiles) {
-    return max(0, tiles - first_tile<kPair>() + tile_step<kPair>() - 1) / tile_step<kPair>();
 }
 
 // silu(g) * u in fp32 with CUDA's expf and its approximate division (2 ulp; a denominator past
@@ -145,8 +128,8 @@ __device__ __forceinline__ float silu_mul(float g, float u) {
 }
 
 struct Shared {
-    uint64_t full[kMaxStages], empty[kMaxStages], peer[kMaxStages], acc_full[kAccs],
-        acc_empty[kAccs], sc_full[kScales], sc_empty[kScales], done;
+    uint64_t full[kStages], empty[kStages], acc_full[kAccs], acc_empty[kAccs], sc_full[kScales],
+        sc_empty[kScales], done;
     uint32_t tmem;
     int abort;
     float as[kScales][kGroup][kMT];       // per block: the tokens' scales
@@ -155,7 +138,7 @@ struct Shared {
     float patch[kEpiWarps][32][kPatch + 1];
 };
 
-constexpr size_t kSmem = 1024 + (size_t)kRing + sizeof(Shared);
+constexpr size_t kSmem = 1024 + (size_t)kStages * kStage + sizeof(Shared);
 static_assert(kSmem <= 232448, "shared memory");
 
 struct Pos {                          // ring position
@@ -192,122 +175,106 @@ __device__ __forceinline__ bool waitw(Shared &S, uint64_t *bar, uint32_t parity,
     return __all_sync(0xffffffffu, wait1(S, bar, parity, st));
 }
 
-template <int kMode, int kPair>
-__device__ void produce(const TcArgs &a, Shared &S, uint8_t *ring, int tiles, int rank,
-                        const CUtensorMap *w0, const CUtensorMap *w1, const CUtensorMap *x,
-                        const CUtensorMap *x16) {
+template <int kMode>
+__device__ void produce(const TcArgs &a, Shared &S, uint8_t *ring, int tiles, const CUtensorMap *w0,
+                        const CUtensorMap *w1, const CUtensorMap *x, const CUtensorMap *x16) {
     const int lane = threadIdx.x & 31;
-    const int mine = tiles_of_cta<kPair>(tiles);
     Pos p;
     int issued = 0;
-    if (mine == 0) return;
-    Tile next = tile_at<kMode, kPair>(a, first_tile<kPair>(), rank);
+    int i = blockIdx.x;
+    if (i >= tiles) return;
+    Tile next = tile_at<kMode>(a, i);
     bool ok = true;
-    for (int m = 0; ok && m < mine; m++) {
+    for (; ok && i < tiles; i += gridDim.x) {
         const Tile t = next;
         // more than half a tile of tokens comes as one box of 128 rows (those past the slice, if
         // they exist, are read and not used): every box costs the copy engine time of its own
         const bool whole = t.n > kMT / 2;
-        const int npad = whole ? kMT : max(0, (t.n + 15) & ~15);
+        const int npad = whole ? kMT : (t.n + 15) & ~15;
         // the next tile's place arrives while this one's blocks are issued
-        if (m + 1 < mine)
-            next = tile_at<kMode, kPair>(a, first_tile<kPair>() + (m + 1) * tile_step<kPair>(), rank);
+        if (i + (int)gridDim.x < tiles) next = tile_at<kMode>(a, i + gridDim.x);
         for (int b = 0; b < a.nkb; b++) {
             if (!waitw(S, &S.empty[p.s], p.ph ^ 1u, a.status)) {
                 ok = false;
                 break;
             }
-            uint8_t *st = ring + (size_t)p.s * stage_bytes(kPair);
+            uint8_t *st = ring + (size_t)p.s * kStage;
             uint64_t *bar = &S.full[p.s];
             if (lane == 0) {
-                mbar_arrive_expect_tx(bar, weight_bytes(kPair) + (uint32_t)npad * kSBlk);
+                mbar_arrive_expect_tx(bar, kWeights + (uint32_t)npad * kSBlk);
                 const int r0 = kMode == kGateUp ? t.rt * 128 : t.rt * kNW;
                 const int r1 = kMode == kGateUp ? r0 : r0 + 128;
-                if (kPair == 1 || rank == 0) tma_load_3d(st, w0, b * kSBlk, r0, t.e, bar);
-                if (kPair == 1) tma_load_3d(st + kOperand, w1, b * kSBlk, r1, t.e, bar);
-                if (kPair == 2 && rank == 1) tma_load_3d(st, w1, b * kSBlk, r1, t.e, bar);
-                if (whole) tma_load_2d(st + weight_bytes(kPair), x, b * kSBlk, t.slot, bar);
+                tma_load_3d(st, w0, b * kSBlk, r0, t.e, bar);
+                tma_load_3d(st + kOperand, w1, b * kSBlk, r1, t.e, bar);
+                if (whole) tma_load_2d(st + kWeights, x, b * kSBlk, t.slot, bar);
             }
             __syncwarp();
             if (!whole && 16 * lane < npad)
-                tma_load_2d(st + weight_bytes(kPair) + lane * 16 * kSBlk, x16, b * kSBlk,
-                            t.slot + 16 * lane, bar);
+                tma_load_2d(st + kWeights + lane * 16 * kSBlk, x16, b * kSBlk, t.slot + 16 * lane,
+                            bar);
             issued++;
-            p.next(stages(kPair));
+            p.next(kStages);
         }
     }
     // leaving early, the copies in flight land before the CTA goes; else the stages' last uses
-    // are over (a pair's commits reach both CTAs)
-    for (int j = max(0, issued - stages(kPair)); j < issued; j++) {
-        const int s = j % stages(kPair);
-        const uint32_t ph = (uint32_t)(j / stages(kPair)) & 1u;
+    // are over
+    for (int j = max(0, issued - kStages); j < issued; j++) {
+        const uint32_t ph = (uint32_t)(j / kStages) & 1u;
         if (ok)
-            wait1(S, &S.empty[s], ph, a.status);
+            wait1(S, &S.empty[j % kStages], ph, a.status);
         else
-            mbar_wait_bounded(&S.full[s], ph, kWaitNs);
+            mbar_wait_bounded(&S.full[j % kStages], ph, kWaitNs);
     }
 }
 
-// The MMA issuer: warp 1 of a single CTA or of a pair's first.  The whole warp walks the loop and
-// one elected lane issues, so that the descriptors stay in uniform registers.
-template <int kPair>
+// Blocks of the tiles that this CTA takes.
+__device__ __forceinline__ int64_t blocks_of_cta(const TcArgs &a, int tiles) {
+    const int step = gridDim.x;
+    return (int64_t)(max(0, tiles - (int)blockIdx.x + step - 1) / step) * a.nkb;
+}
+
+// The MMA issuer.  The whole warp walks the loop and one elected lane issues, so that the
+// descriptors stay in uniform registers.
 __device__ void multiply(const TcArgs &a, Shared &S, uint8_t *ring, int tiles, uint32_t tmem) {
-    constexpr uint32_t idesc = instr_desc(0, kPair * kMT, kNW);
-    const int64_t total = (int64_t)tiles_of_cta<kPair>(tiles) * a.nkb;
+    constexpr uint32_t idesc = instr_desc(0, kMT, kNW);
+    const int64_t total = blocks_of_cta(a, tiles);
     Pos p, q;
     for (int64_t i = 0; i < total; i++) {
         if (!waitw(S, &S.full[p.s], p.ph, a.status) ||
-            (kPair == 2 && !waitw(S, &S.peer[p.s], p.ph, a.status)) ||
             !waitw(S, &S.acc_empty[q.s], q.ph ^ 1u, a.status)) {
             if (elect_one()) {
-                kPair == 2 ? umma_commit_pair(&S.done) : umma_commit(&S.done);
+                umma_commit(&S.done);
                 mbar_wait_bounded(&S.done, 0, kWaitNs);
             }
             return;
         }
         tc_fence_after();
-        const uint32_t st = smem_u32(ring) + (uint32_t)p.s * stage_bytes(kPair);
-        const uint64_t x = smem_desc(st + weight_bytes(kPair), 1024, 2), w = smem_desc(st, 1024, 2);
+        const uint32_t st = smem_u32(ring) + (uint32_t)p.s * kStage;
+        const uint64_t x = smem_desc(st + kWeights, 1024, 2), w = smem_desc(st, 1024, 2);
         const uint32_t d = tmem + (uint32_t)(q.s * kNW);
         if (elect_one()) {
 #pragma unroll
-            for (int j = 0; j < 4; j++) {        // 32 bytes of k a step: 2 units of 16 bytes
-                if (kPair == 2)
-                    umma_f8_pair(d, x + 2 * j, w + 2 * j, idesc, j > 0);
-                else
-                    umma_f8(d, x + 2 * j, w + 2 * j, idesc, j > 0);
-            }
-            kPair == 2 ? umma_commit_both(&S.acc_full[q.s]) : umma_commit(&S.acc_full[q.s]);
-            kPair == 2 ? umma_commit_both(&S.empty[p.s]) : umma_commit(&S.empty[p.s]);
+            for (int j = 0; j < 4; j++)          // 32 bytes of k a step: 2 units of 16 bytes
+                umma_f8(d, x + 2 * j, w + 2 * j, idesc, j > 0);
+            umma_commit(&S.acc_full[q.s]);
+            umma_commit(&S.empty[p.s]);
         }
         __syncwarp();
-        p.next(stages(kPair));
+        p.next(kStages);
         q.next(kAccs);
     }
 }
 
-// One thread of a pair's second CTA: its full stages are announced to the first.
-__device__ void announce(const TcArgs &a, Shared &S, int tiles) {
-    const int64_t total = (int64_t)tiles_of_cta<2>(tiles) * a.nkb;
-    Pos p;
-    for (int64_t i = 0; i < total; i++) {
-        if (!wait1(S, &S.full[p.s], p.ph, a.status)) return;
-        fence_proxy_async_smem();
-        mbar_arrive_at(&S.peer[p.s], 0);
-        p.next(stages(2));
-    }
-}
-
 // Warp 2: the scales of every block, in the order the epilogue takes them, copied into the ring.
-template <int kMode, int kPair>
-__device__ void scales(const TcArgs &a, Shared &S, int tiles, int rank) {
+template <int kMode>
+__device__ void scales(const TcArgs &a, Shared &S, int tiles) {
     const int lane = threadIdx.x & 31;
-    const int mine = tiles_of_cta<kPair>(tiles);
-    if (mine == 0) return;
     Pos p;
     int u = 0;                              // block within the group
-    Tile next = tile_at<kMode, kPair>(a, first_tile<kPair>(), rank);
-    for (int m = 0; m < mine; m++) {
+    int i = blockIdx.x;
+    if (i >= tiles) return;
+    Tile next = tile_at<kMode>(a, i);
+    for (; i < tiles; i += gridDim.x) {
         const Tile t = next;
         const float *as = a.as + t.slot + lane;
         const float *s0 = a.ws0 + t.e * a.ws_expert, *s1;
@@ -319,8 +286,7 @@ __device__ void scales(const TcArgs &a, Shared &S, int tiles, int rank) {
             s1 = t.rt * kNW + kSBlk < a.rows ? s0 + a.nkb : s0;    // past the last rows: not stored
         }
         const float *mine_ws = lane == 0 ? s0 : s1;
-        if (m + 1 < mine)
-            next = tile_at<kMode, kPair>(a, first_tile<kPair>() + (m + 1) * tile_step<kPair>(), rank);
+        if (i + (int)gridDim.x < tiles) next = tile_at<kMode>(a, i + gridDim.x);
 #pragma unroll 1
         for (int b = 0; b < a.nkb; b++) {
             if (u == 0 && !waitw(S, &S.sc_empty[p.s], p.ph ^ 1u, a.status)) {
@@ -383,8 +349,8 @@ __device__ __forceinline__ void store16(T *p, const float *acc) {
     }
 }
 
-template <int kMode, int kPair, typename T>
-__device__ void finish(const TcArgs &a, Shared &S, int tiles, int rank, uint32_t tmem) {
+template <int kMode, typename T>
+__device__ void finish(const TcArgs &a, Shared &S, int tiles, uint32_t tmem) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int quad = warp & 3, part = (warp - kEpiWarp0) >> 2;
     const int row = quad * 32 + lane;
@@ -393,13 +359,12 @@ __device__ void finish(const TcArgs &a, Shared &S, int tiles, int rank, uint32_t
     Pos q, p;
     int u = 0;                          // block within the scale ring's group
     uint32_t par = 0;
-    const int mine = tiles_of_cta<kPair>(tiles);
-    if (mine == 0) return;
-    Tile next = tile_at<kMode, kPair>(a, first_tile<kPair>(), rank);
-    for (int m = 0; m < mine; m++) {
+    int i = blockIdx.x;
+    if (i >= tiles) return;
+    Tile next = tile_at<kMode>(a, i);
+    for (; i < tiles; i += gridDim.x) {
         const Tile t = next;
-        if (m + 1 < mine)
-            next = tile_at<kMode, kPair>(a, first_tile<kPair>() + (m + 1) * tile_step<kPair>(), rank);
+        if (i + (int)gridDim.x < tiles) next = tile_at<kMode>(a, i + gridDim.x);
         float acc[2][32];
 #pragma unroll
         for (int j = 0; j < 32; j++) acc[0][j] = acc[1][j] = 0.f;
@@ -432,12 +397,7 @@ __device__ void finish(const TcArgs &a, Shared &S, int tiles, int rank, uint32_t
                 tc_fence_before();
             }
             __syncwarp();
-            if (lane == 0) {
-                if (kPair == 2)
-                    mbar_arrive_at(&S.acc_empty[q.s], 0);
-                else
-                    mbar_arrive(&S.acc_empty[q.s]);
-            }
+            if (lane == 0) mbar_arrive(&S.acc_empty[q.s]);
             q.next(kAccs);
             if (++u == kGroup) {
                 u = 0;
@@ -540,26 +500,23 @@ __device__ void finish(const TcArgs &a, Shared &S, int tiles, int rank, uint32_t
     }
 }
 
-template <int kMode, int kPair, typename T>
+template <int kMode, typename T>
 __global__ void __launch_bounds__(kThreads, 1)
     k_scaled_tc(const TcArgs a, const __grid_constant__ CUtensorMap w0,
                 const __grid_constant__ CUtensorMap w1, const __grid_constant__ CUtensorMap x,
                 const __grid_constant__ CUtensorMap x16) {
     extern __shared__ uint8_t raw[];
-    // the same offset in both CTAs of a pair: dynamic shared memory starts at one address
     uint8_t *ring = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
-    Shared &S = *reinterpret_cast<Shared *>(ring + (size_t)kRing);
+    Shared &S = *reinterpret_cast<Shared *>(ring + (size_t)kStages * kStage);
     const int warp = threadIdx.x >> 5;
-    const int rank = kPair == 2 ? (int)cluster_rank() : 0;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < stages(kPair); i++) {
+        for (int i = 0; i < kStages; i++) {
             mbar_init(&S.full[i], 1);
             mbar_init(&S.empty[i], 1);
-            mbar_init(&S.peer[i], 1);
         }
         for (int i = 0; i < kAccs; i++) {
             mbar_init(&S.acc_full[i], 1);
-            mbar_init(&S.acc_empty[i], kPair * kEpiWarps);
+            mbar_init(&S.acc_empty[i], kEpiWarps);
         }
         for (int i = 0; i < kScales; i++) {
             mbar_init(&S.sc_full[i], 32);
@@ -570,56 +527,40 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_barrier_init();
     }
     if (warp == 1) {
-        if (kPair == 2) {
-            tmem_alloc2(&S.tmem, kTmemCols);
-            tmem_relinquish2();
-        } else {
-            tmem_alloc(&S.tmem, kTmemCols);
-            tmem_relinquish();
-        }
+        tmem_alloc(&S.tmem, kTmemCols);
+        tmem_relinquish();
     }
     tc_fence_before();
     __syncthreads();
-    if (kPair == 2) cluster_sync();
     tc_fence_after();
     const uint32_t tmem = S.tmem;
-    constexpr int kSlice = kPair * kMT;
-    const int tiles = (kMode == kDense ? (a.M + kSlice - 1) / kSlice : *a.nslices) * a.row_tiles;
+    const int tiles = (kMode == kDense ? (a.M + kMT - 1) / kMT : *a.nslices) * a.row_tiles;
     if (warp < kEpiWarp0) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRoleRegs));
-        if (warp == 0) {
-            produce<kMode, kPair>(a, S, ring, tiles, rank, &w0, &w1, &x, &x16);
-        } else if (warp == 1) {
-            if (rank == 0)
-                multiply<kPair>(a, S, ring, tiles, tmem);
-            else if ((threadIdx.x & 31) == 0)
-                announce(a, S, tiles);
-        } else if (warp == 2) {
-            scales<kMode, kPair>(a, S, tiles, rank);
-        }
+        if (warp == 0)
+            produce<kMode>(a, S, ring, tiles, &w0, &w1, &x, &x16);
+        else if (warp == 1)
+            multiply(a, S, ring, tiles, tmem);
+        else if (warp == 2)
+            scales<kMode>(a, S, tiles);
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
-        finish<kMode, kPair, T>(a, S, tiles, rank, tmem);
+        finish<kMode, T>(a, S, tiles, tmem);
     }
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    // neither CTA of a pair leaves while the other's MMAs, commits or arrivals may reach it
-    if (kPair == 2) cluster_sync();
     if (warp == 1) {
         tc_fence_after();
-        if (kPair == 2)
-            tmem_dealloc2(tmem, kTmemCols);
-        else
-            tmem_dealloc(tmem, kTmemCols);
+        tmem_dealloc(tmem, kTmemCols);
     }
 }
 
-// The runs of up to `run` slots of every expert with tokens, ascending, the shared one's last: the
+// The runs of up to 128 slots of every expert with tokens, ascending, the shared one's last: the
 // tiles' token side.  One CTA.
 __global__ void __launch_bounds__(1024)
     k_scaled_slices(const int32_t *__restrict__ offsets, int E, int T, int k, int shared,
-                    int run, Job *slices, int32_t *nslices, uint32_t *status) {
+                    Job *slices, int32_t *nslices, uint32_t *status) {
     __shared__ int s_first[kMaxE];
     __shared__ int s_warp[33];
     const int A = T * k;
@@ -627,21 +568,21 @@ __global__ void __launch_bounds__(1024)
         const int o = offsets[e], o1 = offsets[e + 1];
         const bool fits = o >= 0 && o <= o1 && o1 <= A;      // else not what a router wrote
         if (!fits) set_status(status, MOE_ERR_BOUNDS);
-        s_first[e] = fits ? (o1 - o + run - 1) / run : 0;
+        s_first[e] = fits ? (o1 - o + kMT - 1) / kMT : 0;
     }
     __syncthreads();
     // overlapping runs of damaged offsets could pass the list's end: those are left out too
-    const int most = A / run + min(E, A);
+    const int most = A / kMT + min(E, A);
     const int n = min(block_exclusive_scan<1024>(s_first, E, s_warp), most);
     for (int e = threadIdx.x; e < E; e += 1024) {
         const int o = offsets[e], o1 = offsets[e + 1];
         if (!(o >= 0 && o <= o1 && o1 <= A)) continue;
-        for (int s = o, j = s_first[e]; s < o1 && j < most; s += run, j++)
-            slices[j] = Job{e, s, min(run, o1 - s), 0};
+        for (int s = o, j = s_first[e]; s < o1 && j < most; s += kMT, j++)
+            slices[j] = Job{e, s, min(kMT, o1 - s), 0};
     }
-    const int ns = shared ? (T + run - 1) / run : 0;
+    const int ns = shared ? (T + kMT - 1) / kMT : 0;
     for (int j = threadIdx.x; j < ns; j += 1024)
-        slices[n + j] = Job{E, A + j * run, min(run, T - j * run), 1};
+        slices[n + j] = Job{E, A + j * kMT, min(kMT, T - j * kMT), 1};
     if (threadIdx.x == 0) *nslices = n + ns;
 }
 
@@ -740,11 +681,11 @@ bool encode(CUtensorMap *m, const void *base, int cols, int64_t rows, int64_t st
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int kMode, int kPair, typename T>
+template <int kMode, typename T>
 cudaError_t run_tc(const TcArgs &a, const CUtensorMap &w0, const CUtensorMap &w1,
                    const CUtensorMap &x, const CUtensorMap &x16, int64_t most_tiles,
                    cudaStream_t st) {
-    auto kernel = k_scaled_tc<kMode, kPair, T>;
+    auto kernel = k_scaled_tc<kMode, T>;
     // the register split needs every register of the launch it was made for
     static const bool fits = [&] {
         cudaFuncAttributes at{};
@@ -754,31 +695,10 @@ cudaError_t run_tc(const TcArgs &a, const CUtensorMap &w0, const CUtensorMap &w1
     cudaError_t err = ensure_smem(kernel, kSmem);
     if (err != cudaSuccess) return err;
     const int sms = sm_count();
-    if (sms < kPair) return cudaErrorInvalidDevice;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(std::min<int64_t>(sms / kPair, most_tiles) * kPair));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kSmem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = kPair;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = kPair == 2 ? 1 : 0;
-    err = cudaLaunchKernelEx(&cfg, kernel, a, w0, w1, x, x16);
-    if (err != cudaSuccess) return err;
+    if (sms <= 0) return cudaErrorInvalidDevice;
+    kernel<<<(unsigned)std::min<int64_t>(sms, most_tiles), kThreads, kSmem, st>>>(a, w0, w1, x, x16);
     note_launches(1);
     return cudaGetLastError();
-}
-
-// Pairs of CTAs or single ones.
-template <int kMode, typename T>
-cudaError_t run_tc(bool pair, const TcArgs &a, const CUtensorMap &w0, const CUtensorMap &w1,
-                   const CUtensorMap &x, const CUtensorMap &x16, int64_t most_tiles,
-                   cudaStream_t st) {
-    return pair ? run_tc<kMode, 2, T>(a, w0, w1, x, x16, most_tiles, st)
-                : run_tc<kMode, 1, T>(a, w0, w1, x, x16, most_tiles, st);
 }
 
 size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
@@ -812,11 +732,6 @@ ExpertsWs experts_ws(const moe_scaled_weights &w, int T, int k) {
     return L;
 }
 
-bool use_pair(int M) { return M > kMT; }
-bool use_pair_experts(const moe_scaled_weights &w, int T, int k) {
-    return (int64_t)T * k > 4 * (int64_t)kMT * w.n_experts;
-}
-
 template <typename Y>
 cudaError_t run_combine(const ScaledExpertsArgs &e, const void *y, const float *ys, cudaStream_t st) {
     const moe_scaled_weights &w = e.w;
@@ -847,9 +762,8 @@ cudaError_t experts_tc(const ScaledExpertsArgs &e, uint8_t *ws, cudaStream_t st)
         !encode(&h, ws + L.hq, F, L.slots, F, 0, 128) ||
         !encode(&h16, ws + L.hq, F, L.slots, F, 0, 16))
         return cudaErrorInvalidValue;
-    const bool pair = use_pair_experts(w, e.T, e.k);
-    k_scaled_slices<<<1, 1024, 0, st>>>(e.offsets, w.n_experts, e.T, e.k, w.shared,
-                                        pair ? 2 * kMT : kMT, slices, nslices, e.status);
+    k_scaled_slices<<<1, 1024, 0, st>>>(e.offsets, w.n_experts, e.T, e.k, w.shared, slices,
+                                        nslices, e.status);
     note_launches(1);
     cudaError_t err = cudaGetLastError();
     if (err != cudaSuccess) return err;
@@ -870,7 +784,7 @@ cudaError_t experts_tc(const ScaledExpertsArgs &e, uint8_t *ws, cudaStream_t st)
     a.ws0 = w.d_gate_s;
     a.ws1 = w.d_up_s;
     a.ws_expert = (int64_t)sblocks(F) * sblocks(H);
-    err = run_tc<kGateUp, float>(pair, a, gate, up, x, x16, L.most_slices * a.row_tiles, st);
+    err = run_tc<kGateUp, float>(a, gate, up, x, x16, L.most_slices * a.row_tiles, st);
     if (err != cudaSuccess) return err;
     a.nkb = sblocks(F);
     a.rows = H;
@@ -882,19 +796,18 @@ cudaError_t experts_tc(const ScaledExpertsArgs &e, uint8_t *ws, cudaStream_t st)
     a.vec = true;
     const int64_t tiles = L.most_slices * a.row_tiles;
     if (e.out_dt == MOE_DT_F32) {
-        err = run_tc<kDown, float>(pair, a, down, down, h, h16, tiles, st);
+        err = run_tc<kDown, float>(a, down, down, h, h16, tiles, st);
         return err != cudaSuccess ? err : run_combine<float>(e, ws + L.y, nullptr, st);
     }
     a.ys = ys;
     // 2^y_exp * 65504 >= nkb * 128 * 448^2
     a.y_exp = (int)std::ceil(std::log2(a.nkb * (128.0 * 448.0 * 448.0) / 65504.0));
-    err = run_tc<kDown, __half>(pair, a, down, down, h, h16, tiles, st);
+    err = run_tc<kDown, __half>(a, down, down, h, h16, tiles, st);
     return err != cudaSuccess ? err : run_combine<__half>(e, ws + L.y, ys, st);
 }
 
 cudaError_t matmul_tc(const ScaledMatmulArgs &m, cudaStream_t st) {
     CUtensorMap b, x, x16;
-    const bool pair = use_pair(m.M);
     if (!encode(&b, m.b, m.K, m.N, m.ldb, 1, 128) || !encode(&x, m.a, m.K, m.M, m.lda, 0, 128) ||
         !encode(&x16, m.a, m.K, m.M, m.lda, 0, 16))
         return cudaErrorInvalidValue;
@@ -910,12 +823,11 @@ cudaError_t matmul_tc(const ScaledMatmulArgs &m, cudaStream_t st) {
     a.ldo = m.ldo;
     a.vec = (uintptr_t)m.out % 32 == 0 && m.ldo * dtype_bytes(m.dt) % 32 == 0 && m.N % 16 == 0;
     a.status = m.status;
-    const int slice = pair ? 2 * kMT : kMT;
-    const int64_t tiles = (int64_t)((m.M + slice - 1) / slice) * a.row_tiles;
+    const int64_t tiles = (int64_t)((m.M + kMT - 1) / kMT) * a.row_tiles;
     if (tiles > INT32_MAX) return cudaErrorInvalidValue;
     return with_dtype(m.dt, [&](auto *tag) {
         using E = std::remove_pointer_t<decltype(tag)>;
-        return run_tc<kDense, E>(pair, a, b, b, x, x16, tiles, st);
+        return run_tc<kDense, E>(a, b, b, x, x16, tiles, st);
     });
 }
 
