@@ -1,9 +1,21 @@
 // k_scored.cu -- routing by scores: softmax or sigmoid of the logits, a balance bias that takes
 // part in the choice alone, groups of experts of which the best stay, top-k, weights from the
-// chosen scores.
+// chosen scores; then the grouping of the (token, slot) pairs by expert.
 //
-// The order of the choice is that of 64-bit scores, so that a near-tie is decided as the formula
-// decides it, whatever the order of a sum or the last bits of an fp32 exponential would say.
+// The choice is that of 64-bit scores, so that a near-tie is decided as the formula decides it,
+// whatever the order of a sum or the last bits of an fp32 exponential would say.  Only what may
+// be chosen pays for 64 bits (k_scored_rows, a warp per token, the row in registers):
+//   - the k-th largest of the 32 lanes' own maxima is a bound that the k chosen reach, so the
+//     experts at or above it (for fp32 scores: above it less twice their error) hold the choice;
+//     there are seldom more than a dozen;
+//   - these candidates, one per lane, get 64-bit scores and are sorted by (value, id);
+//   - groups are ranked by fp32 sums, and by 64-bit ones where two lie within the error;
+//   - a row with more than 32 candidates (ties, mostly masked rows) takes 64-bit rounds over all.
+// Without a bias the order is that of the logits, which needs no scores.
+//
+// Grouping (the order of a3): counts per chunk of 64 tokens come out of the routing kernel's shared
+// memory, a second kernel turns them into places per chunk, a third writes the permutation.  Up to
+// one chunk is routed and grouped by one CTA in one launch.
 #include <math.h>
 
 #include "route_dev.cuh"
@@ -13,7 +25,10 @@ namespace moe {
 
 namespace {
 
-constexpr int kWarps = 4;      // tokens per CTA, a warp each
+constexpr int kWarps = 4;             // k_scored_wide: tokens per CTA, a warp each
+constexpr int kMaxNV = 32;            // experts per lane held in registers (1024 experts)
+// k_scored_rows: threads for a chunk of 64 tokens, a warp per token at a time
+constexpr int row_threads(int nv) { return nv <= 16 ? 1024 : 512; }
 
 __device__ __forceinline__ double warp_sum(double v) {
 #pragma unroll
@@ -30,15 +45,408 @@ struct Score {
     }
 };
 
-// One warp per token; its row of 64-bit values in shared memory.
-__global__ void __launch_bounds__(kWarps * 32) k_scored_topk(
-    const float *__restrict__ logits, int T, int E, int k, const moe_route_rule rule,
+// An order-preserving integer of a float (no NaN).
+__device__ __forceinline__ uint32_t order_key(float v) {
+    const uint32_t b = __float_as_uint(v + 0.0f);        // -0 and 0 are one value
+    return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+
+// Rounds of argmax over v[NV] per lane (element i of a lane is expert lane + 32 i), ties to the
+// lower id; returns the j-th choice in lane j.
+template <int NV, typename V>
+__device__ __noinline__ int select_rounds(V (&v)[NV], int k) {
+    const int lane = threadIdx.x & 31;
+    int mine = 0;
+    for (int j = 0; j < k; j++) {
+        V bv = -INFINITY;
+        int bi = INT_MAX;
+#pragma unroll
+        for (int i = 0; i < NV; i++)
+            if (v[i] > bv) {
+                bv = v[i];
+                bi = lane + 32 * i;
+            }
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) {
+            const V ov = __shfl_xor_sync(kFull, bv, o);
+            const int oi = __shfl_xor_sync(kFull, bi, o);
+            if (ov > bv || (ov == bv && oi < bi)) {
+                bv = ov;
+                bi = oi;
+            }
+        }
+        if (lane == j) mine = bi;
+#pragma unroll
+        for (int i = 0; i < NV; i++)
+            if (bi == lane + 32 * i) v[i] = -INFINITY;   // taken (every other value is larger)
+    }
+    return mine;
+}
+
+// Top two of a lane's share of its group: values come from get(element).
+template <typename V, typename Get>
+__device__ __forceinline__ V group_value(int per, int first, int step, int width, int top, Get get) {
+    V b1 = -INFINITY, b2 = -INFINITY;
+    for (int i = first; i < per; i += step) {
+        const V v = get(i);
+        b2 = fmax(b2, fmin(b1, v));
+        b1 = fmax(b1, v);
+    }
+    for (int o = width / 2; o >= 1; o >>= 1) {
+        const V o1 = __shfl_xor_sync(kFull, b1, o), o2 = __shfl_xor_sync(kFull, b2, o);
+        b2 = fmax(fmin(b1, o1), fmax(b2, o2));
+        b1 = fmax(b1, o1);
+    }
+    return top == 2 ? b1 + b2 : b1;
+}
+
+// Which groups stay (a bit each), from lane g's value of group g.  *gap: the smallest kept value
+// less the largest dropped one.
+template <typename V>
+__device__ __forceinline__ unsigned keep_groups(V mine, int n_group, int topk_group, V *gap) {
+    const int lane = threadIdx.x & 31;
+    int rank = 0;
+    for (int g = 0; g < n_group; g++) {
+        const V o = __shfl_sync(kFull, mine, g);
+        rank += o > mine || (o == mine && g < lane);
+    }
+    const bool in = lane < n_group, keep = in && rank < topk_group;
+    V lo = keep ? mine : (V)INFINITY, hi = in && !keep ? mine : (V)-INFINITY;
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) {
+        lo = fmin(lo, __shfl_xor_sync(kFull, lo, o));
+        hi = fmax(hi, __shfl_xor_sync(kFull, hi, o));
+    }
+    *gap = lo - hi;
+    return __ballot_sync(kFull, keep);
+}
+
+// One token by one warp.  row: E + E / 32 floats of shared memory of the warp's own (groups), cand:
+// 32 ints.  ids and w: k entries each (lane j writes entry j).
+template <int NV>
+__device__ void route_row(const float *__restrict__ src, int E, int k, const moe_route_rule &rule,
+                          float *row, int *cand, int32_t *ids, float *w, uint32_t *status) {
+    const int lane = threadIdx.x & 31;
+    const float *bias = rule.d_bias;
+    const bool sigmoid = rule.score == MOE_SCORE_SIGMOID;
+    float l[NV], top = -INFINITY, size = 0.f;
+    bool fin = true;
+#pragma unroll
+    for (int i = 0; i < NV; i++) {
+        const int e = lane + 32 * i;
+        l[i] = e < E ? __ldg(src + e) : -INFINITY;
+        fin = fin && (e >= E || isfinite(l[i]));
+        top = fmaxf(top, l[i]);
+    }
+    if (bias) {
+#pragma unroll
+        for (int i = 0; i < NV; i++) {
+            const int e = lane + 32 * i;
+            const float b = e < E ? __ldg(bias + e) : 0.f;
+            fin = fin && isfinite(b);
+            size = fmaxf(size, fabsf(b));
+        }
+    }
+    if (!__all_sync(kFull, fin)) {
+        if (lane < k) {
+            ids[lane] = lane;
+            w[lane] = __fdiv_rn(1.0f, (float)k);
+        }
+        if (lane == 0) set_status(status, MOE_ERR_NONFINITE);
+        return;
+    }
+    Score score{rule.score, 0.0, 1.0};
+    float inv32 = 1.0f;
+    if (!sigmoid) {
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+        score.top = top;
+        if (bias) {                       // the scores meet the bias: 64 bits
+            double sum = 0.0;
+#pragma unroll 1
+            for (int e = lane; e < E; e += 32) sum += exp((double)__ldg(src + e) - (double)top);
+            score.inv = 1.0 / warp_sum(sum);
+        } else if (!rule.renorm || rule.group_top == 2) {
+            float sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < NV; i++) sum += expf(l[i] - top);
+            score.inv = 1.0 / warp_sum((double)sum);
+        }
+        inv32 = (float)score.inv;
+    }
+    // fp32 values: scores plus bias, at most err from the 64-bit ones (a score is at most 1 and a
+    // few roundings off, the sum rounds once more)
+    const bool grouped = rule.n_group > 1;
+    const bool need = bias || (grouped && rule.group_top == 2);
+    float v[NV];
+    float err = 0.f;
+    if (need) {
+        if (bias) size = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(size)));
+        err = 0x1p-19f * (1.0f + size);
+#pragma unroll
+        for (int i = 0; i < NV; i++) {
+            const int e = lane + 32 * i;
+            const float s = sigmoid ? __fdividef(1.0f, 1.0f + __expf(-l[i]))
+                                    : __expf(l[i] - top) * inv32;
+            v[i] = e < E ? s + (bias ? __ldg(bias + e) : 0.f) : -INFINITY;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NV; i++) v[i] = l[i];
+    }
+    unsigned keep = ~0u;
+    int per = E;
+    if (grouped) {
+        per = E / rule.n_group;
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < NV; i++) {
+            const int e = lane + 32 * i;
+            if (e < E) row[e + (e >> 5)] = v[i];
+        }
+        __syncwarp();
+        int width = 32;                   // lanes per group
+        while (width > 1 && 32 / width < rule.n_group) width >>= 1;
+        const int g = lane / width, base = g * per;
+        const bool mine = g < rule.n_group;
+        float value = group_value<float>(mine ? per : 0, lane % width, width, width, rule.group_top,
+                                         [&](int i) {
+                                             const int e = base + i;
+                                             return row[e + (e >> 5)];
+                                         });
+        float gap;
+        keep = keep_groups(__shfl_sync(kFull, value, (lane * width) & 31), rule.n_group,
+                           rule.topk_group, &gap);
+        if (need && rule.topk_group < rule.n_group && gap <= 4.0f * err) {
+            const double exact = group_value<double>(
+                mine ? per : 0, lane % width, width, width, rule.group_top, [&](int i) {
+                    const int e = base + i;
+                    return score(__ldg(src + e)) + (bias ? (double)__ldg(bias + e) : 0.0);
+                });
+            double gap64;
+            keep = keep_groups(__shfl_sync(kFull, exact, (lane * width) & 31), rule.n_group,
+                               rule.topk_group, &gap64);
+        }
+    }
+    // the order's values; experts of dropped groups and past the end are out
+    if (!bias) err = 0.f;
+    const uint32_t magic = per > 1 ? (uint32_t)(0xffffffffu / (uint32_t)per + 1u) : 0u;
+    uint32_t best = 0;
+#pragma unroll
+    for (int i = 0; i < NV; i++) {
+        const int e = lane + 32 * i;
+        if (!bias) v[i] = l[i];
+        if (grouped) {
+            const int g = per > 1 ? (int)__umulhi((uint32_t)e, magic) : e;
+            if (!((keep >> (g & 31)) & 1u)) v[i] = -INFINITY;
+        }
+        best = max(best, order_key(v[i]));
+    }
+    // the k-th largest lane maximum (or a lower value, where lanes tie)
+    uint32_t bound = 0, left = best;
+    for (int j = 0; j < k; j++) {
+        bound = __reduce_max_sync(kFull, left);
+        if (left == bound) left = 0;
+    }
+    const uint32_t out_key = order_key(-INFINITY);
+    float least = -INFINITY;
+    if (bound > out_key) {
+        const float b = __uint_as_float(bound & 0x80000000u ? bound & 0x7fffffffu : ~bound);
+        least = err > 0.f ? b - 2.0f * err : b;
+    }
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < NV; i++) {
+        const bool in = v[i] >= least && v[i] > -INFINITY;
+        const unsigned m = __ballot_sync(kFull, in);
+        const int at = n + __popc(m & ((1u << lane) - 1u));
+        if (in && at < 32) cand[at] = lane + 32 * i;
+        n += __popc(m);
+    }
+    __syncwarp();
+    int my_id = 0;
+    if (n > 32) {
+        if (bias) {
+            double d[NV];
+#pragma unroll 1
+            for (int i = 0; i < NV; i++) {
+                const int e = lane + 32 * i;
+                const double x = e < E ? score(__ldg(src + e)) + (double)__ldg(bias + e) : 0.0;
+#pragma unroll
+                for (int q = 0; q < NV; q++)
+                    if (q == i) d[q] = v[q] > -INFINITY ? x : -INFINITY;
+            }
+            my_id = select_rounds<NV, double>(d, k);
+        } else {
+            float c[NV];                   // a copy: the call takes an address
+#pragma unroll
+            for (int i = 0; i < NV; i++) c[i] = v[i];
+            my_id = select_rounds<NV, float>(c, k);
+        }
+    } else {
+        // one candidate per lane, sorted by (value descending, id ascending)
+        my_id = lane < n ? cand[lane] : INT_MAX;
+        double d = -INFINITY;
+        if (lane < n) {
+            const float x = __ldg(src + my_id);
+            d = bias ? score(x) + (double)__ldg(bias + my_id) : (double)x;
+        }
+#pragma unroll
+        for (int size2 = 2; size2 <= 32; size2 <<= 1) {
+#pragma unroll
+            for (int o = size2 >> 1; o >= 1; o >>= 1) {
+                const double od = __shfl_xor_sync(kFull, d, o);
+                const int oi = __shfl_xor_sync(kFull, my_id, o);
+                const bool before = od > d || (od == d && oi < my_id);   // the other sorts first
+                const bool first = ((lane & size2) == 0) == ((lane & o) == 0);
+                if (before == first) {
+                    d = od;
+                    my_id = oi;
+                }
+            }
+        }
+    }
+    __syncwarp();
+    const double s = lane < k ? score(__ldg(src + my_id)) : 0.0;
+    double r = s;
+    if (rule.renorm) {
+        const double sum = warp_sum(s);
+        r = sum > 0.0 ? s / sum : 0.0;
+    }
+    if (lane < k) {
+        ids[lane] = my_id;
+        w[lane] = (float)(r * (double)rule.scale);
+    }
+}
+
+struct RouteOut {
+    int32_t *ids;
+    float *w;
+    int32_t *counts, *offsets, *perm, *inv_perm;
+    uint32_t *status;
+};
+
+// Places of a chunk's pairs, in ascending (token, slot): base[e] is the next place of expert e.
+// One warp.
+__device__ __forceinline__ void place_pairs(const int *pairs, int n, int first, int *base,
+                                            int32_t *perm, int32_t *inv_perm) {
+    const int lane = threadIdx.x & 31;
+    for (int a0 = 0; a0 < n; a0 += 32) {
+        const int a = a0 + lane;
+        const bool act = a < n;
+        const int e = act ? pairs[a] : -1;
+        const unsigned peers = __match_any_sync(kFull, e);
+        const int leader = __ffs(peers) - 1;
+        if (act) {
+            const int pos = base[e] + __popc(peers & ((1u << lane) - 1u));
+            perm[pos] = first + a;
+            if (inv_perm) inv_perm[first + a] = pos;
+        }
+        __syncwarp();
+        if (act && lane == leader) base[e] += __popc(peers);
+        __syncwarp();
+    }
+}
+
+// grid: chunks of 64 tokens.  One chunk in all (kWhole): also the grouping.
+template <int NV, bool kWhole>
+__global__ void __launch_bounds__(row_threads(NV), 1)
+    k_scored_rows(const float *__restrict__ logits, int T, int E, int k, const moe_route_rule rule,
+                  const RouteOut o, int32_t *chunk_counts) {
+    constexpr int kThreads = row_threads(NV), kTokens = kThreads / 32;
+    extern __shared__ float s_rows[];            // [warps][E + E / 32], when there are groups
+    __shared__ int s_cnt[NV * 32];
+    __shared__ int s_ids[kChunk * kMaxK];
+    __shared__ int s_cand[kTokens][32];
+    __shared__ int s_warp[33];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int t0 = blockIdx.x * kChunk, nt = min(kChunk, T - t0);
+    for (int e = threadIdx.x; e < E; e += kThreads) s_cnt[e] = 0;
+    for (int t = warp; t < nt; t += kTokens) {
+        int32_t *ids = s_ids + t * k;
+        route_row<NV>(logits + (size_t)(t0 + t) * E, E, k, rule,
+                      s_rows + (size_t)warp * (E + (E + 31) / 32), s_cand[warp], ids,
+                      o.w + (size_t)(t0 + t) * k, o.status);
+        __syncwarp();
+        if (lane < k) o.ids[(size_t)(t0 + t) * k + lane] = ids[lane];
+    }
+    __syncthreads();
+    for (int a = threadIdx.x; a < nt * k; a += kThreads) atomicAdd(&s_cnt[s_ids[a]], 1);
+    __syncthreads();
+    if constexpr (kWhole) {
+        for (int e = threadIdx.x; e < E; e += kThreads) o.counts[e] = s_cnt[e];
+        const int total = block_exclusive_scan<kThreads>(s_cnt, E, s_warp);
+        for (int e = threadIdx.x; e < E; e += kThreads) o.offsets[e] = s_cnt[e];
+        if (threadIdx.x == 0) o.offsets[E] = total;
+        __syncthreads();
+        if (warp == 0) place_pairs(s_ids, nt * k, 0, s_cnt, o.perm, o.inv_perm);
+    } else {
+        for (int e = threadIdx.x; e < E; e += kThreads)
+            chunk_counts[(size_t)blockIdx.x * E + e] = s_cnt[e];
+    }
+}
+
+// grid: 32 experts a CTA; thread (segment, expert).  Totals, and per chunk how many pairs of the
+// expert earlier chunks hold.
+__global__ void __launch_bounds__(1024)
+    k_scored_chunks(const int32_t *__restrict__ chunk_counts, int n_chunks, int E,
+                    int32_t *chunk_base, int32_t *counts) {
+    __shared__ int s_sum[32][33];
+    const int seg = threadIdx.x >> 5, lane = threadIdx.x & 31, e = blockIdx.x * 32 + lane;
+    const int per = (n_chunks + 31) / 32, c0 = seg * per, c1 = min(n_chunks, c0 + per);
+    int sum = 0;
+    if (e < E) {
+#pragma unroll 4
+        for (int c = c0; c < c1; c++) sum += __ldg(chunk_counts + (size_t)c * E + e);
+    }
+    s_sum[seg][lane] = sum;
+    __syncthreads();
+    int run = 0, all = 0;
+#pragma unroll
+    for (int s = 0; s < 32; s++) {
+        const int x = s_sum[s][lane];
+        run += s < seg ? x : 0;
+        all += x;
+    }
+    if (e >= E) return;
+    if (seg == 0) counts[e] = all;
+    for (int c = c0; c < c1; c++) {
+        chunk_base[(size_t)c * E + e] = run;
+        run += __ldg(chunk_counts + (size_t)c * E + e);
+    }
+}
+
+// grid: chunks.  Every CTA adds up the experts' totals (the first writes the offsets) and places
+// its chunk's pairs.
+__global__ void __launch_bounds__(256)
+    k_scored_place(int T, int E, int k, const int32_t *__restrict__ chunk_base, const RouteOut o) {
+    extern __shared__ int s_base[];              // [E]
+    __shared__ int s_ids[kChunk * kMaxK];
+    __shared__ int s_warp[33];
+    const int t0 = blockIdx.x * kChunk, n = min(kChunk, T - t0) * k;
+    for (int e = threadIdx.x; e < E; e += 256) s_base[e] = __ldg(o.counts + e);
+    for (int a = threadIdx.x; a < n; a += 256) s_ids[a] = __ldg(o.ids + (size_t)t0 * k + a);
+    __syncthreads();
+    const int total = block_exclusive_scan<256>(s_base, E, s_warp);
+    if (blockIdx.x == 0) {
+        for (int e = threadIdx.x; e < E; e += 256) o.offsets[e] = s_base[e];
+        if (threadIdx.x == 0) o.offsets[E] = total;
+        __syncthreads();
+    }
+    for (int e = threadIdx.x; e < E; e += 256)
+        s_base[e] += __ldg(chunk_base + (size_t)blockIdx.x * E + e);
+    __syncthreads();
+    if (threadIdx.x < 32) place_pairs(s_ids, n, t0 * k, s_base, o.perm, o.inv_perm);
+}
+
+// More experts than registers hold: one warp per token, its row of 64-bit values in shared memory.
+__global__ void __launch_bounds__(kWarps * 32) k_scored_wide(    const float *__restrict__ logits, int T, int E, int k, const moe_route_rule rule,
     int32_t *ids, float *w, uint32_t *status) {
-    extern __shared__ double s_rows[];
+    extern __shared__ double s_wide[];
     const int wid = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int t = blockIdx.x * kWarps + wid;
     if (t >= T) return;
-    double *row = s_rows + (size_t)wid * E;
+    double *row = s_wide + (size_t)wid * E;
     const float *src = logits + (size_t)t * E;
     const float *bias = rule.d_bias;
     ids += (size_t)t * k;
@@ -139,27 +547,62 @@ __global__ void __launch_bounds__(kWarps * 32) k_scored_topk(
     }
 }
 
+template <int NV>
+cudaError_t run_rows(const float *logits, int T, int E, int k, const moe_route_rule &rule,
+                     const RouteOut &o, int32_t *chunk_counts, cudaStream_t st) {
+    const size_t smem = rule.n_group > 1 ? (size_t)(row_threads(NV) / 32) * (E + (E + 31) / 32) * sizeof(float) : 0;
+    const int n_chunks = (T + kChunk - 1) / kChunk;
+    auto kernel = n_chunks == 1 ? k_scored_rows<NV, true> : k_scored_rows<NV, false>;
+    cudaError_t err = ensure_smem(kernel, smem);
+    if (err != cudaSuccess) return err;
+    kernel<<<n_chunks, row_threads(NV), smem, st>>>(logits, T, E, k, rule, o, chunk_counts);
+    note_launches(1);
+    return cudaGetLastError();
+}
+
 }  // namespace
 
 cudaError_t launch_route_scored(const float *logits, int T, int E, int k,
                                 const moe_route_rule &rule, int32_t *ids, float *w,
                                 int32_t *counts, int32_t *offsets, int32_t *perm,
                                 int32_t *inv_perm, uint32_t *status, void *ws, cudaStream_t st) {
-    const size_t smem = (size_t)kWarps * E * sizeof(double);
-    cudaError_t err = ensure_smem(k_scored_topk, smem);
+    const RouteWs L = route_ws(T, E, k);
+    uint8_t *p = static_cast<uint8_t *>(ws);
+    int32_t *chunk_counts = reinterpret_cast<int32_t *>(p + L.chunk_counts);
+    int32_t *chunk_base = reinterpret_cast<int32_t *>(p + L.chunk_base);
+    if (E > 32 * kMaxNV) {
+        const size_t smem = (size_t)kWarps * E * sizeof(double);
+        cudaError_t err = ensure_smem(k_scored_wide, smem);
+        if (err != cudaSuccess) return err;
+        k_scored_wide<<<(T + kWarps - 1) / kWarps, kWarps * 32, smem, st>>>(logits, T, E, k, rule,
+                                                                           ids, w, status);
+        note_launches(1);
+        err = cudaGetLastError();
+        if (err != cudaSuccess) return err;
+        return launch_group(ids, T, k, E, 0, counts, offsets, perm, inv_perm, chunk_counts,
+                            chunk_base, reinterpret_cast<Job *>(p + L.jobs),
+                            reinterpret_cast<int32_t *>(p + L.njobs), st);
+    }
+    const RouteOut o{ids, w, counts, offsets, perm, inv_perm, status};
+    cudaError_t err;
+    if (E <= 128)
+        err = run_rows<4>(logits, T, E, k, rule, o, chunk_counts, st);
+    else if (E <= 256)
+        err = run_rows<8>(logits, T, E, k, rule, o, chunk_counts, st);
+    else if (E <= 512)
+        err = run_rows<16>(logits, T, E, k, rule, o, chunk_counts, st);
+    else
+        err = run_rows<kMaxNV>(logits, T, E, k, rule, o, chunk_counts, st);
     if (err != cudaSuccess) return err;
-    k_scored_topk<<<(T + kWarps - 1) / kWarps, kWarps * 32, smem, st>>>(logits, T, E, k, rule, ids,
-                                                                       w, status);
+    const int n_chunks = (T + kChunk - 1) / kChunk;
+    if (n_chunks == 1) return cudaSuccess;
+    k_scored_chunks<<<(E + 31) / 32, 1024, 0, st>>>(chunk_counts, n_chunks, E, chunk_base, counts);
     note_launches(1);
     err = cudaGetLastError();
     if (err != cudaSuccess) return err;
-    const RouteWs L = route_ws(T, E, k);
-    uint8_t *p = static_cast<uint8_t *>(ws);
-    return launch_group(ids, T, k, E, 0, counts, offsets, perm, inv_perm,
-                        reinterpret_cast<int32_t *>(p + L.chunk_counts),
-                        reinterpret_cast<int32_t *>(p + L.chunk_base),
-                        reinterpret_cast<Job *>(p + L.jobs),
-                        reinterpret_cast<int32_t *>(p + L.njobs), st);
+    k_scored_place<<<n_chunks, 256, (size_t)E * sizeof(int), st>>>(T, E, k, chunk_base, o);
+    note_launches(1);
+    return cudaGetLastError();
 }
 
 }  // namespace moe
