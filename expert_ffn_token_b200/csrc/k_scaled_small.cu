@@ -9,8 +9,19 @@
 // 64-byte half block, straight into the fragments of two MMAs, and the activations are permuted
 // likewise.  No shared memory, no conversion of weights.
 //
-// The weights of 16 rows are split over k among a CTA's 8 warps; their partial sums meet in
-// shared memory in the order of the warps, so results repeat.
+// Where there are few rows to read, the weights of 16 rows are split over k among a CTA's 8 warps,
+// whose partial sums meet in shared memory in the order of the warps, so results repeat.
+//
+// The experts' layer, one token (two kernels): k_one_gateup splits 16 gate and 16 up rows of one
+// routed expert over k, every warp quantising the blocks of x that it needs; k_one_down gives 16
+// output rows of all the token's experts to one CTA, which combines them, and starts its weight
+// loads before the first kernel has ended.
+// 2 to 8 tokens (three kernels): k_few_prep lists the distinct experts with the tokens routed to
+// them and quantises x once; k_few_gateup takes 128 ffn values of one expert per CTA, 16 rows and
+// all of k per warp, so that h can be quantised in place; k_few_down takes 16 output rows over all
+// experts.  An expert's rows are read once for all its tokens, which are the MMA's columns.
+#include <algorithm>
+
 #include "ptx.cuh"
 #include "scaled.cuh"
 
@@ -20,7 +31,6 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kTile = 16;                 // weight rows per CTA
-constexpr int kPitch = kSBlk + 16;        // bytes per activation row in shared memory
 
 // One 64-byte half block: rows g (lo) and g + 8 (hi), columns' 16 bytes x.
 __device__ __forceinline__ void mma64(float (&c)[4], const uint4 &lo, const uint4 &hi,
@@ -37,11 +47,17 @@ __device__ __forceinline__ void mma64(float (&c)[4], const uint4 &lo, const uint
         : "r"(lo.z), "r"(hi.z), "r"(lo.w), "r"(hi.w), "r"(x.z), "r"(x.w));
 }
 
-__device__ __forceinline__ uint4 ldg_stream(const uint8_t *p) {
+// 16 bytes at p, or zeros: one predicated load, so that a run of them issues without a branch or a
+// use in between (with the bytes masked as they came, a block's eight loads took 4 us).
+__device__ __forceinline__ uint4 ldg16_if(const uint8_t *p, bool in) {
     uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.u32 p, %5, 0;\n\t"
+        "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+        "@p ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];\n\t}"
+        : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+        : "l"(p), "r"((uint32_t)in));
     return v;
 }
 
@@ -56,13 +72,20 @@ __device__ __forceinline__ uint4 keep_bytes(uint4 v, int n) {
     return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
-// 16 bytes of row p at column k of K columns, zeros past the end (the row's stride is a multiple
-// of 16, so a chunk that starts inside it lies inside it).
-__device__ __forceinline__ uint4 row16(const uint8_t *p, int k, int K) {
-    if (!p || k >= K) return make_uint4(0u, 0u, 0u, 0u);
-    const uint4 v = ldg_stream(p + k);
-    return K - k >= 16 ? v : keep_bytes(v, K - k);
-}
+// One block's 16 bytes per half of a row (at column k and k + 64 of K columns; zeros past the end,
+// where K is a multiple of 16 or the bytes are cut afterwards: the row's stride is a multiple of
+// 16, so a chunk that starts inside it lies inside it).
+struct Half2 {
+    uint4 a, b;
+    __device__ __forceinline__ void load(const uint8_t *p, bool row, int k, int K) {
+        a = ldg16_if(p + k, row && k < K);
+        b = ldg16_if(p + k + 64, row && k + 64 < K);
+    }
+    __device__ __forceinline__ void cut(int k, int K) {
+        a = keep_bytes(a, K - k);
+        b = keep_bytes(b, K - k - 64);
+    }
+};
 
 // The partial sums red[warp][col * 16 + row] of entry i, added in warp order.
 __device__ __forceinline__ float sum_warps(const float (*red)[kTile * 8], int i) {
@@ -87,27 +110,49 @@ __global__ void __launch_bounds__(kWarps * 32) k_scaled_rows(const ScaledMatmulA
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, tig = lane & 3;
     const int n0 = blockIdx.x * kTile, m0 = blockIdx.y * 8;
     const int nb = sblocks(a.K);
-    const uint8_t *lo = n0 + g < a.N ? a.b + (int64_t)(n0 + g) * a.ldb : nullptr;
-    const uint8_t *hi = n0 + g + 8 < a.N ? a.b + (int64_t)(n0 + g + 8) * a.ldb : nullptr;
-    const uint8_t *xr = m0 + g < a.M ? a.a + (int64_t)(m0 + g) * a.lda : nullptr;
+    const uint8_t *lo = a.b + (int64_t)min(n0 + g, a.N - 1) * a.ldb;
+    const uint8_t *hi = a.b + (int64_t)min(n0 + g + 8, a.N - 1) * a.ldb;
+    const uint8_t *xr = a.a + (int64_t)min(m0 + g, a.M - 1) * a.lda;
     const float *ws = a.bs + (int64_t)(n0 / kSBlk) * nb;
     const int c0 = m0 + 2 * tig, c1 = c0 + 1;
     float acc[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int b = warp; b < nb; b += kWarps) {
+    struct Block {
+        Half2 l, h, x;
+        float sw, s0, s1;
+    } q[2];
+    auto load = [&](Block &k, int b) {
         const int k0 = b * kSBlk + 16 * tig;
-        const uint4 l0 = row16(lo, k0, a.K), l1 = row16(lo, k0 + 64, a.K);
-        const uint4 h0 = row16(hi, k0, a.K), h1 = row16(hi, k0 + 64, a.K);
-        const uint4 x0 = row16(xr, k0, a.K), x1 = row16(xr, k0 + 64, a.K);
-        const float sw = __ldg(ws + b);
-        const float s0 = c0 < a.M ? __ldg(a.as + b * a.ldas + c0) * sw : 0.f;
-        const float s1 = c1 < a.M ? __ldg(a.as + b * a.ldas + c1) * sw : 0.f;
+        const bool in = b < nb;
+        k.l.load(lo, in && n0 + g < a.N, k0, a.K);
+        k.h.load(hi, in && n0 + g + 8 < a.N, k0, a.K);
+        k.x.load(xr, in && m0 + g < a.M, k0, a.K);
+        k.sw = in ? __ldg(ws + b) : 0.f;
+        k.s0 = in && c0 < a.M ? __ldg(a.as + b * a.ldas + c0) : 0.f;
+        k.s1 = in && c1 < a.M ? __ldg(a.as + b * a.ldas + c1) : 0.f;
+    };
+    auto add = [&](Block &k, int b) {
+        if (b >= nb) return;
+        const int k0 = b * kSBlk + 16 * tig;
+        if ((b + 1) * kSBlk > a.K) {
+            k.l.cut(k0, a.K);
+            k.h.cut(k0, a.K);
+            k.x.cut(k0, a.K);
+        }
         float c[4] = {0.f, 0.f, 0.f, 0.f};
-        mma64(c, l0, h0, x0);
-        mma64(c, l1, h1, x1);
+        mma64(c, k.l.a, k.h.a, k.x.a);
+        mma64(c, k.l.b, k.h.b, k.x.b);
+        const float s0 = k.s0 * k.sw, s1 = k.s1 * k.sw;
         acc[0] = fmaf(c[0], s0, acc[0]);
         acc[1] = fmaf(c[1], s1, acc[1]);
         acc[2] = fmaf(c[2], s0, acc[2]);
         acc[3] = fmaf(c[3], s1, acc[3]);
+    };
+    load(q[0], warp);
+    for (int b = warp; b < nb; b += 2 * kWarps) {
+        load(q[1], b + kWarps);
+        add(q[0], b);
+        load(q[0], b + 2 * kWarps);
+        add(q[1], b + kWarps);
     }
     put_frag(red[warp], acc, g, tig);
     __syncthreads();
@@ -119,23 +164,233 @@ __global__ void __launch_bounds__(kWarps * 32) k_scaled_rows(const ScaledMatmulA
     }
 }
 
-// ------------------------------------------------------------------ the experts
+// ------------------------------------------------------------------ the experts, one token
 
-// The distinct experts of the batch, in order of first appearance in ids, then the shared one:
-// job j's expert, and per token the weight of its output (the sum over the token's slots that
-// name the expert) with a bit telling whether it is routed there at all.  All threads of the CTA;
-// s_ids holds T * k entries, at most one per thread.
-struct Jobs {
-    int n;
-    int expert[kSmallT * kMaxK + 1];
-    int count[kWarps + 1];
+// Weight rows g and g + 8 of one block of k.
+struct Rows16 {
+    Half2 lo, hi;
+    __device__ __forceinline__ void load(const uint8_t *p, int64_t pitch, bool in, int k, int K) {
+        lo.load(p, in, k, K);
+        hi.load(p + 8 * pitch, in, k, K);
+    }
+    __device__ __forceinline__ void multiply(float (&c)[4], const uint4 &x0, const uint4 &x1) const {
+        mma64(c, lo.a, hi.a, x0);
+        mma64(c, lo.b, hi.b, x1);
+    }
 };
 
-__device__ __forceinline__ void build_jobs(const ScaledExpertsArgs &a, Jobs &J, int *s_ids) {
-    const int A = a.T * a.k, i = threadIdx.x, lane = i & 31, warp = i >> 5;
+__device__ __forceinline__ uint32_t byte_word(uint32_t v, int src) {
+    return __shfl_sync(0xffffffffu, v, src);
+}
+// The activation fragment of one token from the packed bytes that quant_block left in the lanes
+// (lane l: bytes 4 l .. 4 l + 3): column 0 is the token, the others are zero.
+__device__ __forceinline__ void one_column(uint32_t p, uint4 &x0, uint4 &x1) {
+    const int lane = threadIdx.x & 31, s = 4 * (lane & 3);
+    const uint4 a = make_uint4(byte_word(p, s), byte_word(p, s + 1), byte_word(p, s + 2),
+                               byte_word(p, s + 3));
+    const uint4 b = make_uint4(byte_word(p, 16 + s), byte_word(p, 17 + s), byte_word(p, 18 + s),
+                               byte_word(p, 19 + s));
+    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+    x0 = lane < 4 ? a : zero;
+    x1 = lane < 4 ? b : zero;
+}
+
+// Slot j's expert: the token's j-th id, the shared expert behind them; -1 (reported) out of range.
+__device__ __forceinline__ int one_expert(const ScaledExpertsArgs &a, int j) {
+    if (j == a.k) return a.w.n_experts;
+    const int e = __ldg(a.ids + j);
+    if (e >= 0 && e < a.w.n_experts) return e;
+    set_status(a.status, MOE_ERR_BOUNDS);
+    return -1;
+}
+
+// grid (ffn / 16, slots): h of 16 rows of one slot's expert.
+template <typename T>
+__global__ void __launch_bounds__(kWarps * 32) k_one_gateup(const ScaledExpertsArgs a) {
+    __shared__ float red[2][kWarps][kTile];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, tig = lane & 3;
+    ptx::launch_dependents();
+    const int j = blockIdx.y, e = one_expert(a, j);
+    if (e < 0) return;
+    const int H = a.w.hidden, F = a.w.ffn, hb = sblocks(H);
+    const int f0 = blockIdx.x * kTile;
+    const int64_t r0 = (int64_t)e * F + f0 + g;
+    const uint8_t *gp = a.w.d_gate + r0 * H, *up = a.w.d_up + r0 * H;
+    const int64_t sb = ((int64_t)e * sblocks(F) + f0 / kSBlk) * hb;
+    const float *gs = a.w.d_gate_s + sb, *us = a.w.d_up_s + sb;
+    float ag[2] = {0.f, 0.f}, au[2] = {0.f, 0.f};      // rows g and g + 8
+    for (int b = warp; b < hb; b += kWarps) {
+        Rows16 wg, wu;
+        wg.load(gp, H, true, b * kSBlk + 16 * tig, H);
+        wu.load(up, H, true, b * kSBlk + 16 * tig, H);
+        const float sg = __ldg(gs + b), su = __ldg(us + b);
+        const int c = b * kSBlk + 4 * lane;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (c < H) v = load4(static_cast<const T *>(a.x) + c);
+        float s;
+        bool fin;
+        const uint32_t p = quant_block(v, &s, &fin);
+        if (!fin && lane == 0) set_status(a.status, MOE_ERR_NONFINITE);
+        uint4 x0, x1;
+        one_column(p, x0, x1);
+        float cg[4] = {0.f, 0.f, 0.f, 0.f}, cu[4] = {0.f, 0.f, 0.f, 0.f};
+        wg.multiply(cg, x0, x1);
+        wu.multiply(cu, x0, x1);
+        ag[0] = fmaf(cg[0], s * sg, ag[0]);
+        ag[1] = fmaf(cg[2], s * sg, ag[1]);
+        au[0] = fmaf(cu[0], s * su, au[0]);
+        au[1] = fmaf(cu[2], s * su, au[1]);
+    }
+    if (tig == 0) {                                     // column 0 of the fragments
+        red[0][warp][g] = ag[0];
+        red[0][warp][g + 8] = ag[1];
+        red[1][warp][g] = au[0];
+        red[1][warp][g + 8] = au[1];
+    }
+    __syncthreads();
+    if (threadIdx.x < kTile) {
+        float gv = 0.f, uv = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; w++) {
+            gv += red[0][w][threadIdx.x];
+            uv += red[1][w][threadIdx.x];
+        }
+        a.h[(int64_t)j * F + f0 + threadIdx.x] = __fdiv_rn(gv, 1.0f + expf(-gv)) * uv;
+    }
+}
+
+// grid (hidden / 16): 16 output rows over every slot's expert.  Items (slot, block of ffn) go round
+// the warps, four at a time.
+template <typename T>
+__global__ void __launch_bounds__(kWarps * 32) k_one_down(const ScaledExpertsArgs a) {
+    constexpr int kBatch = 4;
+    __shared__ float red[kWarps][kTile];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, tig = lane & 3;
+    const int H = a.w.hidden, F = a.w.ffn, fb = sblocks(F);
+    const int n0 = blockIdx.x * kTile;
+    const int items = (a.k + a.w.shared) * fb;
+    Rows16 w[kBatch];
+    float c[kBatch];                       // weight scale times routing weight
+    int slot[kBatch];
+    auto load = [&](int first) {
+#pragma unroll
+        for (int u = 0; u < kBatch; u++) {
+            const int i = first + u * kWarps;
+            const int j = min(i, items - 1) / fb, b = min(i, items - 1) - j * fb;
+            const int e = i < items ? one_expert(a, j) : -1;
+            slot[u] = e >= 0 ? j : -1;
+            const int64_t x = max(e, 0);
+            w[u].load(a.w.d_down + (x * H + n0 + g) * F, F, e >= 0, b * kSBlk + 16 * tig, F);
+            const float r = j < a.k ? __ldg(a.rw + j) : a.gate ? __ldg(a.gate) : 1.0f;
+            c[u] = __ldg(a.w.d_down_s + (x * sblocks(H) + n0 / kSBlk) * fb + b) * r;
+        }
+    };
+    load(warp);
+    ptx::grid_dependency_wait();           // h is complete
+    float acc[2] = {0.f, 0.f};
+    for (int first = warp; first < items; first += kBatch * kWarps) {
+        if (first != warp) load(first);
+        float4 h[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; u++) {
+            const int i = first + u * kWarps, col = (i % fb) * kSBlk + 4 * lane;
+            h[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (slot[u] >= 0 && col < F)
+                h[u] = __ldcg(reinterpret_cast<const float4 *>(a.h + (int64_t)slot[u] * F + col));
+        }
+#pragma unroll
+        for (int u = 0; u < kBatch; u++) {
+            if (slot[u] < 0) continue;
+            float s;
+            bool fin;
+            const uint32_t p = quant_block(h[u], &s, &fin);
+            if (!fin && lane == 0) set_status(a.status, MOE_ERR_NONFINITE);
+            uint4 x0, x1;
+            one_column(p, x0, x1);
+            float cc[4] = {0.f, 0.f, 0.f, 0.f};
+            w[u].multiply(cc, x0, x1);
+            acc[0] = fmaf(cc[0], s * c[u], acc[0]);
+            acc[1] = fmaf(cc[2], s * c[u], acc[1]);
+        }
+    }
+    if (tig == 0) {
+        red[warp][g] = acc[0];
+        red[warp][g + 8] = acc[1];
+    }
+    __syncthreads();
+    if (threadIdx.x < kTile) {
+        float s = 0.f;
+#pragma unroll
+        for (int q = 0; q < kWarps; q++) s += red[q][threadIdx.x];
+        static_cast<T *>(a.out)[n0 + threadIdx.x] = from_f32<T>(s);
+    }
+}
+
+// ------------------------------------------------------------------ the experts, 2 to 8 tokens
+
+// What k_few_prep leaves in the workspace.
+struct FewWs {
+    uint8_t *xq;         // [8][hidden]
+    float *xs;           // [blocks][8]
+    int32_t *njobs;
+    int32_t *expert;     // [jobs]: the distinct experts, the shared one last
+    int32_t *mask;       // [jobs]: a bit per token routed there
+    float *weight;       // [jobs][8]: the weight of the expert's output per token
+    uint8_t *hq;         // [jobs][8][ffn]
+    float *hs;           // [jobs][8][blocks of ffn]
+};
+
+size_t few_layout(int T, int k, int shared, int H, int F, uint8_t *base, FewWs *out) {
+    const size_t jobs = (size_t)T * k + (shared ? 1 : 0);
+    size_t p = 0;
+    auto take = [&](size_t bytes) {
+        uint8_t *r = base + p;
+        p = (p + bytes + 255) & ~size_t(255);
+        return r;
+    };
+    FewWs w{};
+    w.xq = take((size_t)kSmallT * H);
+    w.xs = reinterpret_cast<float *>(take((size_t)sblocks(H) * kSmallT * 4));
+    w.njobs = reinterpret_cast<int32_t *>(take(4));
+    w.expert = reinterpret_cast<int32_t *>(take(jobs * 4));
+    w.mask = reinterpret_cast<int32_t *>(take(jobs * 4));
+    w.weight = reinterpret_cast<float *>(take(jobs * kSmallT * 4));
+    w.hq = take(jobs * kSmallT * F);
+    w.hs = reinterpret_cast<float *>(take(jobs * kSmallT * sblocks(F) * 4));
+    if (out) *out = w;
+    return p;
+}
+
+// CTA 0 lists the jobs; the others quantise a block of a token per warp.
+template <typename T>
+__global__ void __launch_bounds__(256) k_few_prep(const ScaledExpertsArgs a, const FewWs f) {
+    ptx::launch_dependents();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (blockIdx.x > 0) {
+        const int H = a.w.hidden, hb = sblocks(H);
+        const int unit = ((int)blockIdx.x - 1) * 8 + warp;
+        const int t = unit / hb, b = unit - t * hb;
+        if (t >= a.T) return;
+        const int c = b * kSBlk + 4 * lane;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (c < H) v = load4(static_cast<const T *>(a.x) + (int64_t)t * H + c);
+        float s;
+        bool fin;
+        const uint32_t p = quant_block(v, &s, &fin);
+        if (c < H) *reinterpret_cast<uint32_t *>(f.xq + (int64_t)t * H + c) = p;
+        if (lane == 0) {
+            f.xs[b * kSmallT + t] = s;
+            if (!fin) set_status(a.status, MOE_ERR_NONFINITE);
+        }
+        return;
+    }
+    // the distinct experts in order of first appearance; a thread per (token, slot) pair
+    __shared__ int s_ids[kSmallT * kMaxK];
+    __shared__ int s_count[8];
+    const int A = a.T * a.k, i = threadIdx.x;
     int e = -1;
     if (i < A) {
-        e = a.ids[i];
+        e = __ldg(a.ids + i);
         if (e < 0 || e >= a.w.n_experts) {
             e = -1;
             set_status(a.status, MOE_ERR_BOUNDS);
@@ -143,201 +398,223 @@ __device__ __forceinline__ void build_jobs(const ScaledExpertsArgs &a, Jobs &J, 
         s_ids[i] = e;
     }
     __syncthreads();
-    bool first = i < A && e >= 0;
+    bool first = e >= 0;
     for (int b = 0; b < i && first; b++) first = s_ids[b] != e;
     const unsigned m = __ballot_sync(0xffffffffu, first);
-    if (lane == 0) J.count[warp] = __popc(m);
+    if (lane == 0) s_count[warp] = __popc(m);
     __syncthreads();
     int base = 0, total = 0;
 #pragma unroll
-    for (int w = 0; w < kWarps; w++) {
-        base += w < warp ? J.count[w] : 0;
-        total += J.count[w];
+    for (int w = 0; w < 8; w++) {
+        base += w < warp ? s_count[w] : 0;
+        total += s_count[w];
     }
-    if (first) J.expert[base + __popc(m & ((1u << lane) - 1u))] = e;
+    if (first) {
+        const int j = base + __popc(m & ((1u << lane) - 1u));
+        unsigned mask = 0;
+        for (int t = 0; t < a.T; t++) {
+            float w = 0.f;                 // a token that names the expert twice adds both weights
+            for (int q = 0; q < a.k; q++) {
+                if (s_ids[t * a.k + q] != e) continue;
+                mask |= 1u << t;
+                w += __ldg(a.rw + t * a.k + q);
+            }
+            f.weight[j * kSmallT + t] = w;
+        }
+        f.expert[j] = e;
+        f.mask[j] = (int)mask;
+    }
     if (i == 0) {
-        if (a.w.shared) J.expert[total] = a.w.n_experts;
-        J.n = total + (a.w.shared ? 1 : 0);
-    }
-    __syncthreads();
-}
-
-// Whether token t is routed to expert e, and with what weight.
-__device__ __forceinline__ bool routed(const ScaledExpertsArgs &a, const int *s_ids, int e, int t,
-                                       float *w) {
-    if (e == a.w.n_experts) {
-        *w = a.gate ? a.gate[t] : 1.0f;
-        return true;
-    }
-    bool on = false;
-    float s = 0.f;
-    for (int j = 0; j < a.k; j++) {
-        if (s_ids[t * a.k + j] != e) continue;
-        on = true;
-        s += a.rw[t * a.k + j];
-    }
-    *w = s;
-    return on;
-}
-
-// Activation columns of one block for a warp: 8 rows of e4m3 bytes and their scales.
-struct __align__(16) Cols {
-    uint8_t q[8 * kPitch];
-    float s[8];
-};
-
-__device__ __forceinline__ void put_col(Cols &C, int t, float4 v, uint32_t *status) {
-    const int lane = threadIdx.x & 31;
-    float s;
-    bool fin;
-    const uint32_t p = quant_block(v, &s, &fin);
-    *reinterpret_cast<uint32_t *>(C.q + t * kPitch + 4 * lane) = p;
-    if (lane == 0) {
-        C.s[t] = s;
-        if (!fin) set_status(status, MOE_ERR_NONFINITE);
+        *f.njobs = total + a.w.shared;
+        if (a.w.shared) {
+            f.expert[total] = a.w.n_experts;
+            f.mask[total] = (1 << a.T) - 1;
+            for (int t = 0; t < a.T; t++)
+                f.weight[total * kSmallT + t] = a.gate ? __ldg(a.gate + t) : 1.0f;
+        }
     }
 }
 
-// grid (ffn / 16, most jobs): h of 16 rows of one job's expert for the tokens routed to it.
-template <typename T>
-__global__ void __launch_bounds__(kWarps * 32) k_small_gateup(const ScaledExpertsArgs a) {
-    __shared__ float red[2][kWarps][kTile * 8];
-    __shared__ Cols cols[kWarps];
-    __shared__ Jobs J;
-    __shared__ int s_ids[kSmallT * kMaxK];
+// 16 bytes that a kernel before this one wrote, or zeros.
+__device__ __forceinline__ uint4 ldcg16_if(const uint8_t *p, bool in) {
+    uint4 v;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.u32 p, %5, 0;\n\t"
+        "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+        "@p ld.global.cg.v4.u32 {%0,%1,%2,%3}, [%4];\n\t}"
+        : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+        : "l"(p), "r"((uint32_t)in)
+        : "memory");
+    return v;
+}
+
+// grid (blocks of ffn, most jobs): 128 ffn values of one expert, a warp per 16; h quantised.
+__global__ void __launch_bounds__(kWarps * 32) k_few_gateup(const ScaledExpertsArgs a, const FewWs f) {
+    __shared__ uint32_t s_max[kWarps][8];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, tig = lane & 3;
+    ptx::grid_dependency_wait();
     ptx::launch_dependents();
-    for (int i = threadIdx.x; i < kWarps * (int)sizeof(Cols) / 4; i += blockDim.x)
-        reinterpret_cast<uint32_t *>(cols)[i] = 0u;
-    build_jobs(a, J, s_ids);
     const int j = blockIdx.y;
-    if (j >= J.n) return;
-    const int e = J.expert[j];
-    const int H = a.w.hidden, F = a.w.ffn, hb = sblocks(H);
-    const int f0 = blockIdx.x * kTile;
-    const int64_t r0 = (int64_t)e * F + f0;
-    const uint8_t *wg = a.w.d_gate + r0 * H, *wu = a.w.d_up + r0 * H;
-    const int64_t sb = ((int64_t)e * sblocks(F) + f0 / kSBlk) * hb;
-    const float *gs = a.w.d_gate_s + sb, *us = a.w.d_up_s + sb;
-    unsigned on = 0;
-    for (int t = 0; t < a.T; t++) {
-        float w;
-        if (routed(a, s_ids, e, t, &w)) on |= 1u << t;
-    }
-    Cols &C = cols[warp];
-    float ag[4] = {0.f, 0.f, 0.f, 0.f}, au[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int b = warp; b < hb; b += kWarps) {
-        const int k0 = b * kSBlk + 16 * tig;
-        const uint8_t *g0 = wg + (int64_t)g * H, *g1 = g0 + 8 * (int64_t)H;
-        const uint8_t *u0 = wu + (int64_t)g * H, *u1 = u0 + 8 * (int64_t)H;
-        const uint4 w0 = row16(g0, k0, H), w1 = row16(g1, k0, H);
-        const uint4 w2 = row16(g0, k0 + 64, H), w3 = row16(g1, k0 + 64, H);
-        const uint4 v0 = row16(u0, k0, H), v1 = row16(u1, k0, H);
-        const uint4 v2 = row16(u0, k0 + 64, H), v3 = row16(u1, k0 + 64, H);
-        const float sg = __ldg(gs + b), su = __ldg(us + b);
-        const int c = b * kSBlk + 4 * lane;
-        for (int t = 0; t < a.T; t++) {
-            if (!((on >> t) & 1u)) continue;
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (c < H) v = load4(static_cast<const T *>(a.x) + (int64_t)t * H + c);
-            put_col(C, t, v, a.status);
+    if (j >= __ldcg(f.njobs)) return;
+    const int e = __ldcg(f.expert + j);
+    const unsigned mask = (unsigned)__ldcg(f.mask + j);
+    const int H = a.w.hidden, F = a.w.ffn, hb = sblocks(H), fb = sblocks(F);
+    const int f0 = blockIdx.x * kSBlk + warp * kTile;
+    float hv[4] = {0.f, 0.f, 0.f, 0.f};    // rows g, g + 8 by columns 2 tig, 2 tig + 1
+    if (f0 < F) {
+        const int64_t r0 = (int64_t)e * F + f0 + g;
+        const uint8_t *gp = a.w.d_gate + r0 * H, *up = a.w.d_up + r0 * H;
+        const int64_t sb = ((int64_t)e * fb + blockIdx.x) * hb;
+        const float *gs = a.w.d_gate_s + sb, *us = a.w.d_up_s + sb;
+        const uint8_t *xr = f.xq + (int64_t)g * H;
+        const bool col = g < a.T;
+        float ag[4] = {0.f, 0.f, 0.f, 0.f}, au[4] = {0.f, 0.f, 0.f, 0.f};
+        Rows16 wg[2], wu[2];
+        wg[0].load(gp, H, true, 16 * tig, H);
+        wu[0].load(up, H, true, 16 * tig, H);
+        // two blocks' weights in flight per warp
+        auto block = [&](int b, int cur) {
+            wg[cur ^ 1].load(gp, H, b + 1 < hb, (b + 1) * kSBlk + 16 * tig, H);
+            wu[cur ^ 1].load(up, H, b + 1 < hb, (b + 1) * kSBlk + 16 * tig, H);
+            const int k0 = b * kSBlk + 16 * tig;
+            const uint4 x0 = ldcg16_if(xr + k0, col && k0 < H);
+            const uint4 x1 = ldcg16_if(xr + k0 + 64, col && k0 + 64 < H);
+            const float2 xs =
+                __ldcg(reinterpret_cast<const float2 *>(f.xs + b * kSmallT + 2 * tig));
+            const float sg = __ldg(gs + b), su = __ldg(us + b);
+            float cg[4] = {0.f, 0.f, 0.f, 0.f}, cu[4] = {0.f, 0.f, 0.f, 0.f};
+            wg[cur].multiply(cg, x0, x1);
+            wu[cur].multiply(cu, x0, x1);
+            const float g0 = xs.x * sg, g1 = xs.y * sg, u0 = xs.x * su, u1 = xs.y * su;
+            ag[0] = fmaf(cg[0], g0, ag[0]);
+            ag[1] = fmaf(cg[1], g1, ag[1]);
+            ag[2] = fmaf(cg[2], g0, ag[2]);
+            ag[3] = fmaf(cg[3], g1, ag[3]);
+            au[0] = fmaf(cu[0], u0, au[0]);
+            au[1] = fmaf(cu[1], u1, au[1]);
+            au[2] = fmaf(cu[2], u0, au[2]);
+            au[3] = fmaf(cu[3], u1, au[3]);
+        };
+        int b = 0;
+        for (; b + 1 < hb; b += 2) {
+            block(b, 0);
+            block(b + 1, 1);
         }
-        __syncwarp();
-        const uint4 x0 = *reinterpret_cast<const uint4 *>(C.q + g * kPitch + 16 * tig);
-        const uint4 x1 = *reinterpret_cast<const uint4 *>(C.q + g * kPitch + 64 + 16 * tig);
-        const float s0 = C.s[2 * tig], s1 = C.s[2 * tig + 1];
-        float cg[4] = {0.f, 0.f, 0.f, 0.f}, cu[4] = {0.f, 0.f, 0.f, 0.f};
-        mma64(cg, w0, w1, x0);
-        mma64(cu, v0, v1, x0);
-        mma64(cg, w2, w3, x1);
-        mma64(cu, v2, v3, x1);
-        ag[0] = fmaf(cg[0], s0 * sg, ag[0]);
-        ag[1] = fmaf(cg[1], s1 * sg, ag[1]);
-        ag[2] = fmaf(cg[2], s0 * sg, ag[2]);
-        ag[3] = fmaf(cg[3], s1 * sg, ag[3]);
-        au[0] = fmaf(cu[0], s0 * su, au[0]);
-        au[1] = fmaf(cu[1], s1 * su, au[1]);
-        au[2] = fmaf(cu[2], s0 * su, au[2]);
-        au[3] = fmaf(cu[3], s1 * su, au[3]);
-        __syncwarp();
+        if (b < hb) block(b, 0);
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            // a column that is not routed here holds another token's products or nothing
+            const bool on = (mask >> (2 * tig + (i & 1))) & 1u;
+            hv[i] = on ? __fdiv_rn(ag[i], 1.0f + expf(-ag[i])) * au[i] : 0.f;
+        }
     }
-    put_frag(red[0][warp], ag, g, tig);
-    put_frag(red[1][warp], au, g, tig);
+    // the largest |h| of each column over the CTA's 128 rows
+    uint32_t m0 = max(__float_as_uint(hv[0]) & 0x7fffffffu, __float_as_uint(hv[2]) & 0x7fffffffu);
+    uint32_t m1 = max(__float_as_uint(hv[1]) & 0x7fffffffu, __float_as_uint(hv[3]) & 0x7fffffffu);
+#pragma unroll
+    for (int o = 4; o <= 16; o <<= 1) {
+        m0 = max(m0, __shfl_xor_sync(0xffffffffu, m0, o));
+        m1 = max(m1, __shfl_xor_sync(0xffffffffu, m1, o));
+    }
+    if (g == 0) {
+        s_max[warp][2 * tig] = m0;
+        s_max[warp][2 * tig + 1] = m1;
+    }
     __syncthreads();
-    const int i = threadIdx.x;
-    if (i < kTile * 8 && ((on >> (i / kTile)) & 1u)) {
-        const float gv = sum_warps(red[0], i), uv = sum_warps(red[1], i);
-        a.h[((int64_t)j * kSmallT + i / kTile) * F + f0 + i % kTile] =
-            __fdiv_rn(gv, 1.0f + expf(-gv)) * uv;
+#pragma unroll
+    for (int c = 0; c < 2; c++) {
+        const int t = 2 * tig + c;
+        uint32_t mx = 0u;
+#pragma unroll
+        for (int w = 0; w < kWarps; w++) mx = max(mx, s_max[w][t]);
+        if (!((mask >> t) & 1u)) continue;
+        const bool fin = mx < 0x7f800000u;
+        const float sc = fin ? __fdiv_rn(__uint_as_float(mx), kE4M3Max) : 0.f;
+        const int64_t row = (int64_t)j * kSmallT + t;
+        if (warp == 0 && g == 0) {
+            f.hs[row * fb + blockIdx.x] = sc;
+            if (!fin) set_status(a.status, MOE_ERR_NONFINITE);
+        }
+        if (f0 < F) {
+            const float4 v = make_float4(hv[c], hv[c + 2], 0.f, 0.f);
+            const uint32_t p = sc > 0.f ? quant4(v, sc, __frcp_rn(sc)) : 0u;
+            f.hq[row * F + f0 + g] = (uint8_t)p;
+            f.hq[row * F + f0 + g + 8] = (uint8_t)(p >> 8);
+        }
     }
 }
 
-// grid (hidden / 16): 16 output rows for all tokens, over every job.
+// grid (hidden / 16): 16 output rows for all tokens, over every job.  Items (job, block of ffn) go
+// round the warps, two at a time; the first two's weights are loaded before h is complete.
 template <typename T>
-__global__ void __launch_bounds__(kWarps * 32) k_small_down(const ScaledExpertsArgs a) {
+__global__ void __launch_bounds__(kWarps * 32) k_few_down(const ScaledExpertsArgs a, const FewWs f) {
+    constexpr int kBatch = 2;
     __shared__ float red[kWarps][kTile * 8];
-    __shared__ Cols cols[kWarps];
-    __shared__ Jobs J;
-    __shared__ int s_ids[kSmallT * kMaxK];
-    __shared__ float s_w[kSmallT * kMaxK + 1][kSmallT];
-    __shared__ uint8_t s_on[kSmallT * kMaxK + 1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, tig = lane & 3;
-    for (int i = threadIdx.x; i < kWarps * (int)sizeof(Cols) / 4; i += blockDim.x)
-        reinterpret_cast<uint32_t *>(cols)[i] = 0u;
-    build_jobs(a, J, s_ids);
-    for (int j = threadIdx.x; j < J.n; j += blockDim.x) {
-        unsigned on = 0;
-        for (int t = 0; t < a.T; t++) {
-            float w;
-            if (routed(a, s_ids, J.expert[j], t, &w)) on |= 1u << t;
-            s_w[j][t] = w;
-        }
-        for (int t = a.T; t < kSmallT; t++) s_w[j][t] = 0.f;
-        s_on[j] = (uint8_t)on;
-    }
-    __syncthreads();
     const int H = a.w.hidden, F = a.w.ffn, fb = sblocks(F);
     const int n0 = blockIdx.x * kTile;
-    Cols &C = cols[warp];
-    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+    // the job list was complete before k_few_gateup let this kernel start
+    __shared__ int s_expert[kSmallT * kMaxK + 1], s_mask[kSmallT * kMaxK + 1];
+    const int njobs = __ldcg(f.njobs), items = njobs * fb;
+    for (int j = threadIdx.x; j < max(njobs, 1); j += blockDim.x) {
+        s_expert[j] = njobs ? __ldcg(f.expert + j) : 0;
+        s_mask[j] = njobs ? __ldcg(f.mask + j) : 0;
+    }
+    __syncthreads();
+    struct Item {
+        Rows16 w;
+        int job, b, mask;
+        float sw;
+    } it[2][kBatch];
+    auto load = [&](Item (&q)[kBatch], int first) {
+#pragma unroll
+        for (int u = 0; u < kBatch; u++) {
+            const int i = first + u * kWarps;
+            const bool in = i < items;
+            q[u].job = in ? i / fb : 0;
+            q[u].b = in ? i - q[u].job * fb : 0;
+            const int64_t e = s_expert[q[u].job];
+            q[u].mask = in ? s_mask[q[u].job] : 0;
+            q[u].w.load(a.w.d_down + (e * H + n0 + g) * F, F, in, q[u].b * kSBlk + 16 * tig, F);
+            q[u].sw = __ldg(a.w.d_down_s + (e * sblocks(H) + n0 / kSBlk) * fb + q[u].b);
+        }
+    };
+    load(it[0], warp);
     ptx::grid_dependency_wait();
-    for (int i = warp; i < J.n * fb; i += kWarps) {
-        const int j = i / fb, b = i - j * fb, e = J.expert[j];
-        const unsigned on = s_on[j];
-        const uint8_t *p0 = a.w.d_down + ((int64_t)e * H + n0 + g) * F, *p1 = p0 + 8 * (int64_t)F;
-        const int k0 = b * kSBlk + 16 * tig;
-        const uint4 w0 = row16(p0, k0, F), w1 = row16(p1, k0, F);
-        const uint4 w2 = row16(p0, k0 + 64, F), w3 = row16(p1, k0 + 64, F);
-        const float sw = __ldg(a.w.d_down_s + ((int64_t)e * sblocks(H) + n0 / kSBlk) * fb + b);
-        const int c = b * kSBlk + 4 * lane;
-        for (int t = 0; t < a.T; t++) {
-            if (!((on >> t) & 1u)) continue;
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (c < F)
-                v = __ldcg(reinterpret_cast<const float4 *>(
-                    a.h + ((int64_t)j * kSmallT + t) * F + c));
-            put_col(C, t, v, a.status);
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+    auto batch = [&](Item (&q)[kBatch], Item (&n)[kBatch], int first) {
+        load(n, first + kBatch * kWarps);
+#pragma unroll
+        for (int u = 0; u < kBatch; u++) {
+            if (!q[u].mask) continue;
+            const int64_t row = (int64_t)q[u].job * kSmallT;
+            const int k0 = q[u].b * kSBlk + 16 * tig;
+            const bool col = (q[u].mask >> g) & 1;
+            const uint8_t *hr = f.hq + (row + g) * F;
+            const uint4 x0 = ldcg16_if(hr + k0, col && k0 < F);
+            const uint4 x1 = ldcg16_if(hr + k0 + 64, col && k0 + 64 < F);
+            float cc[4] = {0.f, 0.f, 0.f, 0.f};
+            q[u].w.multiply(cc, x0, x1);
+            // a token that is not routed here takes nothing, whatever the weights hold
+#pragma unroll
+            for (int c = 0; c < 2; c++) {
+                const int t = 2 * tig + c;
+                if (!((q[u].mask >> t) & 1)) continue;
+                const float s = __ldcg(f.hs + (row + t) * fb + q[u].b) * q[u].sw *
+                                __ldcg(f.weight + row + t);
+                acc[c] = fmaf(cc[c], s, acc[c]);
+                acc[c + 2] = fmaf(cc[c + 2], s, acc[c + 2]);
+            }
         }
-        __syncwarp();
-        const uint4 x0 = *reinterpret_cast<const uint4 *>(C.q + g * kPitch + 16 * tig);
-        const uint4 x1 = *reinterpret_cast<const uint4 *>(C.q + g * kPitch + 64 + 16 * tig);
-        float cc[4] = {0.f, 0.f, 0.f, 0.f};
-        mma64(cc, w0, w1, x0);
-        mma64(cc, w2, w3, x1);
-        // a token that is not routed here takes nothing, whatever its column holds
-        if ((on >> (2 * tig)) & 1u) {
-            const float s = C.s[2 * tig] * sw;
-            const float r = s_w[j][2 * tig];
-            acc[0] = fmaf(cc[0] * s, r, acc[0]);
-            acc[2] = fmaf(cc[2] * s, r, acc[2]);
-        }
-        if ((on >> (2 * tig + 1)) & 1u) {
-            const float s = C.s[2 * tig + 1] * sw;
-            const float r = s_w[j][2 * tig + 1];
-            acc[1] = fmaf(cc[1] * s, r, acc[1]);
-            acc[3] = fmaf(cc[3] * s, r, acc[3]);
-        }
-        __syncwarp();
+    };
+    int cur = 0;
+    for (int first = warp; first < items; first += kBatch * kWarps) {
+        if (cur == 0)
+            batch(it[0], it[1], first);
+        else
+            batch(it[1], it[0], first);
+        cur ^= 1;
     }
     put_frag(red[warp], acc, g, tig);
     __syncthreads();
@@ -345,6 +622,24 @@ __global__ void __launch_bounds__(kWarps * 32) k_small_down(const ScaledExpertsA
     if (i < kTile * 8 && i / kTile < a.T)
         static_cast<T *>(a.out)[(int64_t)(i / kTile) * H + n0 + i % kTile] =
             from_f32<T>(sum_warps(red, i));
+}
+
+// Launched behind the previous kernel of the stream (programmatic dependent launch).
+template <typename... P, typename... Q>
+cudaError_t launch_behind(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t st, Q... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t err = cudaLaunchKernelEx(&cfg, kernel, args...);
+    if (err != cudaSuccess) return err;
+    note_launches(1);
+    return cudaGetLastError();
 }
 
 }  // namespace
@@ -360,34 +655,43 @@ cudaError_t launch_scaled_small(const ScaledMatmulArgs &a, cudaStream_t st) {
     });
 }
 
-size_t scaled_small_h_bytes(int T, int k, int shared, int F) {
-    return (size_t)(T * k + (shared ? 1 : 0)) * kSmallT * F * sizeof(float);
+size_t scaled_small_ws_bytes(int T, int k, int shared, int H, int F) {
+    const size_t one = (size_t)(k + shared) * F * sizeof(float);
+    return T == 1 ? one : std::max(one, few_layout(T, k, shared, H, F, nullptr, nullptr));
 }
 
-cudaError_t launch_scaled_experts_small(const ScaledExpertsArgs &a, cudaStream_t st) {
-    const dim3 grid(a.w.ffn / kTile, a.T * a.k + (a.w.shared ? 1 : 0));
+cudaError_t launch_scaled_experts_small(const ScaledExpertsArgs &e, void *ws, cudaStream_t st) {
+    ScaledExpertsArgs a = e;
+    const int jobs = a.T * a.k + a.w.shared;
+    if (a.T == 1) {
+        a.h = static_cast<float *>(ws);
+        const cudaError_t err = with_dtype(a.x_dt, [&](auto *tag) {
+            using E = std::remove_pointer_t<decltype(tag)>;
+            k_one_gateup<E><<<dim3(a.w.ffn / kTile, jobs), kWarps * 32, 0, st>>>(a);
+            note_launches(1);
+            return cudaGetLastError();
+        });
+        if (err != cudaSuccess) return err;
+        return with_dtype(a.out_dt, [&](auto *tag) {
+            using E = std::remove_pointer_t<decltype(tag)>;
+            return launch_behind(k_one_down<E>, dim3(a.w.hidden / kTile), kWarps * 32, st, a);
+        });
+    }
+    FewWs f;
+    few_layout(a.T, a.k, a.w.shared, a.w.hidden, a.w.ffn, static_cast<uint8_t *>(ws), &f);
     cudaError_t err = with_dtype(a.x_dt, [&](auto *tag) {
         using E = std::remove_pointer_t<decltype(tag)>;
-        k_small_gateup<E><<<grid, kWarps * 32, 0, st>>>(a);
+        const int units = a.T * sblocks(a.w.hidden);
+        k_few_prep<E><<<1 + (units + 7) / 8, 256, 0, st>>>(a, f);
         note_launches(1);
         return cudaGetLastError();
     });
     if (err != cudaSuccess) return err;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(a.w.hidden / kTile);
-    cfg.blockDim = dim3(kWarps * 32);
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    err = launch_behind(k_few_gateup, dim3(sblocks(a.w.ffn), jobs), kWarps * 32, st, a, f);
+    if (err != cudaSuccess) return err;
     return with_dtype(a.out_dt, [&](auto *tag) {
         using E = std::remove_pointer_t<decltype(tag)>;
-        const cudaError_t r = cudaLaunchKernelEx(&cfg, k_small_down<E>, a);
-        if (r != cudaSuccess) return r;
-        note_launches(1);
-        return cudaGetLastError();
+        return launch_behind(k_few_down<E>, dim3(a.w.hidden / kTile), kWarps * 32, st, a, f);
     });
 }
 

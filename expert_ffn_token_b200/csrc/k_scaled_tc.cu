@@ -840,15 +840,13 @@ cudaError_t launch_scaled_matmul(const ScaledMatmulArgs &a, void *, cudaStream_t
 }
 
 size_t scaled_experts_ws_bytes(const moe_scaled_weights &w, int T, int k) {
-    return T <= kSmallT ? align256(scaled_small_h_bytes(T, k, w.shared, w.ffn))
+    return T <= kSmallT ? align256(scaled_small_ws_bytes(T, k, w.shared, w.hidden, w.ffn))
                         : experts_ws(w, T, k).total;
 }
 
 cudaError_t launch_scaled_experts(const ScaledExpertsArgs &a, void *ws, cudaStream_t st) {
-    if (a.T > kSmallT) return experts_tc(a, static_cast<uint8_t *>(ws), st);
-    ScaledExpertsArgs s = a;
-    s.h = static_cast<float *>(ws);
-    return launch_scaled_experts_small(s, st);
+    return a.T > kSmallT ? experts_tc(a, static_cast<uint8_t *>(ws), st)
+                         : launch_scaled_experts_small(a, ws, st);
 }
 
 }  // namespace moe

@@ -67,11 +67,11 @@ __device__ __forceinline__ uint32_t cvt_e4m3x2(float lo, float hi) {
     return r;
 }
 
-// x / s to the nearest e4m3 without an intermediate rounding: the 64-bit quotient, rounded to
-// fp32 with its lost bits kept as a sticky last bit, converts as the exact quotient would (fp32
-// has 20 bits more than e4m3, and a 64-bit quotient of two fp32 values is never halfway between
-// two e4m3 values unless it is exact).
-static __device__ __noinline__ uint32_t quant4_exact(float4 v, float s) {
+// x / s to the nearest e4m3 without an intermediate rounding, for any s > 0: the 64-bit quotient,
+// rounded to fp32 with its lost bits kept as a sticky last bit, converts as the exact quotient
+// would (fp32 has 20 bits more than e4m3, and a 64-bit quotient of two fp32 values is never
+// halfway between two e4m3 values unless it is exact).
+static __device__ __noinline__ uint32_t quant4_wide(float4 v, float s) {
     float f[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int i = 0; i < 4; i++) {
@@ -83,17 +83,40 @@ static __device__ __noinline__ uint32_t quant4_exact(float4 v, float s) {
     return cvt_e4m3x2(f[0], f[1]) | (cvt_e4m3x2(f[2], f[3]) << 16);
 }
 
+// The sum of two e4m3 values, halved (exact in fp16), for the two pairs of bytes in a and b.
+__device__ __forceinline__ float2 e4m3_middle(uint32_t a, uint32_t b) {
+    uint32_t x, y;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(x) : "h"((uint16_t)a));
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(y) : "h"((uint16_t)b));
+    const __half2 m = __hmul2(__hadd2(*reinterpret_cast<__half2 *>(&x), *reinterpret_cast<__half2 *>(&y)),
+                              __float2half2_rn(0.5f));
+    return __half22float2(m);
+}
+
 // Four values of a block with scale s > 0 as packed e4m3.  v * RN(1/s) is within 2^-23 of v / s
 // (relative); when the values 2^-21 below and above it convert to the same byte, so does v / s
-// (conversion is monotone).  Otherwise, in about one block of a thousand, or for a scale whose
-// reciprocal is not normal, the exact form decides.  A division for every value costs the
-// quantiser its memory bandwidth.
+// (conversion is monotone).  Otherwise they are neighbours, and v is compared with s times the
+// value halfway between them, exactly, in one multiply-add: equal goes to the even byte.  16-bit
+// inputs are halfway often (their quotients have few bits), so this costs no 64-bit division.
 __device__ __forceinline__ uint32_t quant4(float4 v, float s, float inv) {
+    if (s < 0x1p-100f) return quant4_wide(v, s);       // 1 / s or the exact remainder underflows
     const float a = v.x * inv, b = v.y * inv, c = v.z * inv, d = v.w * inv;
     constexpr float kLo = 1.0f - 0x1p-21f, kHi = 1.0f + 0x1p-21f;
-    const uint32_t lo = cvt_e4m3x2(a * kLo, b * kLo) | (cvt_e4m3x2(c * kLo, d * kLo) << 16);
+    uint32_t lo = cvt_e4m3x2(a * kLo, b * kLo) | (cvt_e4m3x2(c * kLo, d * kLo) << 16);
     const uint32_t hi = cvt_e4m3x2(a * kHi, b * kHi) | (cvt_e4m3x2(c * kHi, d * kHi) << 16);
-    if (lo != hi || s < 0x1p-120f) return quant4_exact(v, s);
+    if (lo != hi) {
+        const float2 m0 = e4m3_middle(lo & 0xffffu, hi & 0xffffu), m1 = e4m3_middle(lo >> 16, hi >> 16);
+        const float f[4] = {v.x, v.y, v.z, v.w}, m[4] = {m0.x, m0.y, m1.x, m1.y};
+        uint32_t out = 0;
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const uint32_t l = (lo >> (8 * i)) & 0xffu, h = (hi >> (8 * i)) & 0xffu;
+            const float r = fmaf(-fabsf(m[i]), s, fabsf(f[i]));
+            const bool up = r > 0.f || (r == 0.f && (l & 1u));
+            out |= (up ? h : l) << (8 * i);
+        }
+        lo = out;
+    }
     return lo;
 }
 
@@ -163,15 +186,15 @@ struct ScaledExpertsArgs {
     void *out;
     int out_dt;
     uint32_t *status;
-    float *h;                      // small batches: h of (job, token) [jobs][8][ffn]
+    float *h;                      // one token: h of every slot [slots][ffn]
 };
 // x quantised into the slots of its tokens: q [slots][hidden], scales [blocks][slots].
 cudaError_t launch_scaled_spread(const ScaledExpertsArgs &e, uint8_t *q, float *s, cudaStream_t st);
 // The layer on the kernels that suit T, and the workspace they need for exactly T tokens.
 size_t scaled_experts_ws_bytes(const moe_scaled_weights &w, int T, int k);
 cudaError_t launch_scaled_experts(const ScaledExpertsArgs &a, void *ws, cudaStream_t st);
-// k_scaled_small.cu: T <= kSmallT in two kernels, and the bytes of h between them.
-size_t scaled_small_h_bytes(int T, int k, int shared, int F);
-cudaError_t launch_scaled_experts_small(const ScaledExpertsArgs &a, cudaStream_t st);
+// k_scaled_small.cu: T <= kSmallT, and the workspace for it.
+size_t scaled_small_ws_bytes(int T, int k, int shared, int H, int F);
+cudaError_t launch_scaled_experts_small(const ScaledExpertsArgs &a, void *ws, cudaStream_t st);
 
 }  // namespace moe
