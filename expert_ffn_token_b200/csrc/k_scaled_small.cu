@@ -386,11 +386,13 @@ __global__ void __launch_bounds__(256) k_few_prep(const ScaledExpertsArgs a, con
     }
     // the distinct experts in order of first appearance; a thread per (token, slot) pair
     __shared__ int s_ids[kSmallT * kMaxK];
+    __shared__ float s_w[kSmallT * kMaxK];
     __shared__ int s_count[8];
     const int A = a.T * a.k, i = threadIdx.x;
     int e = -1;
     if (i < A) {
         e = __ldg(a.ids + i);
+        s_w[i] = __ldg(a.rw + i);
         if (e < 0 || e >= a.w.n_experts) {
             e = -1;
             set_status(a.status, MOE_ERR_BOUNDS);
@@ -417,7 +419,7 @@ __global__ void __launch_bounds__(256) k_few_prep(const ScaledExpertsArgs a, con
             for (int q = 0; q < a.k; q++) {
                 if (s_ids[t * a.k + q] != e) continue;
                 mask |= 1u << t;
-                w += __ldg(a.rw + t * a.k + q);
+                w += s_w[t * a.k + q];
             }
             f.weight[j * kSmallT + t] = w;
         }
@@ -449,10 +451,15 @@ __device__ __forceinline__ uint4 ldcg16_if(const uint8_t *p, bool in) {
     return v;
 }
 
-// grid (blocks of ffn, most jobs): 128 ffn values of one expert, a warp per 16; h quantised.
-__global__ void __launch_bounds__(kWarps * 32) k_few_gateup(const ScaledExpertsArgs a, const FewWs f) {
+// grid (blocks of ffn, most jobs): 128 ffn values of one expert, two warps per 16 of them that take
+// alternate blocks of k; h quantised.
+constexpr int kFewThreads = 512;
+__global__ void __launch_bounds__(kFewThreads, 1)
+    k_few_gateup(const ScaledExpertsArgs a, const FewWs f) {
+    __shared__ float s_part[kWarps][32][8];
     __shared__ uint32_t s_max[kWarps][8];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, tig = lane & 3;
+    const int warp = (threadIdx.x >> 5) & 7, half = threadIdx.x >> 8;
+    const int lane = threadIdx.x & 31, g = lane >> 2, tig = lane & 3;
     ptx::grid_dependency_wait();
     ptx::launch_dependents();
     const int j = blockIdx.y;
@@ -461,7 +468,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_few_gateup(const ScaledExpertsA
     const unsigned mask = (unsigned)__ldcg(f.mask + j);
     const int H = a.w.hidden, F = a.w.ffn, hb = sblocks(H), fb = sblocks(F);
     const int f0 = blockIdx.x * kSBlk + warp * kTile;
-    float hv[4] = {0.f, 0.f, 0.f, 0.f};    // rows g, g + 8 by columns 2 tig, 2 tig + 1
+    float ag[4] = {0.f, 0.f, 0.f, 0.f}, au[4] = {0.f, 0.f, 0.f, 0.f};
     if (f0 < F) {
         const int64_t r0 = (int64_t)e * F + f0 + g;
         const uint8_t *gp = a.w.d_gate + r0 * H, *up = a.w.d_up + r0 * H;
@@ -469,24 +476,32 @@ __global__ void __launch_bounds__(kWarps * 32) k_few_gateup(const ScaledExpertsA
         const float *gs = a.w.d_gate_s + sb, *us = a.w.d_up_s + sb;
         const uint8_t *xr = f.xq + (int64_t)g * H;
         const bool col = g < a.T;
-        float ag[4] = {0.f, 0.f, 0.f, 0.f}, au[4] = {0.f, 0.f, 0.f, 0.f};
-        Rows16 wg[2], wu[2];
-        wg[0].load(gp, H, true, 16 * tig, H);
-        wu[0].load(up, H, true, 16 * tig, H);
-        // two blocks' weights in flight per warp
-        auto block = [&](int b, int cur) {
-            wg[cur ^ 1].load(gp, H, b + 1 < hb, (b + 1) * kSBlk + 16 * tig, H);
-            wu[cur ^ 1].load(up, H, b + 1 < hb, (b + 1) * kSBlk + 16 * tig, H);
+        // everything a block needs is loaded a block ahead, the activations first: a wait for
+        // them must not wait for weights that come from HBM after them
+        struct Block {
+            uint4 x0, x1;
+            float2 xs;
+            float sg, su;
+            Rows16 wg, wu;
+        } q[2];
+        auto load = [&](Block &k, int b) {
             const int k0 = b * kSBlk + 16 * tig;
-            const uint4 x0 = ldcg16_if(xr + k0, col && k0 < H);
-            const uint4 x1 = ldcg16_if(xr + k0 + 64, col && k0 + 64 < H);
-            const float2 xs =
-                __ldcg(reinterpret_cast<const float2 *>(f.xs + b * kSmallT + 2 * tig));
-            const float sg = __ldg(gs + b), su = __ldg(us + b);
+            const bool in = b < hb;
+            k.x0 = ldcg16_if(xr + k0, in && col && k0 < H);
+            k.x1 = ldcg16_if(xr + k0 + 64, in && col && k0 + 64 < H);
+            const int bb = min(b, hb - 1);
+            k.xs = __ldcg(reinterpret_cast<const float2 *>(f.xs + bb * kSmallT + 2 * tig));
+            k.sg = __ldg(gs + bb);
+            k.su = __ldg(us + bb);
+            k.wg.load(gp, H, in, k0, H);
+            k.wu.load(up, H, in, k0, H);
+        };
+        auto add = [&](const Block &k) {
             float cg[4] = {0.f, 0.f, 0.f, 0.f}, cu[4] = {0.f, 0.f, 0.f, 0.f};
-            wg[cur].multiply(cg, x0, x1);
-            wu[cur].multiply(cu, x0, x1);
-            const float g0 = xs.x * sg, g1 = xs.y * sg, u0 = xs.x * su, u1 = xs.y * su;
+            k.wg.multiply(cg, k.x0, k.x1);
+            k.wu.multiply(cu, k.x0, k.x1);
+            const float g0 = k.xs.x * k.sg, g1 = k.xs.y * k.sg;
+            const float u0 = k.xs.x * k.su, u1 = k.xs.y * k.su;
             ag[0] = fmaf(cg[0], g0, ag[0]);
             ag[1] = fmaf(cg[1], g1, ag[1]);
             ag[2] = fmaf(cg[2], g0, ag[2]);
@@ -496,32 +511,49 @@ __global__ void __launch_bounds__(kWarps * 32) k_few_gateup(const ScaledExpertsA
             au[2] = fmaf(cu[2], u0, au[2]);
             au[3] = fmaf(cu[3], u1, au[3]);
         };
-        int b = 0;
-        for (; b + 1 < hb; b += 2) {
-            block(b, 0);
-            block(b + 1, 1);
+        load(q[0], half);
+        for (int b = half; b < hb; b += 4) {
+            load(q[1], b + 2);
+            add(q[0]);
+            if (b + 2 >= hb) break;
+            load(q[0], b + 4);
+            add(q[1]);
         }
-        if (b < hb) block(b, 0);
+    }
+    if (half == 1) {
 #pragma unroll
         for (int i = 0; i < 4; i++) {
-            // a column that is not routed here holds another token's products or nothing
-            const bool on = (mask >> (2 * tig + (i & 1))) & 1u;
-            hv[i] = on ? __fdiv_rn(ag[i], 1.0f + expf(-ag[i])) * au[i] : 0.f;
+            s_part[warp][lane][i] = ag[i];
+            s_part[warp][lane][4 + i] = au[i];
         }
     }
-    // the largest |h| of each column over the CTA's 128 rows
-    uint32_t m0 = max(__float_as_uint(hv[0]) & 0x7fffffffu, __float_as_uint(hv[2]) & 0x7fffffffu);
-    uint32_t m1 = max(__float_as_uint(hv[1]) & 0x7fffffffu, __float_as_uint(hv[3]) & 0x7fffffffu);
+    __syncthreads();
+    float hv[4] = {0.f, 0.f, 0.f, 0.f};    // rows g, g + 8 by columns 2 tig, 2 tig + 1
+    if (half == 0) {
+        if (f0 < F) {
 #pragma unroll
-    for (int o = 4; o <= 16; o <<= 1) {
-        m0 = max(m0, __shfl_xor_sync(0xffffffffu, m0, o));
-        m1 = max(m1, __shfl_xor_sync(0xffffffffu, m1, o));
-    }
-    if (g == 0) {
-        s_max[warp][2 * tig] = m0;
-        s_max[warp][2 * tig + 1] = m1;
+            for (int i = 0; i < 4; i++) {
+                const float gv = ag[i] + s_part[warp][lane][i], uv = au[i] + s_part[warp][lane][4 + i];
+                // a column that is not routed here holds another token's products or nothing
+                const bool on = (mask >> (2 * tig + (i & 1))) & 1u;
+                hv[i] = on ? __fdiv_rn(gv, 1.0f + expf(-gv)) * uv : 0.f;
+            }
+        }
+        // the largest |h| of each column over the CTA's 128 rows
+        uint32_t m0 = max(__float_as_uint(hv[0]) & 0x7fffffffu, __float_as_uint(hv[2]) & 0x7fffffffu);
+        uint32_t m1 = max(__float_as_uint(hv[1]) & 0x7fffffffu, __float_as_uint(hv[3]) & 0x7fffffffu);
+#pragma unroll
+        for (int o = 4; o <= 16; o <<= 1) {
+            m0 = max(m0, __shfl_xor_sync(0xffffffffu, m0, o));
+            m1 = max(m1, __shfl_xor_sync(0xffffffffu, m1, o));
+        }
+        if (g == 0) {
+            s_max[warp][2 * tig] = m0;
+            s_max[warp][2 * tig + 1] = m1;
+        }
     }
     __syncthreads();
+    if (half == 1) return;
 #pragma unroll
     for (int c = 0; c < 2; c++) {
         const int t = 2 * tig + c;
@@ -548,14 +580,15 @@ __global__ void __launch_bounds__(kWarps * 32) k_few_gateup(const ScaledExpertsA
 // grid (hidden / 16): 16 output rows for all tokens, over every job.  Items (job, block of ffn) go
 // round the warps, two at a time; the first two's weights are loaded before h is complete.
 template <typename T>
-__global__ void __launch_bounds__(kWarps * 32) k_few_down(const ScaledExpertsArgs a, const FewWs f) {
+__global__ void __launch_bounds__(kWarps * 32, 2)
+    k_few_down(const ScaledExpertsArgs a, const FewWs f) {
     constexpr int kBatch = 2;
     __shared__ float red[kWarps][kTile * 8];
+    __shared__ int s_expert[kSmallT * kMaxK + 1], s_mask[kSmallT * kMaxK + 1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, tig = lane & 3;
     const int H = a.w.hidden, F = a.w.ffn, fb = sblocks(F);
     const int n0 = blockIdx.x * kTile;
     // the job list was complete before k_few_gateup let this kernel start
-    __shared__ int s_expert[kSmallT * kMaxK + 1], s_mask[kSmallT * kMaxK + 1];
     const int njobs = __ldcg(f.njobs), items = njobs * fb;
     for (int j = threadIdx.x; j < max(njobs, 1); j += blockDim.x) {
         s_expert[j] = njobs ? __ldcg(f.expert + j) : 0;
@@ -566,7 +599,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_few_down(const ScaledExpertsArg
         Rows16 w;
         int job, b, mask;
         float sw;
-    } it[2][kBatch];
+    };
     auto load = [&](Item (&q)[kBatch], int first) {
 #pragma unroll
         for (int u = 0; u < kBatch; u++) {
@@ -576,52 +609,63 @@ __global__ void __launch_bounds__(kWarps * 32) k_few_down(const ScaledExpertsArg
             q[u].b = in ? i - q[u].job * fb : 0;
             const int64_t e = s_expert[q[u].job];
             q[u].mask = in ? s_mask[q[u].job] : 0;
-            q[u].w.load(a.w.d_down + (e * H + n0 + g) * F, F, in, q[u].b * kSBlk + 16 * tig, F);
             q[u].sw = __ldg(a.w.d_down_s + (e * sblocks(H) + n0 / kSBlk) * fb + q[u].b);
+            q[u].w.load(a.w.d_down + (e * H + n0 + g) * F, F, in, q[u].b * kSBlk + 16 * tig, F);
         }
     };
-    load(it[0], warp);
-    ptx::grid_dependency_wait();
     float acc[4] = {0.f, 0.f, 0.f, 0.f};
     auto batch = [&](Item (&q)[kBatch], Item (&n)[kBatch], int first) {
-        load(n, first + kBatch * kWarps);
+        // the activations first: a wait for them must not wait for the next weights
+        uint4 x0[kBatch], x1[kBatch];
+        float s[kBatch][2];
 #pragma unroll
         for (int u = 0; u < kBatch; u++) {
-            if (!q[u].mask) continue;
             const int64_t row = (int64_t)q[u].job * kSmallT;
             const int k0 = q[u].b * kSBlk + 16 * tig;
             const bool col = (q[u].mask >> g) & 1;
             const uint8_t *hr = f.hq + (row + g) * F;
-            const uint4 x0 = ldcg16_if(hr + k0, col && k0 < F);
-            const uint4 x1 = ldcg16_if(hr + k0 + 64, col && k0 + 64 < F);
+            x0[u] = ldcg16_if(hr + k0, col && k0 < F);
+            x1[u] = ldcg16_if(hr + k0 + 64, col && k0 + 64 < F);
+#pragma unroll
+            for (int c = 0; c < 2; c++) {
+                const bool on = (q[u].mask >> (2 * tig + c)) & 1;
+                s[u][c] = on ? __ldcg(f.hs + (row + 2 * tig + c) * fb + q[u].b) *
+                                   __ldcg(f.weight + row + 2 * tig + c)
+                             : 0.f;
+            }
+        }
+        load(n, first + kBatch * kWarps);
+#pragma unroll
+        for (int u = 0; u < kBatch; u++) {
+            if (!q[u].mask) continue;
             float cc[4] = {0.f, 0.f, 0.f, 0.f};
-            q[u].w.multiply(cc, x0, x1);
+            q[u].w.multiply(cc, x0[u], x1[u]);
             // a token that is not routed here takes nothing, whatever the weights hold
 #pragma unroll
             for (int c = 0; c < 2; c++) {
-                const int t = 2 * tig + c;
-                if (!((q[u].mask >> t) & 1)) continue;
-                const float s = __ldcg(f.hs + (row + t) * fb + q[u].b) * q[u].sw *
-                                __ldcg(f.weight + row + t);
-                acc[c] = fmaf(cc[c], s, acc[c]);
-                acc[c + 2] = fmaf(cc[c + 2], s, acc[c + 2]);
+                if (!((q[u].mask >> (2 * tig + c)) & 1)) continue;
+                acc[c] = fmaf(cc[c], s[u][c] * q[u].sw, acc[c]);
+                acc[c + 2] = fmaf(cc[c + 2], s[u][c] * q[u].sw, acc[c + 2]);
             }
         }
     };
-    int cur = 0;
-    for (int first = warp; first < items; first += kBatch * kWarps) {
-        if (cur == 0)
-            batch(it[0], it[1], first);
-        else
-            batch(it[1], it[0], first);
-        cur ^= 1;
+    Item q0[kBatch], q1[kBatch];
+    load(q0, warp);
+    ptx::grid_dependency_wait();
+    for (int first = warp; first < items; first += 2 * kBatch * kWarps) {
+        batch(q0, q1, first);
+        if (first + kBatch * kWarps >= items) break;
+        batch(q1, q0, first + kBatch * kWarps);
     }
     put_frag(red[warp], acc, g, tig);
     __syncthreads();
     const int i = threadIdx.x;
-    if (i < kTile * 8 && i / kTile < a.T)
-        static_cast<T *>(a.out)[(int64_t)(i / kTile) * H + n0 + i % kTile] =
-            from_f32<T>(sum_warps(red, i));
+    if (i < kTile * 8 && i / kTile < a.T) {
+        float sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; w++) sum += red[w][i];
+        static_cast<T *>(a.out)[(int64_t)(i / kTile) * H + n0 + i % kTile] = from_f32<T>(sum);
+    }
 }
 
 // Launched behind the previous kernel of the stream (programmatic dependent launch).
@@ -687,7 +731,7 @@ cudaError_t launch_scaled_experts_small(const ScaledExpertsArgs &e, void *ws, cu
         return cudaGetLastError();
     });
     if (err != cudaSuccess) return err;
-    err = launch_behind(k_few_gateup, dim3(sblocks(a.w.ffn), jobs), kWarps * 32, st, a, f);
+    err = launch_behind(k_few_gateup, dim3(sblocks(a.w.ffn), jobs), kFewThreads, st, a, f);
     if (err != cudaSuccess) return err;
     return with_dtype(a.out_dt, [&](auto *tag) {
         using E = std::remove_pointer_t<decltype(tag)>;
