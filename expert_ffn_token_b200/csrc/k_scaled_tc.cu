@@ -46,7 +46,7 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kMT = 128;                       // most tokens of a tile
+constexpr int kMT = kScaledRun;                // most tokens of a tile
 constexpr int kNW = 256;                       // weight rows of a tile (gate/up: 128 + 128)
 constexpr int kEpiWarp0 = 4, kEpiWarps = 16;
 constexpr int kThreads = (kEpiWarp0 + kEpiWarps) * 32;
@@ -74,7 +74,7 @@ struct TcArgs {
     int rows;                    // weight rows per expert (gate/up: of each of the two)
     int row_tiles;
     int M;                       // dense: rows of a
-    const Job *slices;           // experts: runs of up to 128 slots (k_scaled_slices)
+    const Job *slices;           // experts: runs of up to 128 slots (list_slices)
     const int32_t *nslices;
     const float *as;
     int64_t ldas;
@@ -556,36 +556,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-// The runs of up to 128 slots of every expert with tokens, ascending, the shared one's last: the
-// tiles' token side.  One CTA.
-__global__ void __launch_bounds__(1024)
-    k_scaled_slices(const int32_t *__restrict__ offsets, int E, int T, int k, int shared,
-                    Job *slices, int32_t *nslices, uint32_t *status) {
-    __shared__ int s_first[kMaxE];
-    __shared__ int s_warp[33];
-    const int A = T * k;
-    for (int e = threadIdx.x; e < E; e += 1024) {
-        const int o = offsets[e], o1 = offsets[e + 1];
-        const bool fits = o >= 0 && o <= o1 && o1 <= A;      // else not what a router wrote
-        if (!fits) set_status(status, MOE_ERR_BOUNDS);
-        s_first[e] = fits ? (o1 - o + kMT - 1) / kMT : 0;
-    }
-    __syncthreads();
-    // overlapping runs of damaged offsets could pass the list's end: those are left out too
-    const int most = A / kMT + min(E, A);
-    const int n = min(block_exclusive_scan<1024>(s_first, E, s_warp), most);
-    for (int e = threadIdx.x; e < E; e += 1024) {
-        const int o = offsets[e], o1 = offsets[e + 1];
-        if (!(o >= 0 && o <= o1 && o1 <= A)) continue;
-        for (int s = o, j = s_first[e]; s < o1 && j < most; s += kMT, j++)
-            slices[j] = Job{e, s, min(kMT, o1 - s), 0};
-    }
-    const int ns = shared ? (T + kMT - 1) / kMT : 0;
-    for (int j = threadIdx.x; j < ns; j += 1024)
-        slices[n + j] = Job{E, A + j * kMT, min(kMT, T - j * kMT), 1};
-    if (threadIdx.x == 0) *nslices = n + ns;
-}
-
 // Eight values of y at column 8 c of a slot's row, with their power of two when y is fp16.
 __device__ __forceinline__ void load_y(const float *y, const float *, int64_t slot, int H, int c,
                                        float (&v)[8]) {
@@ -762,12 +732,7 @@ cudaError_t experts_tc(const ScaledExpertsArgs &e, uint8_t *ws, cudaStream_t st)
         !encode(&h, ws + L.hq, F, L.slots, F, 0, 128) ||
         !encode(&h16, ws + L.hq, F, L.slots, F, 0, 16))
         return cudaErrorInvalidValue;
-    k_scaled_slices<<<1, 1024, 0, st>>>(e.offsets, w.n_experts, e.T, e.k, w.shared, slices,
-                                        nslices, e.status);
-    note_launches(1);
-    cudaError_t err = cudaGetLastError();
-    if (err != cudaSuccess) return err;
-    err = launch_scaled_spread(e, ws + L.xq, xs, st);
+    cudaError_t err = launch_scaled_spread(e, ws + L.xq, xs, slices, nslices, st);
     if (err != cudaSuccess) return err;
     TcArgs a{};
     a.slices = slices;
@@ -840,12 +805,12 @@ cudaError_t launch_scaled_matmul(const ScaledMatmulArgs &a, void *, cudaStream_t
 }
 
 size_t scaled_experts_ws_bytes(const moe_scaled_weights &w, int T, int k) {
-    return T <= kSmallT ? align256(scaled_small_ws_bytes(T, k, w.shared, w.hidden, w.ffn))
+    return T <= kSmallExpertsT ? align256(scaled_small_ws_bytes(T, k, w.shared, w.hidden, w.ffn))
                         : experts_ws(w, T, k).total;
 }
 
 cudaError_t launch_scaled_experts(const ScaledExpertsArgs &a, void *ws, cudaStream_t st) {
-    return a.T > kSmallT ? experts_tc(a, static_cast<uint8_t *>(ws), st)
+    return a.T > kSmallExpertsT ? experts_tc(a, static_cast<uint8_t *>(ws), st)
                          : launch_scaled_experts_small(a, ws, st);
 }
 

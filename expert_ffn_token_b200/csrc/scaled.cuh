@@ -11,6 +11,10 @@ namespace moe {
 constexpr int kSBlk = 128;                 // columns (and weight rows) per scale
 constexpr float kE4M3Max = 448.0f;
 constexpr int kSmallT = 8;                 // most tokens of the small-batch kernels (MMA columns)
+// Most tokens of the experts' small-batch kernels.  10 of 512 experts and the shared one, hidden
+// 2560, ffn 640, small / tensor cores: 3 tokens 46 / 58 us (26 experts), 5 tokens 79 / 81 us (50),
+// 8 tokens 117 / 102 us (76).
+constexpr int kSmallExpertsT = 6;
 
 __host__ __device__ inline int sblocks(int n) { return (n + kSBlk - 1) / kSBlk; }
 inline size_t dtype_bytes(int dt) { return dt == MOE_DT_F32 ? 4 : 2; }
@@ -188,8 +192,17 @@ struct ScaledExpertsArgs {
     uint32_t *status;
     float *h;                      // one token: h of every slot [slots][ffn]
 };
-// x quantised into the slots of its tokens: q [slots][hidden], scales [blocks][slots].
-cudaError_t launch_scaled_spread(const ScaledExpertsArgs &e, uint8_t *q, float *s, cudaStream_t st);
+// x quantised into the slots of its tokens: q [slots][hidden], scales [blocks][slots]; and the
+// experts' runs of at most kScaledRun slots, with their number.
+constexpr int kScaledRun = 128;
+struct SliceArgs {
+    const int32_t *offsets;
+    int E, T, k, shared;
+    Job *slices;
+    int32_t *nslices;
+};
+cudaError_t launch_scaled_spread(const ScaledExpertsArgs &e, uint8_t *q, float *s, Job *slices,
+                                 int32_t *nslices, cudaStream_t st);
 // The layer on the kernels that suit T, and the workspace they need for exactly T tokens.
 size_t scaled_experts_ws_bytes(const moe_scaled_weights &w, int T, int k);
 cudaError_t launch_scaled_experts(const ScaledExpertsArgs &a, void *ws, cudaStream_t st);

@@ -121,7 +121,7 @@ moe_status moe_scaled_experts_workspace_size(const moe_scaled_weights *host_weig
     if ((int64_t)max_tokens * (k + 1) > kScaledMaxSlots) return MOE_ERR_UNSUPPORTED;
     // the small-batch kernels' workspace can exceed that of a slightly larger batch
     *bytes = std::max(scaled_experts_ws_bytes(*host_weights, max_tokens, k),
-                      scaled_experts_ws_bytes(*host_weights, std::min(max_tokens, kSmallT), k));
+                      scaled_experts_ws_bytes(*host_weights, std::min(max_tokens, kSmallExpertsT), k));
     return MOE_OK;
 }
 

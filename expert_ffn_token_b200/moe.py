@@ -371,18 +371,32 @@ def scaled_experts(weights: ScaledWeights, d_x: int, x_dtype: int, T: int, k: in
 # ------------------------------------------------------------------ torch convenience
 
 
+_DTYPES: dict = {}
+_FLOATS: tuple = ()
+
+
 def dtype_of(t) -> int:
     """The moe_dtype of a torch tensor (fp32, bf16 or fp16)."""
-    import torch
-    d = {torch.float32: DT_F32, torch.bfloat16: DT_BF16, torch.float16: DT_F16}.get(t.dtype)
+    if not _DTYPES:
+        _fill_dtypes()
+    d = _DTYPES.get(t.dtype)
     if d is None:
         raise MoeError(ERR_UNSUPPORTED, f"dtype {t.dtype}")
     return d
 
 
-def _stream():
+def _fill_dtypes() -> None:
+    global _FLOATS
     import torch
-    return torch.cuda.current_stream().cuda_stream
+    _DTYPES.update({torch.float32: DT_F32, torch.bfloat16: DT_BF16, torch.float16: DT_F16})
+    _FLOATS = tuple(_DTYPES)
+
+
+def _stream(device=None):
+    """The current stream's handle, without the Stream object around it (3 us of a small call)."""
+    import torch
+    return torch._C._cuda_getCurrentRawStream(
+        torch.cuda.current_device() if device is None else device)
 
 
 class Layer:
@@ -428,14 +442,14 @@ class Layer:
             pass
 
 
-def _contiguous(t, name: str, shape=None, dtype=None):
-    """t, checked: on the current CUDA device, contiguous, and of the shape and type asked for."""
-    import torch
-    if not t.is_cuda or t.device.index != torch.cuda.current_device() or not t.is_contiguous():
-        raise ValueError(f"{name}: a contiguous tensor on the current CUDA device is needed")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, not {tuple(shape)}")
-    if dtype is not None and t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
+def _contiguous(t, name: str, shape, dtype, device: int):
+    """t, checked: contiguous, on the CUDA device with this index, of the shape and type asked for
+    (a type or a tuple of types)."""
+    if t.get_device() != device or not t.is_cuda:
+        raise ValueError(f"{name}: a tensor on the current CUDA device is needed")
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, not a contiguous {tuple(shape)}")
+    if t.dtype is not dtype and not (isinstance(dtype, tuple) and t.dtype in dtype):
         raise ValueError(f"{name}: type {t.dtype}")
     return t
 
@@ -450,15 +464,16 @@ class ScaledExperts:
     def __init__(self, gate, gate_scale, up, up_scale, down, down_scale, max_tokens: int, k: int,
                  shared: bool = False, rule: RouteRule | None = None):
         import torch
+        _fill_dtypes()
         n, f, h = gate.shape
         fb, hb = -(-f // 128), -(-h // 128)
-        codes = (torch.uint8, torch.float8_e4m3fn)
-        self.tensors = (_contiguous(gate, "gate", (n, f, h), codes),
-                        _contiguous(up, "up", (n, f, h), codes),
-                        _contiguous(down, "down", (n, h, f), codes),
-                        _contiguous(gate_scale, "gate_scale", (n, fb, hb), torch.float32),
-                        _contiguous(up_scale, "up_scale", (n, fb, hb), torch.float32),
-                        _contiguous(down_scale, "down_scale", (n, hb, fb), torch.float32))
+        codes, f32, dev = (torch.uint8, torch.float8_e4m3fn), torch.float32, torch.cuda.current_device()
+        self.tensors = (_contiguous(gate, "gate", (n, f, h), codes, dev),
+                        _contiguous(up, "up", (n, f, h), codes, dev),
+                        _contiguous(down, "down", (n, h, f), codes, dev),
+                        _contiguous(gate_scale, "gate_scale", (n, fb, hb), f32, dev),
+                        _contiguous(up_scale, "up_scale", (n, fb, hb), f32, dev),
+                        _contiguous(down_scale, "down_scale", (n, hb, fb), f32, dev))
         self.hidden, self.ffn, self.n_experts, self.k = h, f, n - int(shared), k
         self.rule = RouteRule() if rule is None else rule
         self.weights = ScaledWeights(h, f, n - int(shared), int(shared),
@@ -469,41 +484,43 @@ class ScaledExperts:
         self.route_bytes = route_workspace_size(max_tokens, self.n_experts, k)
         self.route_ws = torch.empty(self.route_bytes, dtype=torch.uint8, device=gate.device)
         self.status_word = torch.zeros(1, dtype=torch.int32, device=gate.device)
+        self._ws, self._status = self.ws.data_ptr(), self.status_word.data_ptr()
 
     def route(self, logits):
         """(ids, w, offsets, perm, inv_perm) of fp32 logits [T][experts] by the layer's rule."""
         import torch
-        T, E, k = logits.shape[0], self.n_experts, self.k
-        _contiguous(logits, "logits", (T, E), torch.float32)
+        T, E, k, dev = logits.shape[0], self.n_experts, self.k, torch.cuda.current_device()
+        _contiguous(logits, "logits", (T, E), torch.float32, dev)
         new = lambda *s: torch.empty(s, dtype=torch.int32, device=logits.device)  # noqa: E731
         ids, counts, offsets, perm, inv = new(T, k), new(E), new(E + 1), new(T * k), new(T * k)
         w = torch.empty((T, k), dtype=torch.float32, device=logits.device)
         route_scored(logits.data_ptr(), T, E, k, self.rule, ids.data_ptr(), w.data_ptr(),
                      counts.data_ptr(), offsets.data_ptr(), perm.data_ptr(), inv.data_ptr(),
                      self.status_word.data_ptr(), self.route_ws.data_ptr(), self.route_bytes,
-                     _stream())
+                     _stream(dev))
         return ids, w, offsets, perm, inv
 
     def forward(self, x, ids, w, offsets, perm, inv_perm, gate=None, out=None):
         """The experts' combined output [T][hidden] for tokens routed by route() or route_topk (perm,
         the inverse of inv_perm, is not read)."""
         import torch
-        T, k, E = x.shape[0], self.k, self.n_experts
-        i32, f32 = torch.int32, torch.float32
-        _contiguous(x, "x", (T, self.hidden))
-        _contiguous(ids, "ids", (T, k), i32)
-        _contiguous(w, "w", (T, k), f32)
-        _contiguous(offsets, "offsets", (E + 1,), i32)
-        _contiguous(inv_perm, "inv_perm", (T * k,), i32)
+        T, k, E, dev = x.shape[0], self.k, self.n_experts, torch.cuda.current_device()
+        i32, f32, rows = torch.int32, torch.float32, (T, self.hidden)
+        _contiguous(x, "x", rows, _FLOATS, dev)
+        _contiguous(ids, "ids", (T, k), i32, dev)
+        _contiguous(w, "w", (T, k), f32, dev)
+        _contiguous(offsets, "offsets", (E + 1,), i32, dev)
+        _contiguous(inv_perm, "inv_perm", (T * k,), i32, dev)
         if gate is not None:
-            _contiguous(gate, "gate", (T,), f32)
+            _contiguous(gate, "gate", (T,), f32, dev)
         if out is None:
             out = torch.empty_like(x)
-        _contiguous(out, "out", (T, self.hidden))
+        else:
+            _contiguous(out, "out", rows, _FLOATS, dev)
         scaled_experts(self.weights, x.data_ptr(), dtype_of(x), T, k, ids.data_ptr(),
                        w.data_ptr(), offsets.data_ptr(), inv_perm.data_ptr(),
                        None if gate is None else gate.data_ptr(), out.data_ptr(), dtype_of(out),
-                       self.status_word.data_ptr(), self.ws.data_ptr(), self.ws_bytes, _stream())
+                       self._status, self._ws, self.ws_bytes, _stream(dev))
         return out
 
     def __call__(self, x, logits, gate=None, out=None):

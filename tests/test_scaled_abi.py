@@ -161,7 +161,7 @@ def test_binding_constants_match_the_header(moe):
 def test_layer_refuses_tensors_of_another_form(moe):
     import torch
     with pytest.raises(ValueError):        # not on a CUDA device
-        moe._contiguous(torch.zeros(2, 2), "x")
+        moe._contiguous(torch.zeros(2, 2), "x", (2, 2), torch.float32, 0)
     with pytest.raises(moe.MoeError):
         moe.dtype_of(torch.zeros(1, dtype=torch.float64))
 
