@@ -64,6 +64,7 @@ constexpr uint64_t kWaitNs = 2000000000ull;    // limit of every wait
 // Registers: 640 threads launch with 96 each (61440); the first warpgroup keeps 64 and the four
 // epilogue warpgroups take 104: 128 * 64 + 512 * 104 = 61440.
 constexpr int kLaunchRegs = 96, kRoleRegs = 64, kEpiRegs = 104;
+static_assert(kAccs == 2, "the epilogue flips between two accumulators");
 static_assert(sizeof(Job) == sizeof(int4), "a slice is loaded as one vector");
 static_assert(128 * kRoleRegs + 512 * kEpiRegs <= kThreads * kLaunchRegs, "register split");
 
@@ -152,27 +153,34 @@ struct Pos {                          // ring position
     }
 };
 
-// Bounded wait; false once this CTA gives up.  The clock and the abort flag are looked at once in
-// 64 tries: reading the global timer between tries would delay the wake-up.
-__device__ __forceinline__ bool wait1(Shared &S, uint64_t *bar, uint32_t parity, uint32_t *st) {
+// Bounded wait of a whole warp, with one answer: false once this CTA gives up.  The clock and the
+// abort flag are looked at once in 64 tries: reading the global timer between tries would delay
+// the wake-up.  The vote keeps the loop uniform.
+__device__ __forceinline__ bool waitw(Shared &S, uint64_t *bar, uint32_t parity, uint32_t *st) {
+    if (__all_sync(kFull, mbar_try_wait(bar, parity))) return true;
     uint64_t t0 = 0;
 #pragma unroll 1
-    for (uint32_t i = 0; !mbar_try_wait(bar, parity); i++) {
-        if ((i & 63u) != 63u) continue;
-        if (*(volatile int *)&S.abort) return false;
+    for (uint32_t i = 1; !__all_sync(kFull, mbar_try_wait(bar, parity)); i++) {
+        if (i & 63u) continue;
         const uint64_t t = globaltimer();
         if (t0 == 0) t0 = t;
-        if (t - t0 > kWaitNs) {
+        const bool late = t - t0 > kWaitNs;
+        if (late) {
             *(volatile int *)&S.abort = 1;
             set_status(st, MOE_ERR_TIMEOUT);
-            return false;
         }
+        if (__any_sync(kFull, late || *(volatile int *)&S.abort)) return false;
     }
     return true;
 }
-// The same for a whole warp, with one answer.
-__device__ __forceinline__ bool waitw(Shared &S, uint64_t *bar, uint32_t parity, uint32_t *st) {
-    return __all_sync(0xffffffffu, wait1(S, bar, parity, st));
+// One arrival of the warp, without a branch.
+__device__ __forceinline__ void arrive1(uint64_t *bar, bool mine) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "@p mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];\n\t}" ::"r"(smem_u32(bar)),
+        "r"((uint32_t)mine)
+        : "memory");
 }
 
 template <int kMode>
@@ -221,7 +229,7 @@ __device__ void produce(const TcArgs &a, Shared &S, uint8_t *ring, int tiles, co
     for (int j = max(0, issued - kStages); j < issued; j++) {
         const uint32_t ph = (uint32_t)(j / kStages) & 1u;
         if (ok)
-            wait1(S, &S.empty[j % kStages], ph, a.status);
+            waitw(S, &S.empty[j % kStages], ph, a.status);
         else
             mbar_wait_bounded(&S.full[j % kStages], ph, kWaitNs);
     }
@@ -351,12 +359,13 @@ __device__ __forceinline__ void store16(T *p, const float *acc) {
 
 template <int kMode, typename T>
 __device__ void finish(const TcArgs &a, Shared &S, int tiles, uint32_t tmem) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(kFull, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int quad = warp & 3, part = (warp - kEpiWarp0) >> 2;
     const int row = quad * 32 + lane;
     constexpr bool kHalfY = kMode == kDown && sizeof(T) == 2;
     const uint32_t base = tmem + ((uint32_t)quad << 21) + (uint32_t)(part * 32);  // lane quad * 32
-    Pos q, p;
+    uint32_t q = 0, qph = 0;            // accumulator and its phase
+    Pos p;
     int u = 0;                          // block within the scale ring's group
     uint32_t par = 0;
     int i = blockIdx.x;
@@ -375,7 +384,7 @@ __device__ void finish(const TcArgs &a, Shared &S, int tiles, uint32_t tmem) {
             if (u == 0 && !waitw(S, &S.sc_full[p.s], p.ph, a.status)) return;
             const float v = S.as[p.s][u][row];
             const float2 w = S.ws[p.s][u];
-            if (!waitw(S, &S.acc_full[q.s], q.ph, a.status)) return;
+            if (!waitw(S, &S.acc_full[q], qph, a.status)) return;
             if (busy) {
                 const float f[2] = {v * w.x, v * w.y};
                 if (kHalfY) {
@@ -383,7 +392,7 @@ __device__ void finish(const TcArgs &a, Shared &S, int tiles, uint32_t tmem) {
                     top[1] = fmaxf(top[1], fabsf(f[1]));
                 }
                 tc_fence_after();
-                const uint32_t d = base + (uint32_t)(q.s * kNW);
+                const uint32_t d = base + q * kNW;
 #pragma unroll
                 for (int o = 0; o < 2; o++) {
 #pragma unroll
@@ -397,11 +406,12 @@ __device__ void finish(const TcArgs &a, Shared &S, int tiles, uint32_t tmem) {
                 tc_fence_before();
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(&S.acc_empty[q.s]);
-            q.next(kAccs);
+            arrive1(&S.acc_empty[q], lane == 0);
+            qph ^= q;                            // after the second accumulator
+            q ^= 1u;
             if (++u == kGroup) {
                 u = 0;
-                if (lane == 0) mbar_arrive(&S.sc_empty[p.s]);
+                arrive1(&S.sc_empty[p.s], lane == 0);
                 p.next(kScales);
             }
         }
@@ -508,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ uint8_t raw[];
     uint8_t *ring = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
     Shared &S = *reinterpret_cast<Shared *>(ring + (size_t)kStages * kStage);
-    const int warp = threadIdx.x >> 5;
+    const int warp = __shfl_sync(kFull, (int)threadIdx.x >> 5, 0);
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; i++) {
             mbar_init(&S.full[i], 1);
