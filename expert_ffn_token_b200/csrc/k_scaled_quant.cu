@@ -1,8 +1,12 @@
 // k_scaled_quant.cu -- activations to e4m3 with one fp32 scale per row and 128 columns.
 //
-// Reads every value once and writes a byte per value and 4 bytes per 128: bound by memory.  A
-// warp takes four rows of one column block, so that four loads are in flight per lane and the
-// four scales, neighbours in the block-major scale array, go out together.
+// Reads every value once and writes a byte per value and 4 bytes per 128.  16-bit rows are bound by
+// instructions before memory, so the work is laid out to need few: a half warp holds a block, 8
+// values per lane in one 16-byte load, so that its 16 lanes all end up with the block's largest
+// magnitude after four shuffles and take the division without passing it around; 16-bit
+// magnitudes are compared two at a time.  A warp takes four rows of two neighbouring blocks, so
+// that four loads are in flight and the scales of four rows, neighbours in the block-major scale
+// array, go out together.
 #include "route_dev.cuh"
 #include "scaled.cuh"
 
@@ -70,24 +74,65 @@ __device__ void list_slices(const SliceArgs &a, uint32_t *status) {
     if (threadIdx.x == 0) *a.nslices = n + ns;
 }
 
-template <typename T, bool kVec>
-__device__ __forceinline__ void load_rows(const T *x, int64_t t0, int c, int rows, int K,
-                                          int64_t ldx, float4 (&v)[kRows]) {
-#pragma unroll
-    for (int i = 0; i < kRows; i++) {
-        v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (t0 + i >= rows) continue;
-        const T *p = x + (t0 + i) * ldx + c;
-        if (kVec) {
-            if (c < K) v[i] = load4(p);
-        } else {
-            if (c < K) v[i].x = to_f32(p[0]);
-            if (c + 1 < K) v[i].y = to_f32(p[1]);
-            if (c + 2 < K) v[i].z = to_f32(p[2]);
-            if (c + 3 < K) v[i].w = to_f32(p[3]);
-        }
-    }
+__device__ __forceinline__ float4 widen4(uint32_t a, uint32_t b, __nv_bfloat16 *) {
+    return make_float4(__uint_as_float(a << 16), __uint_as_float(a & 0xffff0000u),
+                       __uint_as_float(b << 16), __uint_as_float(b & 0xffff0000u));
 }
+__device__ __forceinline__ float4 widen4(uint32_t a, uint32_t b, __half *) {
+    const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&a));
+    const float2 y = __half22float2(*reinterpret_cast<const __half2 *>(&b));
+    return make_float4(x.x, x.y, y.x, y.y);
+}
+
+// Eight consecutive values of a row as they came.
+template <typename T>
+struct Eight {                          // 16-bit types, two per word
+    uint32_t w[4];
+    __device__ __forceinline__ void clear() { w[0] = w[1] = w[2] = w[3] = 0u; }
+    __device__ __forceinline__ void load(const T *p) {
+        const uint4 r = __ldg(reinterpret_cast<const uint4 *>(p));
+        w[0] = r.x, w[1] = r.y, w[2] = r.z, w[3] = r.w;
+    }
+    __device__ __forceinline__ void load(const T *p, int n) {
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+            if (i < n)
+                w[i / 2] |= (uint32_t)reinterpret_cast<const uint16_t *>(p)[i] << (16 * (i & 1));
+    }
+    __device__ __forceinline__ float4 quad(int i) const { return widen4(w[2 * i], w[2 * i + 1], (T *)nullptr); }
+    // the largest magnitude as an fp32 pattern (an infinity or NaN has the largest ones)
+    __device__ __forceinline__ uint32_t largest() const {
+        const uint32_t m = __vmaxu2(__vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu),
+                                    __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
+        const uint16_t h = (uint16_t)max(m & 0xffffu, m >> 16);
+        return __float_as_uint(to_f32(*reinterpret_cast<const T *>(&h)));
+    }
+};
+template <>
+struct Eight<float> {
+    float f[8];
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < 8; i++) f[i] = 0.f;
+    }
+    __device__ __forceinline__ void load(const float *p) {
+        const float4 a = load4(p), b = load4(p + 4);
+        f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
+        f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+    }
+    __device__ __forceinline__ void load(const float *p, int n) {
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+            if (i < n) f[i] = p[i];
+    }
+    __device__ __forceinline__ float4 quad(int i) const {
+        return make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+    }
+    __device__ __forceinline__ uint32_t largest() const {
+        return max(abs_bits(make_float4(f[0], f[1], f[2], f[3])),
+                   abs_bits(make_float4(f[4], f[5], f[6], f[7])));
+    }
+};
 
 template <typename T, bool kVec, typename To>
 __global__ void __launch_bounds__(kThreads)
@@ -101,49 +146,91 @@ __global__ void __launch_bounds__(kThreads)
         }
     }
     const int lane = threadIdx.x & 31;
-    const int nb = sblocks(K);
-    const int64_t unit = (int64_t)cta * (kThreads / 32) + (threadIdx.x >> 5);
-    const int64_t rt = unit / nb;
-    const int b = (int)(unit - rt * nb);
-    const int64_t t0 = rt * kRows;
+    const uint32_t pairs = ((uint32_t)sblocks(K) + 1) / 2;
+    const uint32_t unit = (uint32_t)cta * (kThreads / 32) + (threadIdx.x >> 5);
+    const uint32_t rt = unit / pairs, pr = unit - rt * pairs;
+    const int64_t t0 = (int64_t)rt * kRows;
     if (t0 >= rows) return;
-    const int c = b * kSBlk + lane * 4;
-    float4 v[kRows];
-    load_rows<T, kVec>(x, t0, c, rows, K, ldx, v);
-    // the largest magnitudes as integers (a NaN or an infinity has the largest bit patterns);
-    // lane i takes row i's scale and reciprocal, one division for the four
-    uint32_t top = 0;
+    const int b = 2 * (int)pr + (lane >> 4), c = 2 * (int)pr * kSBlk + lane * 8;
+    Eight<T> v[kRows];
 #pragma unroll
     for (int i = 0; i < kRows; i++) {
-        const uint32_t m = __reduce_max_sync(0xffffffffu, abs_bits(v[i]));
-        if (lane == i) top = m;
+        v[i].clear();
+        if (t0 + i >= rows || c >= K) continue;
+        const T *p = x + (t0 + i) * ldx + c;
+        if (kVec)
+            v[i].load(p);
+        else
+            v[i].load(p, K - c);
     }
-    const bool bad = top >= 0x7f800000u;
-    const float sc = bad ? 0.f : __fdiv_rn(__uint_as_float(top), kE4M3Max);
-    const float inv = sc > 0.f ? __frcp_rn(sc) : 0.f;
+    float sc[kRows];
+    uint2 q[kRows];
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < kRows; i++) {
+        uint32_t top = v[i].largest();
+#pragma unroll
+        for (int o = 8; o >= 1; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        sc[i] = scale_of(top);
+        bad = bad || top >= 0x7f800000u;
+        float inv;                     // 1 / scale within 2^-23, inf for 0
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(sc[i]));
+        const float below = inv * kBelow, above = inv * kAbove;
+        const float4 a = v[i].quad(0), d = v[i].quad(1);
+        q[i] = make_uint2(quant4_at(a, below), quant4_at(d, below));
+        const uint2 hi = make_uint2(quant4_at(a, above), quant4_at(d, above));
+        if (sc[i] < 0x1p-100f) {       // zero, not finite, or too small for the arithmetic below
+            q[i] = sc[i] > 0.f ? make_uint2(quant4_wide(a, sc[i]), quant4_wide(d, sc[i]))
+                               : make_uint2(0u, 0u);
+        } else if (q[i].x != hi.x || q[i].y != hi.y) {
+            // one in 200 of 16-bit values is halfway or close: decided one by one
+            const float f[8] = {a.x, a.y, a.z, a.w, d.x, d.y, d.z, d.w};
+#pragma unroll 1
+            for (uint32_t x = q[i].x ^ hi.x, y = q[i].y ^ hi.y; x | y;) {
+                const int n = x ? (__ffs(x) - 1) >> 3 : 4 + ((__ffs(y) - 1) >> 3);
+                float val = f[0];
+#pragma unroll
+                for (int e = 1; e < 8; e++) val = n == e ? f[e] : val;
+                const uint32_t shift = 8 * (n & 3), mask = 0xffu << shift;
+                const uint32_t l = ((n < 4 ? q[i].x : q[i].y) >> shift) & 0xffu;
+                const uint32_t h = ((n < 4 ? hi.x : hi.y) >> shift) & 0xffu;
+                const uint32_t c8 = quant1_decide(val, sc[i], l, h) << shift;
+                if (n < 4) {
+                    q[i].x = (q[i].x & ~mask) | c8;
+                    x &= ~mask;
+                } else {
+                    q[i].y = (q[i].y & ~mask) | c8;
+                    y &= ~mask;
+                }
+            }
+        }
+    }
     if (bad) set_status(status, MOE_ERR_NONFINITE);
-    uint32_t p[kRows];
+    // lane 16 h + i holds the scale of row i, block h
+    float mine = sc[0];
 #pragma unroll
-    for (int i = 0; i < kRows; i++) {
-        const float s = __shfl_sync(0xffffffffu, sc, i), r = __shfl_sync(0xffffffffu, inv, i);
-        p[i] = s > 0.f ? quant4(v[i], s, r) : 0u;
-    }
+    for (int i = 1; i < kRows; i++) mine = (lane & 15) == i ? sc[i] : mine;
+    const bool scale_lane = (lane & 15) < kRows && t0 + (lane & 15) < rows;
     for (int j = 0; j < to.count(); j++) {
         int64_t at = -1;
-        if (lane < kRows && t0 + lane < rows) {
-            at = to.row(t0 + lane, j, status);
-            if (at >= 0) to.s[b * to.lds + at] = sc;
+        if (scale_lane) {
+            at = to.row(t0 + (lane & 15), j, status);
+            if (at >= 0 && b * kSBlk < K) to.s[b * to.lds + at] = mine;
         }
 #pragma unroll
         for (int i = 0; i < kRows; i++) {
-            const int64_t r = __shfl_sync(0xffffffffu, at, i);
-            if (r < 0) continue;
+            int64_t r;
+            if constexpr (To::kList)
+                r = __shfl_sync(0xffffffffu, at, i);
+            else
+                r = t0 + i < rows ? t0 + i : -1;
+            if (r < 0 || c >= K) continue;
             uint8_t *o = to.q + r * to.ldq + c;
-            if (c + 3 < K) {
-                *reinterpret_cast<uint32_t *>(o) = p[i];
+            if (c + 8 <= K) {
+                *reinterpret_cast<uint2 *>(o) = q[i];
             } else {
-                for (int n = 0; n < 3; n++)
-                    if (c + n < K) o[n] = (uint8_t)(p[i] >> (8 * n));
+                for (int n = 0; n < 7; n++)
+                    if (c + n < K) o[n] = (uint8_t)((n < 4 ? q[i].x : q[i].y) >> (8 * (n & 3)));
             }
         }
     }
@@ -153,13 +240,13 @@ template <typename To>
 cudaError_t run(const void *x, int dt, int T, int K, int64_t ldx, const To &to, uint32_t *status,
                 cudaStream_t st) {
     if (T <= 0) return cudaSuccess;
-    const int64_t units = (int64_t)((T + kRows - 1) / kRows) * sblocks(K);
+    const int64_t units = (int64_t)((T + kRows - 1) / kRows) * ((sblocks(K) + 1) / 2);
     const unsigned grid = (unsigned)((units + kThreads / 32 - 1) / (kThreads / 32)) + To::kList;
     return with_dtype(dt, [&](auto *tag) {
         using E = std::remove_pointer_t<decltype(tag)>;
         const E *p = static_cast<const E *>(x);
-        // vector loads where every lane's four elements start on their natural boundary
-        const bool vec = ((uintptr_t)x % (4 * sizeof(E))) == 0 && ldx % 4 == 0 && K % 4 == 0;
+        // vector loads where every lane's eight elements start on a 16-byte boundary
+        const bool vec = (uintptr_t)x % 16 == 0 && ldx * sizeof(E) % 16 == 0 && K % 8 == 0;
         if (vec)
             k_scaled_quantize<E, true, To><<<grid, kThreads, 0, st>>>(p, T, K, ldx, to, status);
         else

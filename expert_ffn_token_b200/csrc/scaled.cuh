@@ -87,41 +87,49 @@ static __device__ __noinline__ uint32_t quant4_wide(float4 v, float s) {
     return cvt_e4m3x2(f[0], f[1]) | (cvt_e4m3x2(f[2], f[3]) << 16);
 }
 
-// The sum of two e4m3 values, halved (exact in fp16), for the two pairs of bytes in a and b.
-__device__ __forceinline__ float2 e4m3_middle(uint32_t a, uint32_t b) {
-    uint32_t x, y;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(x) : "h"((uint16_t)a));
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(y) : "h"((uint16_t)b));
-    const __half2 m = __hmul2(__hadd2(*reinterpret_cast<__half2 *>(&x), *reinterpret_cast<__half2 *>(&y)),
-                              __float2half2_rn(0.5f));
-    return __half22float2(m);
+// The scale amax / 448 of a largest magnitude given as an fp32 pattern, 0 when it is not finite.  A
+// product with 1 / 448, its exact remainder and one more multiply-add give the correctly rounded
+// quotient; near the subnormals, where the remainder may underflow, the division does.
+__device__ __forceinline__ float scale_of(uint32_t top) {
+    const float x = __uint_as_float(top);
+    constexpr float r = 1.0f / kE4M3Max;
+    const float q = x * r;
+    const float s = fmaf(fmaf(-q, kE4M3Max, x), r, q);
+    if (top >= 0x7f800000u) return 0.f;
+    return x < 0x1p-90f ? __fdiv_rn(x, kE4M3Max) : s;
 }
 
-// Four values of a block with scale s > 0 as packed e4m3.  v * RN(1/s) is within 2^-23 of v / s
-// (relative); when the values 2^-21 below and above it convert to the same byte, so does v / s
-// (conversion is monotone).  Otherwise they are neighbours, and v is compared with s times the
-// value halfway between them, exactly, in one multiply-add: equal goes to the even byte.  16-bit
-// inputs are halfway often (their quotients have few bits), so this costs no 64-bit division.
+// v / s to e4m3 where it lies between the neighbouring codes l and h (of v's sign, |l| < |h|): v is
+// compared with s times the value halfway between them, exactly, in one multiply-add; equal goes
+// to the even code.
+__device__ __forceinline__ uint32_t quant1_decide(float v, float s, uint32_t l, uint32_t h) {
+    uint32_t x;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(x) : "h"((uint16_t)(l | (h << 8))));
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&x));
+    const float r = fmaf(-0.5f * fabsf(f.x + f.y), s, fabsf(v));      // the sum and half are exact
+    return r > 0.f || (r == 0.f && (l & 1u)) ? h : l;
+}
+
+// Four values of a block with scale s > 0 as packed e4m3.  v / s by a reciprocal within 2^-23 of
+// 1 / s is within 2^-21; when the values 2^-21 below and above it convert to the same byte, so
+// does v / s (conversion is monotone).  Otherwise they are neighbours and quant1_decide tells.
+// 16-bit inputs are halfway often (their quotients have few bits), so this costs no division.
+constexpr float kBelow = 1.0f - 0x1p-21f, kAbove = 1.0f + 0x1p-21f;
+__device__ __forceinline__ uint32_t quant4_at(float4 v, float r) {
+    return cvt_e4m3x2(v.x * r, v.y * r) | (cvt_e4m3x2(v.z * r, v.w * r) << 16);
+}
 __device__ __forceinline__ uint32_t quant4(float4 v, float s, float inv) {
+    const uint32_t lo = quant4_at(v, inv * kBelow), hi = quant4_at(v, inv * kAbove);
     if (s < 0x1p-100f) return quant4_wide(v, s);       // 1 / s or the exact remainder underflows
-    const float a = v.x * inv, b = v.y * inv, c = v.z * inv, d = v.w * inv;
-    constexpr float kLo = 1.0f - 0x1p-21f, kHi = 1.0f + 0x1p-21f;
-    uint32_t lo = cvt_e4m3x2(a * kLo, b * kLo) | (cvt_e4m3x2(c * kLo, d * kLo) << 16);
-    const uint32_t hi = cvt_e4m3x2(a * kHi, b * kHi) | (cvt_e4m3x2(c * kHi, d * kHi) << 16);
-    if (lo != hi) {
-        const float2 m0 = e4m3_middle(lo & 0xffffu, hi & 0xffffu), m1 = e4m3_middle(lo >> 16, hi >> 16);
-        const float f[4] = {v.x, v.y, v.z, v.w}, m[4] = {m0.x, m0.y, m1.x, m1.y};
-        uint32_t out = 0;
+    if (lo == hi) return lo;
+    const float f[4] = {v.x, v.y, v.z, v.w};
+    uint32_t out = 0;
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-            const uint32_t l = (lo >> (8 * i)) & 0xffu, h = (hi >> (8 * i)) & 0xffu;
-            const float r = fmaf(-fabsf(m[i]), s, fabsf(f[i]));
-            const bool up = r > 0.f || (r == 0.f && (l & 1u));
-            out |= (up ? h : l) << (8 * i);
-        }
-        lo = out;
+    for (int i = 0; i < 4; i++) {
+        const uint32_t l = (lo >> (8 * i)) & 0xffu, h = (hi >> (8 * i)) & 0xffu;
+        out |= (l == h ? l : quant1_decide(f[i], s, l, h)) << (8 * i);
     }
-    return lo;
+    return out;
 }
 
 // The largest magnitude of four values, as the integer whose order it follows.
@@ -135,10 +143,9 @@ __device__ __forceinline__ uint32_t abs_bits(float4 v) {
 // scale 0) when a value was not finite.
 __device__ __forceinline__ uint32_t quant_block(float4 v, float *s, bool *finite) {
     const uint32_t amax = __reduce_max_sync(0xffffffffu, abs_bits(v));
-    const bool fin = amax < 0x7f800000u;
-    const float sc = fin ? __fdiv_rn(__uint_as_float(amax), kE4M3Max) : 0.0f;
+    const float sc = scale_of(amax);
     *s = sc;
-    *finite = fin;
+    *finite = amax < 0x7f800000u;
     return sc > 0.0f ? quant4(v, sc, __frcp_rn(sc)) : 0u;
 }
 
