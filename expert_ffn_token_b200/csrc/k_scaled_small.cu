@@ -668,24 +668,6 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
     }
 }
 
-// Launched behind the previous kernel of the stream (programmatic dependent launch).
-template <typename... P, typename... Q>
-cudaError_t launch_behind(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t st, Q... args) {
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads);
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const cudaError_t err = cudaLaunchKernelEx(&cfg, kernel, args...);
-    if (err != cudaSuccess) return err;
-    note_launches(1);
-    return cudaGetLastError();
-}
-
 }  // namespace
 
 cudaError_t launch_scaled_small(const ScaledMatmulArgs &a, cudaStream_t st) {
@@ -718,7 +700,7 @@ cudaError_t launch_scaled_experts_small(const ScaledExpertsArgs &e, void *ws, cu
         if (err != cudaSuccess) return err;
         return with_dtype(a.out_dt, [&](auto *tag) {
             using E = std::remove_pointer_t<decltype(tag)>;
-            return launch_behind(k_one_down<E>, dim3(a.w.hidden / kTile), kWarps * 32, st, a);
+            return launch_behind(k_one_down<E>, dim3(a.w.hidden / kTile), kWarps * 32, 0, st, a);
         });
     }
     FewWs f;
@@ -731,11 +713,11 @@ cudaError_t launch_scaled_experts_small(const ScaledExpertsArgs &e, void *ws, cu
         return cudaGetLastError();
     });
     if (err != cudaSuccess) return err;
-    err = launch_behind(k_few_gateup, dim3(sblocks(a.w.ffn), jobs), kFewThreads, st, a, f);
+    err = launch_behind(k_few_gateup, dim3(sblocks(a.w.ffn), jobs), kFewThreads, 0, st, a, f);
     if (err != cudaSuccess) return err;
     return with_dtype(a.out_dt, [&](auto *tag) {
         using E = std::remove_pointer_t<decltype(tag)>;
-        return launch_behind(k_few_down<E>, dim3(a.w.hidden / kTile), kWarps * 32, st, a, f);
+        return launch_behind(k_few_down<E>, dim3(a.w.hidden / kTile), kWarps * 32, 0, st, a, f);
     });
 }
 

@@ -18,6 +18,7 @@
 // one chunk is routed and grouped by one CTA in one launch.
 #include <math.h>
 
+#include "ptx.cuh"
 #include "route_dev.cuh"
 #include "scaled.cuh"
 
@@ -49,6 +50,10 @@ struct Score {
 __device__ __forceinline__ uint32_t order_key(float v) {
     const uint32_t b = __float_as_uint(v + 0.0f);        // -0 and 0 are one value
     return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+
+__device__ __forceinline__ float key_value(uint32_t k) {
+    return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
 }
 
 // Rounds of argmax over v[NV] per lane (element i of a lane is expert lane + 32 i), ties to the
@@ -130,24 +135,29 @@ __device__ void route_row(const float *__restrict__ src, int E, int k, const moe
     const float *bias = rule.d_bias;
     const bool sigmoid = rule.score == MOE_SCORE_SIGMOID;
     float l[NV], top = -INFINITY, size = 0.f;
-    bool fin = true;
+    uint32_t mag = 0;                     // the largest magnitude: not finite from 0x7f800000 on
 #pragma unroll
     for (int i = 0; i < NV; i++) {
         const int e = lane + 32 * i;
-        l[i] = e < E ? __ldg(src + e) : -INFINITY;
-        fin = fin && (e >= E || isfinite(l[i]));
+        l[i] = -INFINITY;
+        if (e < E) {
+            l[i] = __ldg(src + e);
+            mag = max(mag, __float_as_uint(l[i]) & 0x7fffffffu);
+        }
         top = fmaxf(top, l[i]);
     }
     if (bias) {
+        uint32_t b = 0;
 #pragma unroll
         for (int i = 0; i < NV; i++) {
             const int e = lane + 32 * i;
-            const float b = e < E ? __ldg(bias + e) : 0.f;
-            fin = fin && isfinite(b);
-            size = fmaxf(size, fabsf(b));
+            if (e < E) b = max(b, __float_as_uint(__ldg(bias + e)) & 0x7fffffffu);
         }
+        b = __reduce_max_sync(kFull, b);
+        size = __uint_as_float(b);
+        mag = max(mag, b);
     }
-    if (!__all_sync(kFull, fin)) {
+    if (__any_sync(kFull, mag >= 0x7f800000u)) {
         if (lane < k) {
             ids[lane] = lane;
             w[lane] = __fdiv_rn(1.0f, (float)k);
@@ -181,7 +191,6 @@ __device__ void route_row(const float *__restrict__ src, int E, int k, const moe
     float v[NV];
     float err = 0.f;
     if (need) {
-        if (bias) size = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(size)));
         err = 0x1p-19f * (1.0f + size);
 #pragma unroll
         for (int i = 0; i < NV; i++) {
@@ -198,25 +207,52 @@ __device__ void route_row(const float *__restrict__ src, int E, int k, const moe
     int per = E;
     if (grouped) {
         per = E / rule.n_group;
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < NV; i++) {
-            const int e = lane + 32 * i;
-            if (e < E) row[e + (e >> 5)] = v[i];
-        }
-        __syncwarp();
-        int width = 32;                   // lanes per group
+        const bool lined = per % 32 == 0;             // a group is whole registers of the warp
+        float value = -INFINITY;                      // lane g: the value of group g
+        int width = 32;                               // else: lanes per group
         while (width > 1 && 32 / width < rule.n_group) width >>= 1;
         const int g = lane / width, base = g * per;
         const bool mine = g < rule.n_group;
-        float value = group_value<float>(mine ? per : 0, lane % width, width, width, rule.group_top,
-                                         [&](int i) {
-                                             const int e = base + i;
-                                             return row[e + (e >> 5)];
-                                         });
+        if (lined) {
+            const int regs = per >> 5;
+            int left = regs, at_group = 0;
+            uint32_t b1 = 0, b2 = 0;                  // this lane's two largest of the group
+#pragma unroll
+            for (int i = 0; i < NV; i++) {
+                const uint32_t x = order_key(v[i]);
+                b2 = max(b2, min(b1, x));
+                b1 = max(b1, x);
+                if (--left == 0) {                    // the group's last register
+                    const uint32_t m1 = __reduce_max_sync(kFull, b1);
+                    float sum = key_value(m1);
+                    if (rule.group_top == 2) {
+                        const unsigned at = __ballot_sync(kFull, b1 == m1);
+                        const uint32_t m2 = __reduce_max_sync(kFull, b1 == m1 ? b2 : b1);
+                        sum += key_value(at & (at - 1) ? m1 : m2);
+                    }
+                    if (lane == at_group) value = sum;
+                    at_group++;
+                    left = regs;
+                    b1 = b2 = 0;
+                }
+            }
+        } else {
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < NV; i++) {
+                const int e = lane + 32 * i;
+                if (e < E) row[e + (e >> 5)] = v[i];
+            }
+            __syncwarp();
+            value = group_value<float>(mine ? per : 0, lane % width, width, width, rule.group_top,
+                                       [&](int i) {
+                                           const int e = base + i;
+                                           return row[e + (e >> 5)];
+                                       });
+            value = __shfl_sync(kFull, value, (lane * width) & 31);
+        }
         float gap;
-        keep = keep_groups(__shfl_sync(kFull, value, (lane * width) & 31), rule.n_group,
-                           rule.topk_group, &gap);
+        keep = keep_groups(value, rule.n_group, rule.topk_group, &gap);
         if (need && rule.topk_group < rule.n_group && gap <= 4.0f * err) {
             const double exact = group_value<double>(
                 mine ? per : 0, lane % width, width, width, rule.group_top, [&](int i) {
@@ -248,23 +284,27 @@ __device__ void route_row(const float *__restrict__ src, int E, int k, const moe
         bound = __reduce_max_sync(kFull, left);
         if (left == bound) left = 0;
     }
-    const uint32_t out_key = order_key(-INFINITY);
-    float least = -INFINITY;
-    if (bound > out_key) {
-        const float b = __uint_as_float(bound & 0x80000000u ? bound & 0x7fffffffu : ~bound);
-        least = err > 0.f ? b - 2.0f * err : b;
-    }
-    int n = 0;
+    float least = -3.402823466e+38f;      // every finite value: fewer than k lanes hold any
+    if (bound > order_key(-INFINITY)) least = key_value(bound) - 2.0f * err;
+    int held = 0;
 #pragma unroll
-    for (int i = 0; i < NV; i++) {
-        const bool in = v[i] >= least && v[i] > -INFINITY;
-        const unsigned m = __ballot_sync(kFull, in);
-        const int at = n + __popc(m & ((1u << lane) - 1u));
-        if (in && at < 32) cand[at] = lane + 32 * i;
-        n += __popc(m);
+    for (int i = 0; i < NV; i++) held += v[i] >= least;
+    int at = held;                        // places by a prefix sum over the lanes
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(kFull, at, o);
+        if (lane >= o) at += x;
+    }
+    const int n = __shfl_sync(kFull, at, 31);
+    at -= held;
+    if (n <= 32) {
+#pragma unroll
+        for (int i = 0; i < NV; i++)
+            if (v[i] >= least) cand[at++] = lane + 32 * i;
     }
     __syncwarp();
     int my_id = 0;
+    double s = 0.0;
     if (n > 32) {
         if (bias) {
             double d[NV];
@@ -284,30 +324,41 @@ __device__ void route_row(const float *__restrict__ src, int E, int k, const moe
             my_id = select_rounds<NV, float>(c, k);
         }
     } else {
-        // one candidate per lane, sorted by (value descending, id ascending)
-        my_id = lane < n ? cand[lane] : INT_MAX;
-        double d = -INFINITY;
+        // one candidate per lane, sorted by (value descending, id ascending); the lane a candidate
+        // came from rides in the id's low bits
+        double d = -INFINITY, own = 0.0;
+        int tag = INT_MAX;
         if (lane < n) {
-            const float x = __ldg(src + my_id);
-            d = bias ? score(x) + (double)__ldg(bias + my_id) : (double)x;
+            const int id = cand[lane];
+            const float x = __ldg(src + id);
+            tag = (id << 5) | lane;
+            if (bias || sigmoid) own = score(x);
+            d = bias ? own + (double)__ldg(bias + id) : (double)x;
+            if (!bias && !sigmoid) own = d;
         }
+        const int most = n <= 16 ? 16 : 32;
 #pragma unroll
         for (int size2 = 2; size2 <= 32; size2 <<= 1) {
+            if (size2 > most) break;
 #pragma unroll
             for (int o = size2 >> 1; o >= 1; o >>= 1) {
                 const double od = __shfl_xor_sync(kFull, d, o);
-                const int oi = __shfl_xor_sync(kFull, my_id, o);
-                const bool before = od > d || (od == d && oi < my_id);   // the other sorts first
+                const int oi = __shfl_xor_sync(kFull, tag, o);
+                const bool before = od > d || (od == d && oi < tag);     // the other sorts first
                 const bool first = ((lane & size2) == 0) == ((lane & o) == 0);
                 if (before == first) {
                     d = od;
-                    my_id = oi;
+                    tag = oi;
                 }
             }
         }
+        my_id = tag >> 5;
+        const double s0 = __shfl_sync(kFull, own, tag & 31);
+        s = bias || sigmoid ? s0 : exp(s0 - score.top) * score.inv;
     }
     __syncwarp();
-    const double s = lane < k ? score(__ldg(src + my_id)) : 0.0;
+    if (n > 32) s = lane < k ? score(__ldg(src + my_id)) : 0.0;
+    if (lane >= k) s = 0.0;
     double r = s;
     if (rule.renorm) {
         const double sum = warp_sum(s);
@@ -354,6 +405,7 @@ __global__ void __launch_bounds__(row_threads(NV), 1)
     k_scored_rows(const float *__restrict__ logits, int T, int E, int k, const moe_route_rule rule,
                   const RouteOut o, int32_t *chunk_counts) {
     constexpr int kThreads = row_threads(NV), kTokens = kThreads / 32;
+    ptx::launch_dependents();
     extern __shared__ float s_rows[];            // [warps][E + E / 32], when there are groups
     __shared__ int s_cnt[NV * 32];
     __shared__ int s_ids[kChunk * kMaxK];
@@ -391,13 +443,15 @@ __global__ void __launch_bounds__(row_threads(NV), 1)
 __global__ void __launch_bounds__(1024)
     k_scored_chunks(const int32_t *__restrict__ chunk_counts, int n_chunks, int E,
                     int32_t *chunk_base, int32_t *counts) {
+    ptx::grid_dependency_wait();
+    ptx::launch_dependents();
     __shared__ int s_sum[32][33];
     const int seg = threadIdx.x >> 5, lane = threadIdx.x & 31, e = blockIdx.x * 32 + lane;
     const int per = (n_chunks + 31) / 32, c0 = seg * per, c1 = min(n_chunks, c0 + per);
     int sum = 0;
     if (e < E) {
 #pragma unroll 4
-        for (int c = c0; c < c1; c++) sum += __ldg(chunk_counts + (size_t)c * E + e);
+        for (int c = c0; c < c1; c++) sum += __ldcg(chunk_counts + (size_t)c * E + e);
     }
     s_sum[seg][lane] = sum;
     __syncthreads();
@@ -412,7 +466,7 @@ __global__ void __launch_bounds__(1024)
     if (seg == 0) counts[e] = all;
     for (int c = c0; c < c1; c++) {
         chunk_base[(size_t)c * E + e] = run;
-        run += __ldg(chunk_counts + (size_t)c * E + e);
+        run += __ldcg(chunk_counts + (size_t)c * E + e);
     }
 }
 
@@ -424,8 +478,10 @@ __global__ void __launch_bounds__(256)
     __shared__ int s_ids[kChunk * kMaxK];
     __shared__ int s_warp[33];
     const int t0 = blockIdx.x * kChunk, n = min(kChunk, T - t0) * k;
-    for (int e = threadIdx.x; e < E; e += 256) s_base[e] = __ldg(o.counts + e);
-    for (int a = threadIdx.x; a < n; a += 256) s_ids[a] = __ldg(o.ids + (size_t)t0 * k + a);
+    // the ids were complete before k_scored_chunks let this kernel start
+    for (int a = threadIdx.x; a < n; a += 256) s_ids[a] = __ldcg(o.ids + (size_t)t0 * k + a);
+    ptx::grid_dependency_wait();
+    for (int e = threadIdx.x; e < E; e += 256) s_base[e] = __ldcg(o.counts + e);
     __syncthreads();
     const int total = block_exclusive_scan<256>(s_base, E, s_warp);
     if (blockIdx.x == 0) {
@@ -434,7 +490,7 @@ __global__ void __launch_bounds__(256)
         __syncthreads();
     }
     for (int e = threadIdx.x; e < E; e += 256)
-        s_base[e] += __ldg(chunk_base + (size_t)blockIdx.x * E + e);
+        s_base[e] += __ldcg(chunk_base + (size_t)blockIdx.x * E + e);
     __syncthreads();
     if (threadIdx.x < 32) place_pairs(s_ids, n, t0 * k, s_base, o.perm, o.inv_perm);
 }
@@ -596,13 +652,11 @@ cudaError_t launch_route_scored(const float *logits, int T, int E, int k,
     if (err != cudaSuccess) return err;
     const int n_chunks = (T + kChunk - 1) / kChunk;
     if (n_chunks == 1) return cudaSuccess;
-    k_scored_chunks<<<(E + 31) / 32, 1024, 0, st>>>(chunk_counts, n_chunks, E, chunk_base, counts);
-    note_launches(1);
-    err = cudaGetLastError();
+    err = launch_behind(k_scored_chunks, dim3((E + 31) / 32), 1024, 0, st, chunk_counts, n_chunks, E,
+                        chunk_base, counts);
     if (err != cudaSuccess) return err;
-    k_scored_place<<<n_chunks, 256, (size_t)E * sizeof(int), st>>>(T, E, k, chunk_base, o);
-    note_launches(1);
-    return cudaGetLastError();
+    return launch_behind(k_scored_place, dim3(n_chunks), 256, (size_t)E * sizeof(int), st, T, E, k,
+                         chunk_base, o);
 }
 
 }  // namespace moe

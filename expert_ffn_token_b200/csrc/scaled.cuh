@@ -151,6 +151,28 @@ __device__ __forceinline__ uint32_t quant_block(float4 v, float *s, bool *finite
 
 // ------------------------------------------------------------------ launchers
 
+// Launch behind the previous kernel of the stream (programmatic dependent launch): the kernel may
+// start once every CTA of that one has called launch_dependents or ended, and sees its results
+// after grid_dependency_wait.
+template <typename... P, typename... Q>
+cudaError_t launch_behind(void (*kernel)(P...), dim3 grid, int threads, size_t smem,
+                          cudaStream_t st, Q... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t err = cudaLaunchKernelEx(&cfg, kernel, args...);
+    if (err != cudaSuccess) return err;
+    note_launches(1);
+    return cudaGetLastError();
+}
+
 // ws: moe_route_workspace_size bytes.
 cudaError_t launch_route_scored(const float *logits, int T, int E, int k,
                                 const moe_route_rule &rule, int32_t *ids, float *w,
