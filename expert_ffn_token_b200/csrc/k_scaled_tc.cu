@@ -60,6 +60,7 @@ constexpr int kGroup = 4;                      // blocks whose scales are handed
 constexpr int kScales = 4;                     // depth of the scale ring, in groups
 constexpr int kPatch = 8;                      // columns per turn through shared memory (stores)
 constexpr uint32_t kTmemCols = 512;
+static_assert(kEpiWarps * 32 * 33 * 4 <= kStages * kStage, "the ring holds every warp's 32 columns");
 constexpr uint64_t kWaitNs = 2000000000ull;    // limit of every wait
 // Registers: 640 threads launch with 96 each (61440); the first warpgroup keeps 64 and the four
 // epilogue warpgroups take 104: 128 * 64 + 512 * 104 = 61440.
@@ -358,7 +359,7 @@ __device__ __forceinline__ void store16(T *p, const float *acc) {
 }
 
 template <int kMode, typename T>
-__device__ void finish(const TcArgs &a, Shared &S, int tiles, uint32_t tmem) {
+__device__ void finish(const TcArgs &a, Shared &S, uint8_t *ring, int tiles, uint32_t tmem) {
     const int warp = __shfl_sync(kFull, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int quad = warp & 3, part = (warp - kEpiWarp0) >> 2;
     const int row = quad * 32 + lane;
@@ -482,25 +483,31 @@ __device__ void finish(const TcArgs &a, Shared &S, int tiles, uint32_t tmem) {
                         if (row < t.n && r0 + 16 * j < a.rows)
                             store16(out + r0 + 16 * j, acc[u] + 16 * j);
                 } else {
-                    // rows of any alignment: 8 columns at a time through shared memory, so that a
-                    // warp writes runs of a row
-                    float (&P)[32][kPatch + 1] = S.patch[warp - kEpiWarp0];
+                    // rows of any alignment, through shared memory, so that a warp writes runs of a
+                    // row: after this CTA's last tile 32 columns at a time in the operand ring,
+                    // which no copy or MMA uses any more, before that 8 in a patch of its own
+                    // (777 x 1001 x 1296, one tile per CTA, on the device: 12.9 us, with the patch 14.8).
+                    // Every MMA is over by then: the wait for the last block's sums was for all of them
+                    const bool last = i + (int)gridDim.x >= tiles;
+                    const int run = last ? 32 : kPatch, pitch = run + 1;
+                    float *P = last ? reinterpret_cast<float *>(ring) + (warp - kEpiWarp0) * 32 * 33
+                                    : &S.patch[warp - kEpiWarp0][0][0];
+                    const int first = lane / run, step = 32 / run, col = lane % run;
 #pragma unroll
                     for (int j = 0; j < 32 / kPatch; j++) {
 #pragma unroll
-                        for (int x = 0; x < kPatch; x++) P[lane][x] = acc[u][kPatch * j + x];
+                        for (int x = 0; x < kPatch; x++)
+                            P[lane * pitch + x + (last ? kPatch * j : 0)] = acc[u][kPatch * j + x];
+                        if (last && j + 1 < 32 / kPatch) continue;
                         __syncwarp();
-                        const int col = r0 + kPatch * j + lane % kPatch;
-                        const int first = lane / kPatch;
+                        const int c = r0 + (last ? 0 : kPatch * j) + col;
                         T *o = static_cast<T *>(a.out) +
-                               ((int64_t)t.slot + quad * 32 + first) * a.ldo + col;
-                        if (col < a.rows) {
-#pragma unroll
-                            for (int y = 0; y < 32; y += 32 / kPatch) {
-                                if (quad * 32 + first + y < t.n)
-                                    *o = from_f32<T>(P[first + y][lane % kPatch]);
-                                o += (32 / kPatch) * a.ldo;
-                            }
+                               ((int64_t)t.slot + quad * 32 + first) * a.ldo + c;
+                        if (c < a.rows) {
+                            const int most = min(32, t.n - quad * 32);
+#pragma unroll 4
+                            for (int y = first; y < most; y += step, o += step * a.ldo)
+                                *o = from_f32<T>(P[y * pitch + col]);
                         }
                         __syncwarp();
                     }
@@ -555,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             scales<kMode>(a, S, tiles);
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
-        finish<kMode, T>(a, S, tiles, tmem);
+        finish<kMode, T>(a, S, ring, tiles, tmem);
     }
     __syncwarp();
     tc_fence_before();
