@@ -9,7 +9,8 @@
 // memory and add P_b * (as * bs) to running totals in registers.
 //
 // Tile: 128 tokens (the MMA's M side) by 256 weight rows (N): rows of one matrix, or 128 gate rows
-// and the 128 up rows of the same ffn values.  Tokens sit on the M side so that a tensor-memory
+// and the 128 up rows of the same ffn values; 128 rows where a dense product has few tiles.
+// Tokens sit on the M side so that a tensor-memory
 // lane is a token: an epilogue thread's scale is then one number per block and operand.  With the
 // weights on the M side the scale changes from column to column and has to be read from shared
 // memory, two 16-byte loads per four elements; the loads, not the additions, then bound the
@@ -69,7 +70,10 @@ static_assert(kAccs == 2, "the epilogue flips between two accumulators");
 static_assert(sizeof(Job) == sizeof(int4), "a slice is loaded as one vector");
 static_assert(128 * kRoleRegs + 512 * kEpiRegs <= kThreads * kLaunchRegs, "register split");
 
-enum Mode { kGateUp, kDown, kDense };
+enum Mode { kGateUp, kDown, kDense, kNarrow };
+constexpr bool dense(int mode) { return mode == kDense || mode == kNarrow; }
+constexpr int operands(int mode) { return mode == kNarrow ? 1 : 2; }   // of 128 weight rows, a tile
+constexpr int width(int mode) { return 128 * operands(mode); }
 
 struct TcArgs {
     int nkb;                     // blocks of k
@@ -104,13 +108,13 @@ __device__ __forceinline__ Tile tile_at(const TcArgs &a, int i) {
     Tile t;
     int s = i / a.row_tiles;
     t.rt = i - s * a.row_tiles;
-    if (kMode == kDense) {
+    if (dense(kMode)) {
         // bands of kBand row tiles, so that the tiles in flight cover a compact part of both sides
         const int ns = (a.M + kMT - 1) / kMT;
         const int band = i / (kBand * ns), in = i - band * (kBand * ns);
-        const int width = min(kBand, a.row_tiles - band * kBand);
-        s = in / width;
-        t.rt = band * kBand + in - s * width;
+        const int wide = min(kBand, a.row_tiles - band * kBand);
+        s = in / wide;
+        t.rt = band * kBand + in - s * wide;
         t.e = 0;
         t.slot = s * kMT;
         t.n = min(kMT, a.M - t.slot);
@@ -210,11 +214,11 @@ __device__ void produce(const TcArgs &a, Shared &S, uint8_t *ring, int tiles, co
             uint8_t *st = ring + (size_t)p.s * kStage;
             uint64_t *bar = &S.full[p.s];
             if (lane == 0) {
-                mbar_arrive_expect_tx(bar, kWeights + (uint32_t)npad * kSBlk);
-                const int r0 = kMode == kGateUp ? t.rt * 128 : t.rt * kNW;
+                mbar_arrive_expect_tx(bar, operands(kMode) * kOperand + (uint32_t)npad * kSBlk);
+                const int r0 = kMode == kGateUp ? t.rt * 128 : t.rt * width(kMode);
                 const int r1 = kMode == kGateUp ? r0 : r0 + 128;
                 tma_load_3d(st, w0, b * kSBlk, r0, t.e, bar);
-                tma_load_3d(st + kOperand, w1, b * kSBlk, r1, t.e, bar);
+                if (operands(kMode) == 2) tma_load_3d(st + kOperand, w1, b * kSBlk, r1, t.e, bar);
                 if (whole) tma_load_2d(st + kWeights, x, b * kSBlk, t.slot, bar);
             }
             __syncwarp();
@@ -244,8 +248,9 @@ __device__ __forceinline__ int64_t blocks_of_cta(const TcArgs &a, int tiles) {
 
 // The MMA issuer.  The whole warp walks the loop and one elected lane issues, so that the
 // descriptors stay in uniform registers.
+template <int kMode>
 __device__ void multiply(const TcArgs &a, Shared &S, uint8_t *ring, int tiles, uint32_t tmem) {
-    constexpr uint32_t idesc = instr_desc(0, kMT, kNW);
+    constexpr uint32_t idesc = instr_desc(0, kMT, width(kMode));
     const int64_t total = blocks_of_cta(a, tiles);
     Pos p, q;
     for (int64_t i = 0; i < total; i++) {
@@ -291,8 +296,9 @@ __device__ void scales(const TcArgs &a, Shared &S, int tiles) {
             s0 += (int64_t)t.rt * a.nkb;
             s1 = a.ws1 + t.e * a.ws_expert + (int64_t)t.rt * a.nkb;
         } else {
-            s0 += (int64_t)(2 * t.rt) * a.nkb;
-            s1 = t.rt * kNW + kSBlk < a.rows ? s0 + a.nkb : s0;    // past the last rows: not stored
+            s0 += (int64_t)(operands(kMode) * t.rt) * a.nkb;
+            // past the last rows: not stored
+            s1 = operands(kMode) == 2 && t.rt * kNW + kSBlk < a.rows ? s0 + a.nkb : s0;
         }
         const float *mine_ws = lane == 0 ? s0 : s1;
         if (i + (int)gridDim.x < tiles) next = tile_at<kMode>(a, i + gridDim.x);
@@ -395,7 +401,7 @@ __device__ void finish(const TcArgs &a, Shared &S, uint8_t *ring, int tiles, uin
                 tc_fence_after();
                 const uint32_t d = base + q * kNW;
 #pragma unroll
-                for (int o = 0; o < 2; o++) {
+                for (int o = 0; o < operands(kMode); o++) {
 #pragma unroll
                     for (int j = 0; j < 32; j += 16) {
                         uint32_t r[16];
@@ -461,8 +467,8 @@ __device__ void finish(const TcArgs &a, Shared &S, uint8_t *ring, int tiles, uin
         } else {
             T *out = static_cast<T *>(a.out) + ((int64_t)t.slot + row) * a.ldo;
 #pragma unroll
-            for (int u = 0; u < 2; u++) {
-                const int r0 = t.rt * kNW + u * 128 + part * 32;
+            for (int u = 0; u < operands(kMode); u++) {
+                const int r0 = t.rt * width(kMode) + u * 128 + part * 32;
                 if (kHalfY) {
                     // y as fp16 times a power of two per token and 128 rows: a block's sum is at
                     // most 128 * 448^2 times its scale, so the power follows from the largest
@@ -486,7 +492,7 @@ __device__ void finish(const TcArgs &a, Shared &S, uint8_t *ring, int tiles, uin
                     // rows of any alignment, through shared memory, so that a warp writes runs of a
                     // row: after this CTA's last tile 32 columns at a time in the operand ring,
                     // which no copy or MMA uses any more, before that 8 in a patch of its own
-                    // (777 x 1001 x 1296, one tile per CTA, on the device: 12.9 us, with the patch 14.8).
+                    // (777 x 1001 x 1296, one wide tile per CTA, on the device: 12.9 us, with the patch 14.8).
                     // Every MMA is over by then: the wait for the last block's sums was for all of them
                     const bool last = i + (int)gridDim.x >= tiles;
                     const int run = last ? 32 : kPatch, pitch = run + 1;
@@ -551,13 +557,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = S.tmem;
-    const int tiles = (kMode == kDense ? (a.M + kMT - 1) / kMT : *a.nslices) * a.row_tiles;
+    const int tiles = (dense(kMode) ? (a.M + kMT - 1) / kMT : *a.nslices) * a.row_tiles;
     if (warp < kEpiWarp0) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRoleRegs));
         if (warp == 0)
             produce<kMode>(a, S, ring, tiles, &w0, &w1, &x, &x16);
         else if (warp == 1)
-            multiply(a, S, ring, tiles, tmem);
+            multiply<kMode>(a, S, ring, tiles, tmem);
         else if (warp == 2)
             scales<kMode>(a, S, tiles);
     } else {
@@ -796,7 +802,6 @@ cudaError_t matmul_tc(const ScaledMatmulArgs &m, cudaStream_t st) {
     TcArgs a{};
     a.nkb = sblocks(m.K);
     a.rows = m.N;
-    a.row_tiles = (m.N + kNW - 1) / kNW;
     a.M = m.M;
     a.as = m.as;
     a.ldas = m.ldas;
@@ -805,11 +810,21 @@ cudaError_t matmul_tc(const ScaledMatmulArgs &m, cudaStream_t st) {
     a.ldo = m.ldo;
     a.vec = (uintptr_t)m.out % 32 == 0 && m.ldo * dtype_bytes(m.dt) % 32 == 0 && m.N % 16 == 0;
     a.status = m.status;
-    const int64_t tiles = (int64_t)((m.M + kMT - 1) / kMT) * a.row_tiles;
+    const int64_t ms = (m.M + kMT - 1) / kMT;
+    const int64_t sms = sm_count();
+    if (sms <= 0) return cudaErrorInvalidDevice;
+    // Tiles of 128 weight rows where all of them run at once: 777 x 1001 x 1296 9.5 us (wide 13.6),
+    // 1024 x 1280 x 2560 11.6 (13.8).  Past that wide ones: a narrow tile takes 70 percent of a
+    // wide one's time, so 2048 x 1280 x 2560 19.6 us (wide 14.3), 8192 x 4096 x 4096 180 (133).
+    const bool narrow = ms * ((m.N + 127) / 128) <= sms;
+    const int w = narrow ? width(kNarrow) : width(kDense);
+    a.row_tiles = (m.N + w - 1) / w;
+    const int64_t tiles = ms * a.row_tiles;
     if (tiles > INT32_MAX) return cudaErrorInvalidValue;
     return with_dtype(m.dt, [&](auto *tag) {
         using E = std::remove_pointer_t<decltype(tag)>;
-        return run_tc<kDense, E>(a, b, b, x, x16, tiles, st);
+        return narrow ? run_tc<kNarrow, E>(a, b, b, x, x16, tiles, st)
+                      : run_tc<kDense, E>(a, b, b, x, x16, tiles, st);
     });
 }
 
