@@ -74,7 +74,8 @@ moe_status moe_scaled_quantize(const void *d_x, int dtype, int T, int K, int64_t
     if (!aligned(d_x, dtype_bytes(dtype)) || !aligned(d_q, 16) || ldq % 16 ||
         !words({d_s, d_status}))
         return MOE_ERR_ALIGNMENT;
-    // a warp per four rows and block, counted in 32 bits
+    // a warp per four rows and block, counted in 32 bits, as rows and columns are
+    if (T > (1 << 30) || K > (1 << 30)) return MOE_ERR_UNSUPPORTED;
     if (((int64_t)T + 3) / 4 * sblocks(K) > INT32_MAX) return MOE_ERR_UNSUPPORTED;
     return launch_scaled_quantize(d_x, dtype, T, K, ldx, d_q, ldq, d_s, lds, d_status,
                                   static_cast<cudaStream_t>(stream)) == cudaSuccess

@@ -173,3 +173,13 @@ def test_plain_e4m3_agrees_with_torch():
     v = np.clip(np.concatenate([v, -v]), -448, 448).astype(np.float32)
     t = torch.from_numpy(v).to(torch.float8_e4m3fn)
     assert np.array_equal(t.float().numpy().astype(np.float64), ref.E4M3[ref.encode(v.astype(np.float64))])
+
+
+def test_quantize_refuses_sizes_whose_block_counts_pass_32_bits(moe):
+    L = moe.library()
+    big = (1 << 31) - 1
+    up = 1 << 31
+    assert L.moe_scaled_quantize(FAKE, 0, 1, big, big, FAKE, up, FAKE, 1, None, None) == \
+        moe.ERR_UNSUPPORTED
+    assert L.moe_scaled_quantize(FAKE, 0, big, 1, 1, FAKE, 16, FAKE, big, None, None) == \
+        moe.ERR_UNSUPPORTED
