@@ -52,7 +52,8 @@ moe_status moe_route_scored(const float *d_logits, int T, int E, int k,
         return MOE_ERR_INVALID_ARG;
     if (r.group_top < 1 || r.group_top > 2 || r.group_top > per || !std::isfinite(r.scale))
         return MOE_ERR_INVALID_ARG;
-    if (E > kMaxE || (int64_t)T * k > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+    // pairs and the chunks of tokens are counted in 32 bits
+    if (E > kMaxE || T > (1 << 30) || (int64_t)T * k > INT32_MAX) return MOE_ERR_UNSUPPORTED;
     if (!words({d_logits, r.d_bias, d_ids, d_w, d_counts, d_offsets, d_perm, d_inv_perm, d_status}) ||
         !aligned(d_ws, 256))
         return MOE_ERR_ALIGNMENT;

@@ -183,3 +183,12 @@ def test_quantize_refuses_sizes_whose_block_counts_pass_32_bits(moe):
         moe.ERR_UNSUPPORTED
     assert L.moe_scaled_quantize(FAKE, 0, big, 1, 1, FAKE, 16, FAKE, big, None, None) == \
         moe.ERR_UNSUPPORTED
+
+
+def test_route_scored_refuses_tokens_whose_chunk_count_passes_32_bits(moe):
+    L = moe.library()
+    rule = moe.RouteRule()
+    call = lambda T: L.moe_route_scored(FAKE, T, 1, 1, ctypes.addressof(rule), FAKE, FAKE,  # noqa: E731
+                                        FAKE, FAKE, FAKE, None, None, FAKE, 1 << 60, None)
+    assert call((1 << 31) - 1) == moe.ERR_UNSUPPORTED
+    assert call((1 << 30) + 1) == moe.ERR_UNSUPPORTED
