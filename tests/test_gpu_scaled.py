@@ -458,3 +458,141 @@ def test_route_then_experts_eager_captured_and_on_another_stream(torch, moe, T):
         torch.cuda.synchronize()
         assert torch.equal(out, eager[i])
     assert layer.status() == 0
+
+
+# ------------------------------------------------------------------ calls that share or grow
+
+
+@pytest.mark.parametrize("dtype", list(EPS))
+@pytest.mark.parametrize("M,N,K", [(2000, 1301, 144), (3001, 2003, 130), (2304, 2064, 272)])
+def test_matmul_of_more_tiles_than_run_at_once(torch, moe, dtype, M, N, K):
+    """Wide tiles: one per CTA, and several, with rows of any alignment and with aligned ones."""
+    ldo = N + (5 if N % 16 else 0)
+    rng = np.random.default_rng(M + N + K)
+    kp = -(-K // 16) * 16
+    a, b = np.full((M, kp), 0x7F, np.uint8), np.full((N, kp), 0xFF, np.uint8)
+    a[:, :K] = ref.encode(np.clip(rng.standard_normal((M, K)) * 130, -448, 448))
+    b[:, :K] = ref.encode(np.clip(rng.standard_normal((N, K)) * 130, -448, 448))
+    sa = (np.exp(rng.standard_normal((ref.blocks(K), M))) * 1e-2).astype(np.float32)
+    sb = (np.exp(rng.standard_normal((ref.blocks(N), ref.blocks(K)))) * 1e-3).astype(np.float32)
+    ad, bd, sad, sbd = (_dev(torch, v) for v in (a, b, sa, sb))
+    out = torch.full((M, ldo), -9.0, dtype=getattr(torch, dtype), device="cuda")
+    moe.scaled_matmul(ad.data_ptr(), kp, sad.data_ptr(), M, M, K, bd.data_ptr(), kp, sbd.data_ptr(),
+                      N, out.data_ptr(), moe.dtype_of(out), ldo, None, None, 0, _stream(torch))
+    got = out.double().cpu().numpy()
+    want, mag = ref.matmul(ref.wide_act(a[:, :K], sa), ref.wide_weight(b[:, :K], sb))
+    err = np.abs(got[:, :N] - want)
+    assert (err <= mag * ref.product_error(ref.blocks(K)) + np.abs(want) * EPS[dtype] +
+            2.0 ** -25).all(), (err / mag).max()
+    assert (got[:, N:] == -9.0).all()
+
+
+@pytest.mark.parametrize("M", [5, 200])
+def test_product_and_quantiser_past_32_bit_offsets(torch, moe, M):
+    """Rows so far apart that the last ones lie past 2^32 bytes; what lies between them is left."""
+    pitch, K, N = (1 << 32) // (M - 1) // 16 * 16 + 4096, 272, 48
+    assert (M - 1) * pitch > 1 << 32
+    rng = np.random.default_rng(M)
+    x = _dev(torch, rng.standard_normal((M, K)).astype(np.float32))
+    store = torch.full((M * pitch,), 0x55, dtype=torch.uint8, device="cuda")
+    q = store.view(M, pitch)
+    s = torch.empty((ref.blocks(K), M), device="cuda")
+    moe.scaled_quantize(x.data_ptr(), 0, M, K, K, q.data_ptr(), pitch, s.data_ptr(), M, None,
+                        _stream(torch))
+    rq, rs = ref.quantize(x.cpu().numpy())
+    assert np.array_equal(q[:, :K].cpu().numpy(), rq) and np.array_equal(s.cpu().numpy(), rs)
+    assert (q[:, K:K + 64] == 0x55).all()
+    b = ref.encode(rng.standard_normal((N, K)) * 100)
+    sb = np.full((ref.blocks(N), ref.blocks(K)), 1e-2, np.float32)
+    bd, sbd = _dev(torch, b), _dev(torch, sb)
+    near, out = torch.empty((M, N), device="cuda"), None
+    moe.scaled_matmul(q.data_ptr(), pitch, s.data_ptr(), M, M, K, bd.data_ptr(), K, sbd.data_ptr(),
+                      N, near.data_ptr(), 0, N, None, None, 0, _stream(torch))
+    want, mag = ref.matmul(ref.wide_act(rq, rs), ref.wide_weight(b, sb))
+    assert (np.abs(near.cpu().numpy() - want) <= mag * ref.product_error(ref.blocks(K)) +
+            np.abs(want) * EPS["float32"] + 2.0 ** -25).all()
+    # the same activations close together, the output's rows far apart
+    qd, ldo = _dev(torch, rq), pitch // 4
+    store.fill_(0x55)
+    out = store.view(torch.float32).view(M, ldo)
+    moe.scaled_matmul(qd.data_ptr(), K, s.data_ptr(), M, M, K, bd.data_ptr(), K, sbd.data_ptr(), N,
+                      out.data_ptr(), 0, ldo, None, None, 0, _stream(torch))
+    assert torch.equal(out[:, :N], near)
+    assert (out[:, N:N + 64].contiguous().view(torch.uint8) == 0x55).all()
+
+
+def _layer_inputs(torch, moe, T, seed):
+    E, k, H, F = 24, 4, 384, 144
+    rng = np.random.default_rng(seed)
+    _, layer = make_layer(torch, moe, rng, E, H, F, k, True, T)
+    x = _dev(torch, rng.standard_normal((T, H))).to(torch.bfloat16)
+    l = _dev(torch, (2 * rng.standard_normal((T, E))).astype(np.float32))
+    return layer, x, l
+
+
+@pytest.mark.parametrize("T", [1, 5, 50])
+def test_two_layers_at_once_on_two_streams(torch, moe, T):
+    """Layers share nothing: each with its own workspace, their calls overlap."""
+    a, b = _layer_inputs(torch, moe, T, 1), _layer_inputs(torch, moe, T, 2)
+    want = [l(x, lg) for l, x, lg in (a, b)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(20):
+        for i, (l, x, lg) in enumerate((a, b)):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(l(x, lg))
+    torch.cuda.synchronize()
+    for i in (0, 1):
+        assert all(torch.equal(o, want[i]) for o in got[i])
+    assert a[0].status() == 0 and b[0].status() == 0
+
+
+def test_graphs_that_share_a_workspace(torch, moe):
+    """Graphs of one layer at 1, 5 and 50 tokens use one workspace; replayed in any order on one
+    stream, with eager calls between, each gives its own result.  The output may be x itself."""
+    layer, x, l = _layer_inputs(torch, moe, 50, 3)
+    sizes = (1, 5, 50)
+    want = {T: layer(x[:T], l[:T]).clone() for T in sizes}
+    graphs, buf = {}, {T: x[:T].clone() for T in sizes}
+    torch.cuda.synchronize()
+    for T in sizes:
+        graphs[T] = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graphs[T]):
+            layer(buf[T], l[:T], out=buf[T])
+    for T in (50, 1, 5, 1, 50, 50, 5):
+        buf[T].copy_(x[:T])
+        graphs[T].replay()
+        assert torch.equal(layer(x[:7], l[:7]), layer(x[:7], l[:7]))
+        assert torch.equal(buf[T], want[T])
+    assert layer.status() == 0
+
+
+FIRST_CALL = """
+import sys, torch
+sys.path[:0] = {path!r}
+from expert_ffn_token_b200 import moe
+import test_gpu_scaled as t
+for T in (1, 5, 50):
+    layer, x, l = t._layer_inputs(torch, moe, T, T)
+    out = torch.empty_like(x)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        layer(x, l, out=out)
+    g.replay()
+    assert torch.equal(out, layer(x, l)) and layer.status() == 0
+print("same")
+"""
+
+
+def test_first_call_of_a_process_may_be_captured(torch, moe):
+    """Nothing is loaded, allocated or waited for on a first call that a capture forbids."""
+    import os
+    import subprocess
+    import sys
+
+    here = os.path.dirname(os.path.abspath(__file__))
+    code = FIRST_CALL.format(path=[os.path.dirname(here), here])
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip() == "same", r.stderr[-2000:]
