@@ -253,7 +253,8 @@ __device__ void route_row(const float *__restrict__ src, int E, int k, const moe
         }
         float gap;
         keep = keep_groups(value, rule.n_group, rule.topk_group, &gap);
-        if (need && rule.topk_group < rule.n_group && gap <= 4.0f * err) {
+        // (sums past fp32 are infinite, and the gap of two such is a NaN)
+        if (need && rule.topk_group < rule.n_group && !(gap > 4.0f * err)) {
             const double exact = group_value<double>(
                 mine ? per : 0, lane % width, width, width, rule.group_top, [&](int i) {
                     const int e = base + i;
@@ -496,8 +497,9 @@ __global__ void __launch_bounds__(256)
 }
 
 // More experts than registers hold: one warp per token, its row of 64-bit values in shared memory.
-__global__ void __launch_bounds__(kWarps * 32) k_scored_wide(    const float *__restrict__ logits, int T, int E, int k, const moe_route_rule rule,
-    int32_t *ids, float *w, uint32_t *status) {
+__global__ void __launch_bounds__(kWarps * 32)
+    k_scored_wide(const float *__restrict__ logits, int T, int E, int k, const moe_route_rule rule,
+                  int32_t *ids, float *w, uint32_t *status) {
     extern __shared__ double s_wide[];
     const int wid = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int t = blockIdx.x * kWarps + wid;

@@ -128,6 +128,17 @@ def test_route_scored_ties_and_masks(torch, moe, name):
     check_route(torch, moe, l, k, rule)
 
 
+@pytest.mark.parametrize("E", [64, 120, 2048])
+@pytest.mark.parametrize("sign", [-1, 1])
+def test_route_scored_group_sums_past_fp32(torch, moe, E, sign):
+    """Biases near the type's limits: sums of two that pass fp32 are ranked as 64-bit ones."""
+    rng = np.random.default_rng(E)
+    bias = (sign * rng.uniform(1.8e38, 3.4e38, E)).astype(np.float32)
+    l = (2 * rng.standard_normal((20, E))).astype(np.float32)
+    check_route(torch, moe, l, 4, dict(score="sigmoid", renorm=True, n_group=8, topk_group=3,
+                                       group_top=2, bias=bias))
+
+
 @pytest.mark.parametrize("name", ["softmax", "sigmoid bias", "groups top2 bias"])
 def test_route_scored_near_ties(torch, moe, name):
     """Neighbouring fp32 logits and biases: scores that differ in their last fp32 bits only are
