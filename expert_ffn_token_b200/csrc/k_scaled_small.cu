@@ -16,7 +16,7 @@
 // routed expert over k, every warp quantising the blocks of x that it needs; k_one_down gives 16
 // output rows of all the token's experts to one CTA, which combines them, and starts its weight
 // loads before the first kernel has ended.
-// 2 to 8 tokens (three kernels): k_few_prep lists the distinct experts with the tokens routed to
+// 2 to 4 tokens (three kernels): k_few_prep lists the distinct experts with the tokens routed to
 // them and quantises x once; k_few_gateup takes 128 ffn values of one expert per CTA, 16 rows and
 // all of k per warp, so that h can be quantised in place; k_few_down takes 16 output rows over all
 // experts.  An expert's rows are read once for all its tokens, which are the MMA's columns.
@@ -326,7 +326,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_one_down(const ScaledExpertsArg
     }
 }
 
-// ------------------------------------------------------------------ the experts, 2 to 8 tokens
+// ------------------------------------------------------------------ the experts, 2 to 4 tokens
 
 // What k_few_prep leaves in the workspace.
 struct FewWs {

@@ -820,7 +820,7 @@ cudaError_t matmul_tc(const ScaledMatmulArgs &m, cudaStream_t st) {
     const int w = narrow ? width(kNarrow) : width(kDense);
     a.row_tiles = (m.N + w - 1) / w;
     const int64_t tiles = ms * a.row_tiles;
-    if (tiles > INT32_MAX) return cudaErrorInvalidValue;
+    if (tiles > (1 << 30)) return cudaErrorInvalidValue;      // a tile index plus the grid fits
     return with_dtype(m.dt, [&](auto *tag) {
         using E = std::remove_pointer_t<decltype(tag)>;
         return narrow ? run_tc<kNarrow, E>(a, b, b, x, x16, tiles, st)

@@ -12,9 +12,9 @@ constexpr int kSBlk = 128;                 // columns (and weight rows) per scal
 constexpr float kE4M3Max = 448.0f;
 constexpr int kSmallT = 8;                 // most tokens of the small-batch kernels (MMA columns)
 // Most tokens of the experts' small-batch kernels.  10 of 512 experts and the shared one, hidden
-// 2560, ffn 640, small / tensor cores: 3 tokens 46 / 58 us (26 experts), 5 tokens 79 / 81 us (50),
-// 8 tokens 117 / 102 us (76).
-constexpr int kSmallExpertsT = 6;
+// 2560, ffn 640, all experts equally likely, small / tensor cores: 2 tokens 40 / 50 us, 3 tokens
+// 59 / 66 us, 5 tokens 79 / 73 us, 8 tokens 117 / 93 us.
+constexpr int kSmallExpertsT = 4;
 
 __host__ __device__ inline int sblocks(int n) { return (n + kSBlk - 1) / kSBlk; }
 inline size_t dtype_bytes(int dt) { return dt == MOE_DT_F32 ? 4 : 2; }

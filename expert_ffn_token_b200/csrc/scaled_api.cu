@@ -129,8 +129,8 @@ moe_status moe_scaled_experts_workspace_size(const moe_scaled_weights *host_weig
 
 moe_status moe_scaled_experts(const moe_scaled_weights *host_weights, const void *d_x,
                               int x_dtype, int T, int k, const int32_t *d_ids, const float *d_w,
-                              const int32_t *d_offsets, const int32_t *d_inv_perm, const float *d_gate, void *d_out,
-                              int out_dtype, uint32_t *d_status, void *d_ws, size_t ws_bytes,
+                              const int32_t *d_offsets, const int32_t *d_inv_perm,
+                              const float *d_gate, void *d_out, int out_dtype, uint32_t *d_status, void *d_ws, size_t ws_bytes,
                               void *stream) {
     const moe_status st = check_weights(host_weights);
     if (st != MOE_OK) return st;

@@ -458,6 +458,9 @@ class ScaledExperts:
     """The experts of one layer in e4m3 with 128 x 128 block scales, held in torch tensors, and
     the workspace for up to max_tokens tokens (marshalling only).
 
+    Its calls share one workspace: they follow one another on a stream (graphs of them too); what
+    runs at the same time on another stream is an object of its own.  No gradients.
+
     gate, up [n][ffn][hidden] and down [n][hidden][ffn] (uint8 or float8_e4m3fn), scales fp32
     [n][ceil(rows / 128)][ceil(cols / 128)], n = experts (+ 1 with `shared`)."""
 

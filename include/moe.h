@@ -359,7 +359,7 @@ typedef struct {
 
 /* moe_route_topk with a rule: the same outputs (d_ids, d_w, d_counts, d_offsets, d_perm,
  * d_inv_perm, all as there), workspace (moe_route_workspace_size for T, E, k) and limits
- * (1 <= k <= min(E, 32), E <= 4096); k <= topk_group * E / n_group.  A token with a logit or a
+ * (1 <= k <= min(E, 32), E <= 4096), and T <= 2^30; k <= topk_group * E / n_group.  A token with a logit or a
  * v_e that is not finite gets ids 0..k-1, weights 1/k and MOE_ERR_NONFINITE in d_status (may be
  * NULL).  An expert is masked by a large negative finite logit or bias.                      */
 moe_status moe_route_scored(const float *d_logits, int T, int E, int k,
@@ -369,7 +369,8 @@ moe_status moe_route_scored(const float *d_logits, int T, int E, int k,
                             size_t ws_bytes, void *stream);
 
 /* d_x [T][K] (dtype: moe_dtype, rows ldx elements apart, any alignment of its type) -> a scaled
- * matrix: d_q rows ldq bytes apart (16-byte aligned, ldq a multiple of 16), d_s with lds >= T.
+ * matrix: d_q rows ldq bytes apart (16-byte aligned, ldq a multiple of 16), d_s with lds >= T.  T and K are
+ * at most 2^30.
  * Per row and 128 columns: s = amax / 448 in fp32 and q = the e4m3 value nearest x / s (ties to
  * even; the quotient is not rounded in between); a block whose s is 0 is stored as zeros, a block with a
  * non-finite value as zeros with MOE_ERR_NONFINITE in d_status (may be NULL).  Bytes of d_q past
@@ -382,8 +383,8 @@ moe_status moe_scaled_quantize(const void *d_x, int dtype, int T, int K, int64_t
  * bytes apart, scales d_as with stride ldas >= M) times the transposed scaled weights d_b [N][K]
  * (rows ldb bytes apart, scales d_bs contiguous): every block of 128 k is summed in fp32, scaled
  * in fp32 and added up in fp32, in an order that depends on the sizes alone; one rounding to
- * dtype at the end.  d_a and d_b 16-byte aligned, lda and ldb multiples of 16 (bytes past column
- * K are not used).  d_out aligned to its type.  d_status (may be NULL) receives device-side
+ * dtype at the end.  d_a and d_b 16-byte aligned, lda and ldb multiples of 16 (the bytes from
+ * column K to the next multiple of 16 may be read, in the last row too, but not used).  d_out aligned to its type.  d_status (may be NULL) receives device-side
  * errors.  The workspace (moe_scaled_matmul_workspace_size; may be 0 bytes, then d_ws may be
  * NULL) is 256-byte aligned scratch.  M may be 0.                                            */
 moe_status moe_scaled_matmul_workspace_size(int M, int N, int K, size_t *bytes);
@@ -413,7 +414,9 @@ typedef struct {
  * reported as MOE_ERR_BOUNDS in d_status (may be NULL), a non-finite block of x or h is taken as
  * zeros and reported as MOE_ERR_NONFINITE.  1 <= T <= the max_tokens the workspace was sized for
  * (moe_scaled_experts_workspace_size; 256-byte aligned scratch).  Results do not change from
- * call to call.                                                                              */
+ * call to call.  d_out may be d_x when the types are the same.  Calls that may run at the same
+ * time need workspaces of their own; calls and graphs that follow one another on a stream may
+ * share one.                                                                                 */
 moe_status moe_scaled_experts_workspace_size(const moe_scaled_weights *host_weights,
                                              int max_tokens, int k, size_t *bytes);
 moe_status moe_scaled_experts(const moe_scaled_weights *host_weights, const void *d_x,

@@ -81,7 +81,7 @@ def experts(x, ids, w, gate, W):
     gate [T] or None, W: dict of (codes, scales) of gate, up, down, with `shared`.
 
     Returns (out, tol, half): tol bounds what fp32 arithmetic may change, half what holding every
-    y in fp16 times a power of two per 128 columns adds (batches of more than 6 tokens with a
+    y in fp16 times a power of two per 128 columns adds (batches of more than 4 tokens with a
     16-bit output): 2^-11 of |y|, and half of fp16's smallest step times the power, which is
     less than four times what the largest possible sum asks for.  In tol, g and u carry
     product_error; h = silu(g) u inherits them (|silu'| <= 1.1) with a few fp32 roundings; a
