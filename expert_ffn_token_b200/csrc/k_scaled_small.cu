@@ -20,6 +20,10 @@
 // them and quantises x once; k_few_gateup takes 128 ffn values of one expert per CTA, 16 rows and
 // all of k per warp, so that h can be quantised in place; k_few_down takes 16 output rows over all
 // experts.  An expert's rows are read once for all its tokens, which are the MMA's columns.
+//
+// On the device: one row times 1280 x 2560 2.8 us (3.3 MB: a launch and one trip to memory); one
+// token of 8 experts, hidden 2048, ffn 512, 8.7 us (25 MB, 2.9 TB/s); 3 tokens of 10 of 512 experts
+// and the shared one, hidden 2560, ffn 640, 48 us (124 MB): list 4.8, gate/up 23.3, down 18.3 us.
 #include <algorithm>
 
 #include "ptx.cuh"

@@ -16,6 +16,10 @@
 // Grouping (the order of a3): counts per chunk of 64 tokens come out of the routing kernel's shared
 // memory, a second kernel turns them into places per chunk, a third writes the permutation.  Up to
 // one chunk is routed and grouped by one CTA in one launch.
+//
+// Bound by instructions (about 2300 a token at 512 experts in 8 groups), not by the logits' bytes:
+// 8192 such tokens take 43.5 us on the device, 37.5 us of it k_scored_rows alone (16.8 MB); one
+// token of 256 experts 5.0 us.
 #include <math.h>
 
 #include "ptx.cuh"
