@@ -22,8 +22,8 @@
 // epilogue's last steps: 8192^3 547 us against 560, 4096 x 1280 x 2560 37 against 35, 8192 routed
 // tokens 1270 against 1006).  They are not used.
 //
-// Now, on the device: 8192^3 500 us (2.2 PFLOP/s; 907 clocks a block of k, 512 of them its MMAs; the
-// issue of the sums' promotion fills the rest), 4096 x 1280 x 2560 to fp32 28.6 us (160 tiles: two
+// Now, on the device: 8192^3 500 us (2.2 PFLOP/s; 907 clocks a block of k, 512 of them its MMAs,
+// with the issue slots 65 percent full, mostly of the sums' promotion), 4096 x 1280 x 2560 to fp32 28.6 us (160 tiles: two
 // rounds).  The experts' layer of 10 of 512 experts and the shared one, hidden 2560, ffn 640: 64
 // tokens 306 us (5.9 TB/s of weights), 8192 tokens 932 us.
 //
