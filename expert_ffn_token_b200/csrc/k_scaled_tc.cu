@@ -68,7 +68,7 @@ constexpr int kScales = 4;                     // depth of the scale ring, in gr
 constexpr int kPatch = 8;                      // columns per turn through shared memory (stores)
 constexpr uint32_t kTmemCols = 512;
 static_assert(kEpiWarps * 32 * 33 * 4 <= kStages * kStage, "the ring holds every warp's 32 columns");
-constexpr uint64_t kWaitNs = 2000000000ull;    // limit of every wait
+constexpr uint64_t kDrainNs = 2000000000ull;   // limit of the waits for own copies and products
 // Registers: 640 threads launch with 96 each (61440); the first warpgroup keeps 64 and the four
 // epilogue warpgroups take 104: 128 * 64 + 512 * 104 = 61440.
 constexpr int kLaunchRegs = 96, kRoleRegs = 64, kEpiRegs = 104;
@@ -101,6 +101,7 @@ struct TcArgs {
     int64_t ldo;
     bool vec;                    // out rows are 32-byte aligned and rows a multiple of 16
     uint32_t *status;
+    uint64_t wait_ns;            // limit of every hand-over's wait (moe_scaled_set_wait_limit)
 };
 
 struct Tile {
@@ -167,7 +168,7 @@ struct Pos {                          // ring position
 // Bounded wait of a whole warp, with one answer: false once this CTA gives up.  The clock and the
 // abort flag are looked at once in 64 tries: reading the global timer between tries would delay
 // the wake-up.  The vote keeps the loop uniform.
-__device__ __forceinline__ bool waitw(Shared &S, uint64_t *bar, uint32_t parity, uint32_t *st) {
+__device__ __forceinline__ bool waitw(const TcArgs &a, Shared &S, uint64_t *bar, uint32_t parity) {
     if (__all_sync(kFull, mbar_try_wait(bar, parity))) return true;
     uint64_t t0 = 0;
 #pragma unroll 1
@@ -175,10 +176,10 @@ __device__ __forceinline__ bool waitw(Shared &S, uint64_t *bar, uint32_t parity,
         if (i & 63u) continue;
         const uint64_t t = globaltimer();
         if (t0 == 0) t0 = t;
-        const bool late = t - t0 > kWaitNs;
+        const bool late = t - t0 > a.wait_ns;
         if (late) {
             *(volatile int *)&S.abort = 1;
-            set_status(st, MOE_ERR_TIMEOUT);
+            set_status(a.status, MOE_ERR_TIMEOUT);
         }
         if (__any_sync(kFull, late || *(volatile int *)&S.abort)) return false;
     }
@@ -213,7 +214,7 @@ __device__ void produce(const TcArgs &a, Shared &S, uint8_t *ring, int tiles, co
         // the next tile's place arrives while this one's blocks are issued
         if (i + (int)gridDim.x < tiles) next = tile_at<kMode>(a, i + gridDim.x);
         for (int b = 0; b < a.nkb; b++) {
-            if (!waitw(S, &S.empty[p.s], p.ph ^ 1u, a.status)) {
+            if (!waitw(a, S, &S.empty[p.s], p.ph ^ 1u)) {
                 ok = false;
                 break;
             }
@@ -240,9 +241,9 @@ __device__ void produce(const TcArgs &a, Shared &S, uint8_t *ring, int tiles, co
     for (int j = max(0, issued - kStages); j < issued; j++) {
         const uint32_t ph = (uint32_t)(j / kStages) & 1u;
         if (ok)
-            waitw(S, &S.empty[j % kStages], ph, a.status);
+            waitw(a, S, &S.empty[j % kStages], ph);
         else
-            mbar_wait_bounded(&S.full[j % kStages], ph, kWaitNs);
+            mbar_wait_bounded(&S.full[j % kStages], ph, kDrainNs);
     }
 }
 
@@ -260,11 +261,11 @@ __device__ void multiply(const TcArgs &a, Shared &S, uint8_t *ring, int tiles, u
     const int64_t total = blocks_of_cta(a, tiles);
     Pos p, q;
     for (int64_t i = 0; i < total; i++) {
-        if (!waitw(S, &S.full[p.s], p.ph, a.status) ||
-            !waitw(S, &S.acc_empty[q.s], q.ph ^ 1u, a.status)) {
+        if (!waitw(a, S, &S.full[p.s], p.ph) ||
+            !waitw(a, S, &S.acc_empty[q.s], q.ph ^ 1u)) {
             if (elect_one()) {
                 umma_commit(&S.done);
-                mbar_wait_bounded(&S.done, 0, kWaitNs);
+                mbar_wait_bounded(&S.done, 0, kDrainNs);
             }
             return;
         }
@@ -310,7 +311,7 @@ __device__ void scales(const TcArgs &a, Shared &S, int tiles) {
         if (i + (int)gridDim.x < tiles) next = tile_at<kMode>(a, i + gridDim.x);
 #pragma unroll 1
         for (int b = 0; b < a.nkb; b++) {
-            if (u == 0 && !waitw(S, &S.sc_empty[p.s], p.ph ^ 1u, a.status)) {
+            if (u == 0 && !waitw(a, S, &S.sc_empty[p.s], p.ph ^ 1u)) {
                 cp_async_wait_all();
                 return;
             }
@@ -394,10 +395,10 @@ __device__ void finish(const TcArgs &a, Shared &S, uint8_t *ring, int tiles, uin
         float top[2] = {0.f, 0.f};           // the largest scale of each operand's blocks
 #pragma unroll 1
         for (int b = 0; b < a.nkb; b++) {
-            if (u == 0 && !waitw(S, &S.sc_full[p.s], p.ph, a.status)) return;
+            if (u == 0 && !waitw(a, S, &S.sc_full[p.s], p.ph)) return;
             const float v = S.as[p.s][u][row];
             const float2 w = S.ws[p.s][u];
-            if (!waitw(S, &S.acc_full[q], qph, a.status)) return;
+            if (!waitw(a, S, &S.acc_full[q], qph)) return;
             if (busy) {
                 const float f[2] = {v * w.x, v * w.y};
                 if (kHalfY) {
@@ -767,6 +768,7 @@ cudaError_t experts_tc(const ScaledExpertsArgs &e, uint8_t *ws, cudaStream_t st)
     a.slices = slices;
     a.nslices = nslices;
     a.status = e.status;
+    a.wait_ns = e.wait_ns;
     a.slots = L.slots;
     a.hq = ws + L.hq;
     a.hs = reinterpret_cast<float *>(ws + L.hs);
@@ -816,6 +818,7 @@ cudaError_t matmul_tc(const ScaledMatmulArgs &m, cudaStream_t st) {
     a.ldo = m.ldo;
     a.vec = (uintptr_t)m.out % 32 == 0 && m.ldo * dtype_bytes(m.dt) % 32 == 0 && m.N % 16 == 0;
     a.status = m.status;
+    a.wait_ns = m.wait_ns;
     const int64_t ms = (m.M + kMT - 1) / kMT;
     const int64_t sms = sm_count();
     if (sms <= 0) return cudaErrorInvalidDevice;

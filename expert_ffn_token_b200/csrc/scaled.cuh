@@ -197,6 +197,7 @@ struct ScaledMatmulArgs {
     int dt;
     int64_t ldo;
     uint32_t *status;
+    uint64_t wait_ns;              // limit of every wait inside the tensor-core kernels
 };
 // The product on the kernel that suits its sizes, and the workspace it needs.
 size_t scaled_matmul_ws_bytes(int M, int N, int K);
@@ -219,6 +220,7 @@ struct ScaledExpertsArgs {
     void *out;
     int out_dt;
     uint32_t *status;
+    uint64_t wait_ns;              // as of ScaledMatmulArgs
     float *h;                      // one token: h of every slot [slots][ffn]
 };
 // x quantised into the slots of its tokens: q [slots][hidden], scales [blocks][slots]; and the

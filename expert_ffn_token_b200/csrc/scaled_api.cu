@@ -1,6 +1,7 @@
 // scaled_api.cu -- the entry points of scored routing and of the float8 block-scaled operators
 // (declared in include/moe.h): argument checks, workspace layouts and the choice of kernels.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <initializer_list>
 
@@ -27,6 +28,9 @@ moe_status check_weights(const moe_scaled_weights *w) {
         return MOE_ERR_UNSUPPORTED;
     return MOE_OK;
 }
+
+// moe_scaled_set_wait_limit: these operators have no handle to keep it in.
+std::atomic<uint64_t> g_wait_ns{2000000000ull};
 
 }  // namespace
 
@@ -108,7 +112,7 @@ moe_status moe_scaled_matmul(const uint8_t *d_a, int64_t lda, const float *d_as,
     if (need && (!d_ws || ws_bytes < need)) return MOE_ERR_WORKSPACE;
     if (M == 0) return MOE_OK;
     const ScaledMatmulArgs a{d_a, lda, d_as, ldas, M, K, d_b, ldb, d_bs, N, d_out, dtype, ldo,
-                             d_status};
+                             d_status, g_wait_ns.load(std::memory_order_relaxed)};
     return launch_scaled_matmul(a, d_ws, static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? MOE_OK
                : MOE_ERR_CUDA;
@@ -163,9 +167,16 @@ moe_status moe_scaled_experts(const moe_scaled_weights *host_weights, const void
     a.out = d_out;
     a.out_dt = out_dtype;
     a.status = d_status;
+    a.wait_ns = g_wait_ns.load(std::memory_order_relaxed);
     return launch_scaled_experts(a, d_ws, static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? MOE_OK
                : MOE_ERR_CUDA;
+}
+
+moe_status moe_scaled_set_wait_limit(uint64_t ns) {
+    if (ns == 0) return MOE_ERR_INVALID_ARG;
+    g_wait_ns.store(ns, std::memory_order_relaxed);
+    return MOE_OK;
 }
 
 }  // extern "C"

@@ -43,7 +43,8 @@ EXPORTED = ["moe_arena_create", "moe_arena_destroy", "moe_workspace_size", "moe_
             "moe_forward_routed", "moe_chain_workspace_size", "moe_chain_forward",
             "moe_chain_status", "moe_route_scored", "moe_scaled_quantize",
             "moe_scaled_matmul_workspace_size", "moe_scaled_matmul",
-            "moe_scaled_experts_workspace_size", "moe_scaled_experts"]
+            "moe_scaled_experts_workspace_size", "moe_scaled_experts",
+            "moe_scaled_set_wait_limit"]
 
 
 class ExpertDesc(ctypes.Structure):
@@ -131,6 +132,7 @@ _lib.moe_scaled_matmul.argtypes = [_P, _L, _P, _L, _I, _I, _P, _L, _P, _I, _P, _
 _lib.moe_scaled_experts_workspace_size.argtypes = [_P, _I, _I, ctypes.POINTER(_S)]
 _lib.moe_scaled_experts.argtypes = [_P, _P, _I, _I, _I, _P, _P, _P, _P, _P, _P, _I, _P, _P, _S,
                                     _P]
+_lib.moe_scaled_set_wait_limit.argtypes = [ctypes.c_uint64]
 _lib.moe_kernels_enqueued.argtypes = []
 _lib.moe_kernels_enqueued.restype = ctypes.c_uint64
 
@@ -366,6 +368,12 @@ def scaled_experts(weights: ScaledWeights, d_x: int, x_dtype: int, T: int, k: in
     _check(_lib.moe_scaled_experts(ctypes.addressof(weights), d_x, x_dtype, T, k, d_ids, d_w,
                                    d_offsets, d_inv_perm, d_gate, d_out, out_dtype, d_status,
                                    d_ws, ws_bytes, stream), "moe_scaled_experts")
+
+
+def scaled_set_wait_limit(ns: int) -> None:
+    """moe_scaled_set_wait_limit: limit of every bounded device wait of later scaled_matmul and
+    scaled_experts calls of this process."""
+    _check(_lib.moe_scaled_set_wait_limit(ns), "moe_scaled_set_wait_limit")
 
 
 # ------------------------------------------------------------------ torch convenience

@@ -426,6 +426,14 @@ moe_status moe_scaled_experts(const moe_scaled_weights *host_weights, const void
                               int out_dtype, uint32_t *d_status, void *d_ws, size_t ws_bytes,
                               void *stream);
 
+/* Limit, in nanoseconds, of every bounded wait inside the kernels of later moe_scaled_matmul and
+ * moe_scaled_experts calls of this process (default 2 s; a captured call keeps the limit it was
+ * captured with).  A wait that runs out ends its kernel with MOE_ERR_TIMEOUT in d_status after
+ * the copies and products it had in flight have ended, and leaves part of d_out unwritten:
+ * without a d_status that goes unseen.  The next call starts clean.  ns > 0;
+ * MOE_ERR_INVALID_ARG otherwise.                                                             */
+moe_status moe_scaled_set_wait_limit(uint64_t ns);
+
 /* Number of kernels this library has enqueued (or recorded into a CUDA graph under stream
  * capture) in this process since it was loaded.  Counting a captured forward gives the
  * kernels each replay of that graph launches. */

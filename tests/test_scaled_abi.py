@@ -192,3 +192,11 @@ def test_route_scored_refuses_tokens_whose_chunk_count_passes_32_bits(moe):
                                         FAKE, FAKE, FAKE, None, None, FAKE, 1 << 60, None)
     assert call((1 << 31) - 1) == moe.ERR_UNSUPPORTED
     assert call((1 << 30) + 1) == moe.ERR_UNSUPPORTED
+
+
+def test_wait_limit_is_settable_and_not_zero(moe):
+    with pytest.raises(moe.MoeError) as e:
+        moe.scaled_set_wait_limit(0)
+    assert e.value.code == moe.ERR_INVALID_ARG
+    moe.scaled_set_wait_limit(1)
+    moe.scaled_set_wait_limit(2_000_000_000)       # the default
