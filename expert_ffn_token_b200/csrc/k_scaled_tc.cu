@@ -204,7 +204,7 @@ __device__ void produce(const TcArgs &a, Shared &S, uint8_t *ring, int tiles, co
     int i = blockIdx.x;
     if (i >= tiles) return;
     Tile next = tile_at<kMode>(a, i);
-    bool ok = true;
+    bool ok = true;                   // until a wait runs out
     for (; ok && i < tiles; i += gridDim.x) {
         const Tile t = next;
         // more than half a tile of tokens comes as one box of 128 rows (those past the slice, if
@@ -236,15 +236,9 @@ __device__ void produce(const TcArgs &a, Shared &S, uint8_t *ring, int tiles, co
             p.next(kStages);
         }
     }
-    // leaving early, the copies in flight land before the CTA goes; else the stages' last uses
-    // are over
-    for (int j = max(0, issued - kStages); j < issued; j++) {
-        const uint32_t ph = (uint32_t)(j / kStages) & 1u;
-        if (ok)
-            waitw(a, S, &S.empty[j % kStages], ph);
-        else
-            mbar_wait_bounded(&S.full[j % kStages], ph, kDrainNs);
-    }
+    // whoever gives up: the copies in flight land before the CTA goes
+    for (int j = max(0, issued - kStages); j < issued; j++)
+        mbar_wait_bounded(&S.full[j % kStages], (uint32_t)(j / kStages) & 1u, kDrainNs);
 }
 
 // Blocks of the tiles that this CTA takes.
@@ -262,13 +256,8 @@ __device__ void multiply(const TcArgs &a, Shared &S, uint8_t *ring, int tiles, u
     Pos p, q;
     for (int64_t i = 0; i < total; i++) {
         if (!waitw(a, S, &S.full[p.s], p.ph) ||
-            !waitw(a, S, &S.acc_empty[q.s], q.ph ^ 1u)) {
-            if (elect_one()) {
-                umma_commit(&S.done);
-                mbar_wait_bounded(&S.done, 0, kDrainNs);
-            }
-            return;
-        }
+            !waitw(a, S, &S.acc_empty[q.s], q.ph ^ 1u))
+            break;
         tc_fence_after();
         const uint32_t st = smem_u32(ring) + (uint32_t)p.s * kStage;
         const uint64_t x = smem_desc(st + kWeights, 1024, 2), w = smem_desc(st, 1024, 2);
@@ -284,6 +273,12 @@ __device__ void multiply(const TcArgs &a, Shared &S, uint8_t *ring, int tiles, u
         p.next(kStages);
         q.next(kAccs);
     }
+    // whoever gives up: no MMA is in flight when the tensor memory goes
+    if (elect_one()) {
+        umma_commit(&S.done);
+        mbar_wait_bounded(&S.done, 0, kDrainNs);
+    }
+    __syncwarp();
 }
 
 // Warp 2: the scales of every block, in the order the epilogue takes them, copied into the ring.
@@ -329,6 +324,7 @@ __device__ void scales(const TcArgs &a, Shared &S, int tiles) {
         }
     }
     if (u) cp_async_arrive(&S.sc_full[p.s]);
+    cp_async_wait_all();                    // the epilogue may have given up on them
 }
 
 // acc += r * s for 16 columns.  (Packed two-element multiply-adds need the loaded registers in

@@ -607,3 +607,49 @@ def test_first_call_of_a_process_may_be_captured(torch, moe):
     code = FIRST_CALL.format(path=[os.path.dirname(here), here])
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and r.stdout.strip() == "same", r.stderr[-2000:]
+
+
+# ------------------------------------------------------------------ waits that run out
+
+
+@pytest.fixture
+def short_waits(moe):
+    """A limit far below what the kernels' hand-overs take, and the default again afterwards."""
+    moe.scaled_set_wait_limit(1)
+    yield
+    moe.scaled_set_wait_limit(2_000_000_000)
+
+
+def _product(torch, moe, M, N, K):
+    rng = np.random.default_rng(M + N)
+    a = ref.encode(np.clip(rng.standard_normal((M, K)) * 130, -448, 448))
+    b = ref.encode(np.clip(rng.standard_normal((N, K)) * 130, -448, 448))
+    t = [_dev(torch, v) for v in (a, np.full((ref.blocks(K), M), 1e-2, np.float32), b,
+                                  np.full((ref.blocks(N), ref.blocks(K)), 1e-3, np.float32))]
+    out = torch.zeros((M, N), device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def call():
+        moe.scaled_matmul(t[0].data_ptr(), K, t[1].data_ptr(), M, M, K, t[2].data_ptr(), K,
+                          t[3].data_ptr(), N, out.data_ptr(), 0, N, status.data_ptr(), None, 0,
+                          _stream(torch))
+        torch.cuda.synchronize()
+        return moe.read_status(status.data_ptr(), _stream(torch))
+
+    return call, out
+
+
+@pytest.mark.parametrize("M,N,K", [(300, 512, 4096), (2048, 2560, 4096)])
+def test_matmul_wait_times_out_and_next_call_is_clean(torch, moe, short_waits, M, N, K):
+    """The product's kernels (tiles of 128 and of 256 weight rows) report a wait that runs out, end,
+    and leave nothing behind: the next call's result is the bits of an undisturbed one."""
+    call, out = _product(torch, moe, M, N, K)
+    assert call() == moe.ERR_TIMEOUT
+    moe.scaled_set_wait_limit(2_000_000_000)
+    assert call() == 0
+    first = out.clone()
+    moe.scaled_set_wait_limit(1)
+    assert [call() for _ in range(5)] == [moe.ERR_TIMEOUT] * 5
+    moe.scaled_set_wait_limit(2_000_000_000)
+    out.zero_()
+    assert call() == 0 and torch.equal(out, first)
