@@ -34,7 +34,8 @@
 //   warps 4-19    epilogue: lane quarter (warp % 4), 32 columns of each 128-row operand.  Four warps
 //                 a scheduler, because a block is a chain of hand-overs and tensor-memory loads
 //                 that one warp cannot hide: with two, a block took 1250 clocks, 300 of them work
-// Every hand-off is an mbarrier and every wait is bounded (MOE_ERR_TIMEOUT in the status word).
+// Every hand-off is an mbarrier and every wait but the CTA's first and last __syncthreads, which
+// all threads reach, is bounded (MOE_ERR_TIMEOUT in the status word; moe_scaled_set_wait_limit).
 //
 // The experts' layer quantises x straight into slot order, once per routed expert, so that every
 // tile's token rows are neighbours.  Gathering them in this kernel cost more: a TMA gather of
@@ -142,7 +143,7 @@ __device__ __forceinline__ float silu_mul(float g, float u) {
 
 struct Shared {
     uint64_t full[kStages], empty[kStages], acc_full[kAccs], acc_empty[kAccs], sc_full[kScales],
-        sc_empty[kScales], done;
+        sc_empty[kScales], quarter[4], done;
     uint32_t tmem;
     int abort;
     float as[kScales][kGroup][kMT];       // per block: the tokens' scales
@@ -436,7 +437,10 @@ __device__ void finish(const TcArgs &a, Shared &S, uint8_t *ring, int tiles, uin
                 mx = max(mx, __float_as_uint(acc[0][j]) & 0x7fffffffu);
             }
             S.amax[par][part][row] = mx;
-            named_barrier(1 + quad, 128);
+            // the quarter's four warps meet at an mbarrier: a warp that gave up must not hold the others
+            __syncwarp();
+            arrive1(&S.quarter[quad], lane == 0);
+            if (!waitw(a, S, &S.quarter[quad], par)) return;
             mx = max(max(S.amax[par][0][row], S.amax[par][1][row]),
                      max(S.amax[par][2][row], S.amax[par][3][row]));
             par ^= 1u;
@@ -548,6 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&S.sc_full[i], 32);
             mbar_init(&S.sc_empty[i], kEpiWarps);
         }
+        for (int i = 0; i < 4; i++) mbar_init(&S.quarter[i], 4);
         mbar_init(&S.done, 1);
         S.abort = 0;
         fence_barrier_init();

@@ -653,3 +653,25 @@ def test_matmul_wait_times_out_and_next_call_is_clean(torch, moe, short_waits, M
     moe.scaled_set_wait_limit(2_000_000_000)
     out.zero_()
     assert call() == 0 and torch.equal(out, first)
+
+
+@pytest.mark.parametrize("T", [60, 700])
+def test_experts_wait_times_out_and_next_call_is_clean(torch, moe, short_waits, T):
+    """Likewise for the experts' gate/up and down, whose epilogue warps also wait for one another."""
+    E, k, H, F = 8, 3, 2048, 640
+    rng = np.random.default_rng(T)
+    _, layer = make_layer(torch, moe, rng, E, H, F, k, True, T)
+    x = _dev(torch, rng.standard_normal((T, H))).to(torch.bfloat16)
+    l = _dev(torch, (2 * rng.standard_normal((T, E))).astype(np.float32))
+    layer(x, l)
+    assert layer.status() == moe.ERR_TIMEOUT
+    moe.scaled_set_wait_limit(2_000_000_000)
+    first = layer(x, l)
+    assert layer.status() == 0
+    for _ in range(5):
+        moe.scaled_set_wait_limit(1)
+        layer(x, l)
+        assert layer.status() == moe.ERR_TIMEOUT
+        moe.scaled_set_wait_limit(2_000_000_000)
+        assert torch.equal(layer(x, l), first)
+        assert layer.status() == 0

@@ -200,3 +200,16 @@ def test_wait_limit_is_settable_and_not_zero(moe):
     assert e.value.code == moe.ERR_INVALID_ARG
     moe.scaled_set_wait_limit(1)
     moe.scaled_set_wait_limit(2_000_000_000)       # the default
+
+
+def test_tensor_core_products_wait_on_bounded_barriers_only():
+    """A warp that gives up leaves its loop, so no other may wait for it at a hardware barrier, which
+    has no limit.  The kernel's two __syncthreads are reached by every thread."""
+    import os
+    import re
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    with open(os.path.join(root, "expert_ffn_token_b200", "csrc", "k_scaled_tc.cu")) as f:
+        code = re.sub(r"//[^\n]*", "", f.read())
+    assert not re.search(r"named_barrier|bar\.sync|barrier\.sync|barrier\.cta", code)
+    body = code[code.index("k_scaled_tc(const TcArgs"):]
+    assert len(re.findall(r"__syncthreads\(\)", code)) == 2 == body.count("__syncthreads()")
