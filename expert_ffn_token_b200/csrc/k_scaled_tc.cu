@@ -103,6 +103,7 @@ struct TcArgs {
     bool vec;                    // out rows are 32-byte aligned and rows a multiple of 16
     uint32_t *status;
     uint64_t wait_ns;            // limit of every hand-over's wait (moe_scaled_set_wait_limit)
+    uint32_t look;               // the clock is looked at where a wait's tries have none of these bits
 };
 
 struct Tile {
@@ -168,13 +169,15 @@ struct Pos {                          // ring position
 
 // Bounded wait of a whole warp, with one answer: false once this CTA gives up.  The clock and the
 // abort flag are looked at once in 64 tries: reading the global timer between tries would delay
-// the wake-up.  The vote keeps the loop uniform.
+// the wake-up.  A try suspends the warp for longer than a hand-over takes, so under a short limit
+// the tries do not suspend and the clock is looked at after each.  The vote keeps the loop uniform.
 __device__ __forceinline__ bool waitw(const TcArgs &a, Shared &S, uint64_t *bar, uint32_t parity) {
-    if (__all_sync(kFull, mbar_try_wait(bar, parity))) return true;
+    if (__all_sync(kFull, mbar_test_wait(bar, parity))) return true;
     uint64_t t0 = 0;
 #pragma unroll 1
-    for (uint32_t i = 1; !__all_sync(kFull, mbar_try_wait(bar, parity)); i++) {
-        if (i & 63u) continue;
+    for (uint32_t i = 1; !__all_sync(kFull, a.look ? mbar_try_wait(bar, parity)
+                                                   : mbar_test_wait(bar, parity)); i++) {
+        if (i & a.look) continue;
         const uint64_t t = globaltimer();
         if (t0 == 0) t0 = t;
         const bool late = t - t0 > a.wait_ns;
@@ -682,6 +685,11 @@ bool encode(CUtensorMap *m, const void *base, int cols, int64_t rows, int64_t st
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+void set_limit(TcArgs &a, uint64_t ns) {
+    a.wait_ns = ns;
+    a.look = ns < 1000000 ? 0 : 63;
+}
+
 template <int kMode, typename T>
 cudaError_t run_tc(const TcArgs &a, const CUtensorMap &w0, const CUtensorMap &w1,
                    const CUtensorMap &x, const CUtensorMap &x16, int64_t most_tiles,
@@ -769,7 +777,7 @@ cudaError_t experts_tc(const ScaledExpertsArgs &e, uint8_t *ws, cudaStream_t st)
     a.slices = slices;
     a.nslices = nslices;
     a.status = e.status;
-    a.wait_ns = e.wait_ns;
+    set_limit(a, e.wait_ns);
     a.slots = L.slots;
     a.hq = ws + L.hq;
     a.hs = reinterpret_cast<float *>(ws + L.hs);
@@ -819,7 +827,7 @@ cudaError_t matmul_tc(const ScaledMatmulArgs &m, cudaStream_t st) {
     a.ldo = m.ldo;
     a.vec = (uintptr_t)m.out % 32 == 0 && m.ldo * dtype_bytes(m.dt) % 32 == 0 && m.N % 16 == 0;
     a.status = m.status;
-    a.wait_ns = m.wait_ns;
+    set_limit(a, m.wait_ns);
     const int64_t ms = (m.M + kMT - 1) / kMT;
     const int64_t sms = sm_count();
     if (sms <= 0) return cudaErrorInvalidDevice;
