@@ -75,8 +75,9 @@ class ChainTrace(ctypes.Structure):
 
 
 class RouteRule(ctypes.Structure):
-    """moe_route_rule: score, expert groups, renormalisation, scale and an optional bias (device
-    pointer to fp32 [E] or None)."""
+    """moe_route_rule: score, expert groups, renormalisation, scale and an optional bias: a
+    contiguous fp32 CUDA tensor [E], which the rule keeps, or a device pointer to such memory,
+    which the caller keeps."""
     _fields_ = [("score", ctypes.c_int32), ("n_group", ctypes.c_int32),
                 ("topk_group", ctypes.c_int32), ("group_top", ctypes.c_int32),
                 ("renorm", ctypes.c_int32), ("scale", ctypes.c_float),
@@ -84,6 +85,12 @@ class RouteRule(ctypes.Structure):
 
     def __init__(self, score=SCORE_SOFTMAX, n_group=1, topk_group=1, group_top=1, renorm=True,
                  scale=1.0, d_bias=None):
+        self.bias = None
+        if d_bias is not None and not isinstance(d_bias, int):
+            import torch
+            self.bias = _contiguous(d_bias, "d_bias", (d_bias.numel(),), torch.float32,
+                                    d_bias.get_device())
+            d_bias = d_bias.data_ptr()
         super().__init__(score, n_group, topk_group, group_top, int(renorm), scale, d_bias)
 
 
@@ -454,7 +461,7 @@ def _contiguous(t, name: str, shape, dtype, device: int):
     """t, checked: contiguous, on the CUDA device with this index, of the shape and type asked for
     (a type or a tuple of types)."""
     if t.get_device() != device or not t.is_cuda:
-        raise ValueError(f"{name}: a tensor on the current CUDA device is needed")
+        raise ValueError(f"{name}: a tensor on CUDA device {device} is needed")
     if t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name}: shape {tuple(t.shape)}, not a contiguous {tuple(shape)}")
     if t.dtype is not dtype and not (isinstance(dtype, tuple) and t.dtype in dtype):
@@ -502,6 +509,8 @@ class ScaledExperts:
         import torch
         T, E, k, dev = logits.shape[0], self.n_experts, self.k, torch.cuda.current_device()
         _contiguous(logits, "logits", (T, E), torch.float32, dev)
+        if self.rule.bias is not None:
+            _contiguous(self.rule.bias, "the rule's bias", (E,), torch.float32, dev)
         new = lambda *s: torch.empty(s, dtype=torch.int32, device=logits.device)  # noqa: E731
         ids, counts, offsets, perm, inv = new(T, k), new(E), new(E + 1), new(T * k), new(T * k)
         w = torch.empty((T, k), dtype=torch.float32, device=logits.device)

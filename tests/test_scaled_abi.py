@@ -213,3 +213,46 @@ def test_tensor_core_products_wait_on_bounded_barriers_only():
     assert not re.search(r"named_barrier|bar\.sync|barrier\.sync|barrier\.cta", code)
     body = code[code.index("k_scaled_tc(const TcArgs"):]
     assert len(re.findall(r"__syncthreads\(\)", code)) == 2 == body.count("__syncthreads()")
+
+
+class CudaTensor:
+    """What the binding asks of a tensor on a CUDA device, without one."""
+
+    is_cuda = True
+
+    def __init__(self, shape, dtype, device=0, pointer=FAKE):
+        self.shape, self.dtype, self.device, self.pointer = tuple(shape), dtype, device, pointer
+
+    def get_device(self):
+        return self.device
+
+    def is_contiguous(self):
+        return True
+
+    def numel(self):
+        return int(np.prod(self.shape))
+
+    def data_ptr(self):
+        return self.pointer
+
+
+def test_route_rule_keeps_its_bias(moe):
+    """A rule made from a tensor holds it: later calls do not read memory that was given back."""
+    import gc
+    import weakref
+
+    import torch
+    bias = CudaTensor((64,), torch.float32, pointer=FAKE + 512)
+    gone = weakref.ref(bias)
+    rule = moe.RouteRule(d_bias=bias)
+    del bias
+    gc.collect()
+    assert gone() is not None and rule.d_bias == FAKE + 512
+    del rule
+    gc.collect()
+    assert gone() is None
+    assert moe.RouteRule(d_bias=FAKE).d_bias == FAKE and moe.RouteRule().d_bias is None
+    with pytest.raises(ValueError):
+        moe.RouteRule(d_bias=torch.zeros(64))                       # not on a CUDA device
+    with pytest.raises(ValueError):
+        moe.RouteRule(d_bias=CudaTensor((64,), torch.bfloat16))
