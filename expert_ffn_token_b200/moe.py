@@ -473,7 +473,8 @@ class ScaledExperts:
     """The experts of one layer in e4m3 with 128 x 128 block scales, held in torch tensors, and
     the workspace for up to max_tokens tokens (marshalling only).
 
-    Its calls share one workspace: they follow one another on a stream (graphs of them too); what
+    Everything is on the CUDA device that is current when the layer is made, and its calls are made
+    with that device current.  Its calls share one workspace: they follow one another on a stream (graphs of them too); what
     runs at the same time on another stream is an object of its own.  No gradients.
 
     gate, up [n][ffn][hidden] and down [n][hidden][ffn] (uint8 or float8_e4m3fn), scales fp32
@@ -486,6 +487,7 @@ class ScaledExperts:
         n, f, h = gate.shape
         fb, hb = -(-f // 128), -(-h // 128)
         codes, f32, dev = (torch.uint8, torch.float8_e4m3fn), torch.float32, torch.cuda.current_device()
+        self.device = dev
         self.tensors = (_contiguous(gate, "gate", (n, f, h), codes, dev),
                         _contiguous(up, "up", (n, f, h), codes, dev),
                         _contiguous(down, "down", (n, h, f), codes, dev),
@@ -504,10 +506,18 @@ class ScaledExperts:
         self.status_word = torch.zeros(1, dtype=torch.int32, device=gate.device)
         self._ws, self._status = self.ws.data_ptr(), self.status_word.data_ptr()
 
+    def _current(self) -> int:
+        """The layer's device, which has to be the current one."""
+        import torch
+        if torch.cuda.current_device() != self.device:
+            raise ValueError(f"CUDA device {torch.cuda.current_device()} is current, the layer is on "
+                             f"{self.device}")
+        return self.device
+
     def route(self, logits):
         """(ids, w, offsets, perm, inv_perm) of fp32 logits [T][experts] by the layer's rule."""
         import torch
-        T, E, k, dev = logits.shape[0], self.n_experts, self.k, torch.cuda.current_device()
+        T, E, k, dev = logits.shape[0], self.n_experts, self.k, self._current()
         _contiguous(logits, "logits", (T, E), torch.float32, dev)
         if self.rule.bias is not None:
             _contiguous(self.rule.bias, "the rule's bias", (E,), torch.float32, dev)
@@ -524,7 +534,7 @@ class ScaledExperts:
         """The experts' combined output [T][hidden] for tokens routed by route() or route_topk (perm,
         the inverse of inv_perm, is not read)."""
         import torch
-        T, k, E, dev = x.shape[0], self.k, self.n_experts, torch.cuda.current_device()
+        T, k, E, dev = x.shape[0], self.k, self.n_experts, self._current()
         i32, f32, rows = torch.int32, torch.float32, (T, self.hidden)
         _contiguous(x, "x", rows, _FLOATS, dev)
         _contiguous(ids, "ids", (T, k), i32, dev)
@@ -548,4 +558,4 @@ class ScaledExperts:
         return self.forward(x, *self.route(logits), gate=gate, out=out)
 
     def status(self, clear: bool = True) -> int:
-        return read_status(self.status_word.data_ptr(), _stream(), clear)
+        return read_status(self.status_word.data_ptr(), _stream(self._current()), clear)

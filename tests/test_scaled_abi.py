@@ -256,3 +256,45 @@ def test_route_rule_keeps_its_bias(moe):
         moe.RouteRule(d_bias=torch.zeros(64))                       # not on a CUDA device
     with pytest.raises(ValueError):
         moe.RouteRule(d_bias=CudaTensor((64,), torch.bfloat16))
+
+
+def test_layer_refuses_calls_on_another_device_than_its_own(moe, monkeypatch):
+    """Weights and workspace of a layer are on its device: tensors on another one, current or not, are
+    refused before anything is launched."""
+    import torch
+    called = []
+    monkeypatch.setattr(moe, "scaled_experts", lambda *a: called.append(a))
+    monkeypatch.setattr(moe, "route_scored", lambda *a: called.append(a))
+    monkeypatch.setattr(moe, "read_status", lambda *a: called.append(a))
+    monkeypatch.setattr(moe, "_stream", lambda device=None: 0)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: current)
+    real = torch.empty
+    monkeypatch.setattr(torch, "empty", lambda *a, device=None, **k: real(*a, **k))
+    moe._fill_dtypes()
+    layer = moe.ScaledExperts.__new__(moe.ScaledExperts)
+    layer.device, layer.hidden, layer.n_experts, layer.k, layer.rule = 0, 32, 4, 2, moe.RouteRule()
+    layer.weights, layer._status, layer._ws, layer.ws_bytes = None, FAKE, FAKE, 0
+    layer.status_word = layer.route_ws = CudaTensor((1,), torch.int32)
+    layer.route_bytes = 0
+
+    def run(dev):
+        i32, f32, on = torch.int32, torch.float32, dict(device=dev)
+        layer.forward(CudaTensor((3, 32), f32, **on), CudaTensor((3, 2), i32, **on),
+                      CudaTensor((3, 2), f32, **on), CudaTensor((5,), i32, **on), None,
+                      CudaTensor((6,), i32, **on), out=CudaTensor((3, 32), f32, **on))
+
+    current = 0
+    run(0)
+    layer.status()
+    assert len(called) == 2
+    with pytest.raises(ValueError):
+        run(1)                                   # tensors elsewhere
+    current = 1
+    for dev in (0, 1):
+        with pytest.raises(ValueError):
+            run(dev)                             # the layer elsewhere
+        with pytest.raises(ValueError):
+            layer.route(CudaTensor((3, 4), torch.float32, device=dev))
+    with pytest.raises(ValueError):
+        layer.status()
+    assert len(called) == 2
