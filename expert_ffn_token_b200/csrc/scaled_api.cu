@@ -74,7 +74,8 @@ moe_status moe_route_scored(const float *d_logits, int T, int E, int k,
 moe_status moe_scaled_quantize(const void *d_x, int dtype, int T, int K, int64_t ldx,
                                uint8_t *d_q, int64_t ldq, float *d_s, int64_t lds,
                                uint32_t *d_status, void *stream) {
-    if (!d_x || !d_q || !d_s || !dtype_ok(dtype) || T < 0 || K <= 0) return MOE_ERR_INVALID_ARG;
+    if (!dtype_ok(dtype) || T < 0 || K <= 0) return MOE_ERR_INVALID_ARG;
+    if (T > 0 && (!d_x || !d_q || !d_s)) return MOE_ERR_INVALID_ARG;   // empty tensors have no address
     if (ldx < K || ldq < K || lds < T) return MOE_ERR_INVALID_ARG;
     if (!aligned(d_x, dtype_bytes(dtype)) || !aligned(d_q, 16) || ldq % 16 ||
         !words({d_s, d_status}))
@@ -98,7 +99,8 @@ moe_status moe_scaled_matmul(const uint8_t *d_a, int64_t lda, const float *d_as,
                              int M, int K, const uint8_t *d_b, int64_t ldb, const float *d_bs,
                              int N, void *d_out, int dtype, int64_t ldo, uint32_t *d_status,
                              void *d_ws, size_t ws_bytes, void *stream) {
-    if (!d_a || !d_as || !d_b || !d_bs || !d_out || !dtype_ok(dtype)) return MOE_ERR_INVALID_ARG;
+    if (!d_b || !d_bs || !dtype_ok(dtype)) return MOE_ERR_INVALID_ARG;
+    if (M > 0 && (!d_a || !d_as || !d_out)) return MOE_ERR_INVALID_ARG;
     if (M < 0 || N <= 0 || K <= 0 || lda < K || ldb < K || ldas < M || ldo < N)
         return MOE_ERR_INVALID_ARG;
     // the kernels' tile counts and coordinates are 32-bit

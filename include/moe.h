@@ -374,7 +374,7 @@ moe_status moe_route_scored(const float *d_logits, int T, int E, int k,
  * Per row and 128 columns: s = amax / 448 in fp32 and q = the e4m3 value nearest x / s (ties to
  * even; the quotient is not rounded in between); a block whose s is 0 is stored as zeros, a block with a
  * non-finite value as zeros with MOE_ERR_NONFINITE in d_status (may be NULL).  Bytes of d_q past
- * column K are left as they were.  T may be 0.                                               */
+ * column K are left as they were.  T may be 0 (d_x, d_q and d_s may then be NULL).            */
 moe_status moe_scaled_quantize(const void *d_x, int dtype, int T, int K, int64_t ldx,
                                uint8_t *d_q, int64_t ldq, float *d_s, int64_t lds,
                                uint32_t *d_status, void *stream);
@@ -386,7 +386,8 @@ moe_status moe_scaled_quantize(const void *d_x, int dtype, int T, int K, int64_t
  * dtype at the end.  d_a and d_b 16-byte aligned, lda and ldb multiples of 16 (the bytes from
  * column K to the next multiple of 16 may be read, in the last row too, but not used).  d_out aligned to its type.  d_status (may be NULL) receives device-side
  * errors.  The workspace (moe_scaled_matmul_workspace_size; may be 0 bytes, then d_ws may be
- * NULL) is 256-byte aligned scratch.  M may be 0.                                            */
+ * NULL) is 256-byte aligned scratch.  M may be 0 (d_a, d_as and d_out may then be NULL).  M, N and
+ * K are at most 2^30, lda and ldb below 2^40 (MOE_ERR_UNSUPPORTED).                          */
 moe_status moe_scaled_matmul_workspace_size(int M, int N, int K, size_t *bytes);
 moe_status moe_scaled_matmul(const uint8_t *d_a, int64_t lda, const float *d_as, int64_t ldas,
                              int M, int K, const uint8_t *d_b, int64_t ldb, const float *d_bs,

@@ -298,3 +298,20 @@ def test_layer_refuses_calls_on_another_device_than_its_own(moe, monkeypatch):
     with pytest.raises(ValueError):
         layer.status()
     assert len(called) == 2
+
+
+@pytest.mark.parametrize("dt", [0, 1, 2])
+def test_empty_batches_need_no_addresses(moe, dt):
+    """Zero rows are a call that does nothing, with the null addresses that empty tensors have; the
+    other arguments are checked all the same."""
+    L = moe.library()
+    quantise = lambda K=100, ldq=112: L.moe_scaled_quantize(None, dt, 0, K, 100, None, ldq, None, 0,  # noqa: E731
+                                                            None, None)
+    product = lambda b=FAKE, N=10, ldb=112: L.moe_scaled_matmul(  # noqa: E731
+        None, 112, None, 0, 0, 100, b, ldb, FAKE, N, None, dt, 10, None, None, 0, None)
+    before = moe.kernels_enqueued()
+    assert quantise() == moe.OK and product() == moe.OK
+    assert quantise(K=0) == moe.ERR_INVALID_ARG and quantise(ldq=104) == moe.ERR_ALIGNMENT
+    assert product(b=None) == moe.ERR_INVALID_ARG and product(N=0) == moe.ERR_INVALID_ARG
+    assert product(ldb=120) == moe.ERR_ALIGNMENT
+    assert moe.kernels_enqueued() == before
