@@ -717,7 +717,7 @@ struct ExpertsWs {
     int64_t slots, most_slices;
 };
 
-// y is sized for fp32; with a 16-bit output it is fp16.
+// y is sized for fp32; with a bf16 output it is fp16.
 ExpertsWs experts_ws(const moe_scaled_weights &w, int T, int k) {
     ExpertsWs L{};
     size_t p = 0;
@@ -741,18 +741,15 @@ ExpertsWs experts_ws(const moe_scaled_weights &w, int T, int k) {
     return L;
 }
 
-template <typename Y>
+template <typename Y, typename E>
 cudaError_t run_combine(const ScaledExpertsArgs &e, const void *y, const float *ys, cudaStream_t st) {
     const moe_scaled_weights &w = e.w;
     const int64_t units = (int64_t)e.T * ((w.hidden / 8 + 31) / 32);
-    return with_dtype(e.out_dt, [&](auto *tag) {
-        using E = std::remove_pointer_t<decltype(tag)>;
-        k_scaled_combine<Y, E><<<(unsigned)((units + 7) / 8), 256, 0, st>>>(
-            static_cast<const Y *>(y), ys, e.inv_perm, e.ids, e.rw, e.gate, e.T, e.k, w.n_experts,
-            w.shared, w.hidden, static_cast<E *>(e.out), e.status);
-        note_launches(1);
-        return cudaGetLastError();
-    });
+    k_scaled_combine<Y, E><<<(unsigned)((units + 7) / 8), 256, 0, st>>>(
+        static_cast<const Y *>(y), ys, e.inv_perm, e.ids, e.rw, e.gate, e.T, e.k, w.n_experts,
+        w.shared, w.hidden, static_cast<E *>(e.out), e.status);
+    note_launches(1);
+    return cudaGetLastError();
 }
 
 cudaError_t experts_tc(const ScaledExpertsArgs &e, uint8_t *ws, cudaStream_t st) {
@@ -800,15 +797,19 @@ cudaError_t experts_tc(const ScaledExpertsArgs &e, uint8_t *ws, cudaStream_t st)
     a.ldo = H;
     a.vec = true;
     const int64_t tiles = L.most_slices * a.row_tiles;
-    if (e.out_dt == MOE_DT_F32) {
+    // y is fp32, but for a bf16 output: there fp16's rounding is an eighth of the output's own, and
+    // half the bytes are written and read.  For an fp16 output the two would be equal.
+    if (e.out_dt != MOE_DT_BF16) {
         err = run_tc<kDown, float>(a, down, down, h, h16, tiles, st);
-        return err != cudaSuccess ? err : run_combine<float>(e, ws + L.y, nullptr, st);
+        if (err != cudaSuccess) return err;
+        return e.out_dt == MOE_DT_F32 ? run_combine<float, float>(e, ws + L.y, nullptr, st)
+                                      : run_combine<float, __half>(e, ws + L.y, nullptr, st);
     }
     a.ys = ys;
     // 2^y_exp * 65504 >= nkb * 128 * 448^2
     a.y_exp = (int)std::ceil(std::log2(a.nkb * (128.0 * 448.0 * 448.0) / 65504.0));
     err = run_tc<kDown, __half>(a, down, down, h, h16, tiles, st);
-    return err != cudaSuccess ? err : run_combine<__half>(e, ws + L.y, ys, st);
+    return err != cudaSuccess ? err : run_combine<__half, __nv_bfloat16>(e, ws + L.y, ys, st);
 }
 
 cudaError_t matmul_tc(const ScaledMatmulArgs &m, cudaStream_t st) {

@@ -675,3 +675,24 @@ def test_experts_wait_times_out_and_next_call_is_clean(torch, moe, short_waits, 
         moe.scaled_set_wait_limit(2_000_000_000)
         assert torch.equal(layer(x, l), first)
         assert layer.status() == 0
+
+
+# ------------------------------------------------------------------ what y and h are held in
+
+
+@pytest.mark.parametrize("T,E,k,H,F,shared", [(5, 16, 4, 512, 640, True), (40, 24, 8, 400, 272, False),
+                                              (200, 12, 6, 640, 256, True)])
+def test_experts_fp16_output_is_rounded_once(torch, moe, T, E, k, H, F, shared):
+    """With an fp16 output y is not held in fp16: the sum of k outputs that nearly cancel keeps the
+    accuracy of fp32 sums.  tol is the fp32 arithmetic's, EPS the output's own rounding."""
+    rng = np.random.default_rng(T + F)
+    W, layer = make_layer(torch, moe, rng, E, H, F, k, shared, T)
+    x = rng.standard_normal((T, H))
+    xd = _dev(torch, x).to(torch.float16)
+    ids = np.argsort(-rng.standard_normal((T, E)), 1)[:, :k].astype(np.int32)
+    w = rng.standard_normal((T, k)).astype(np.float32)
+    out = run_experts(torch, layer, xd, ids, w, None, torch.float16)
+    want, tol, _ = ref.experts(xd.double().cpu().numpy(), ids, w, None, W)
+    assert layer.status() == 0
+    err = np.abs(out.double().cpu().numpy() - want)
+    assert (err <= tol + np.abs(want) * EPS["float16"] + 2.0 ** -25).all()
