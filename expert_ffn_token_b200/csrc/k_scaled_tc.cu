@@ -96,8 +96,7 @@ struct TcArgs {
     uint8_t *hq;                 // gate/up: [slots][rows] and scales [row blocks][slots]
     float *hs;
     int64_t slots;
-    float *ys;                   // down to fp16: powers of two [slots][row blocks]
-    int y_exp;                   // and the exponent that keeps a sum of nkb blocks finite
+    uint8_t *ys;                 // down to fp16: powers of two [slots][32 columns], as fp32 exponents
     void *out;
     int64_t ldo;
     bool vec;                    // out rows are 32-byte aligned and rows a multiple of 16
@@ -109,6 +108,11 @@ struct TcArgs {
 struct Tile {
     int e, rt, slot, n;
 };
+
+// Powers of two of y, one per 32 columns: a row tile's eight are neighbours, the two of a thread
+// (columns c and c + 128) one 16-bit store.
+__host__ __device__ inline int ypitch(int n) { return (n + kNW - 1) / kNW * 8; }
+__device__ __forceinline__ int yindex(int c) { return c / kNW * 8 + c % 128 / 32 * 2 + c % kNW / 128; }
 
 // Tile i.  Experts: row tiles are innermost, so that the CTAs that run at the same time share
 // an expert's weights (its slices follow one another) and a slice's tokens.
@@ -376,7 +380,7 @@ __device__ void finish(const TcArgs &a, Shared &S, uint8_t *ring, int tiles, uin
     const int warp = __shfl_sync(kFull, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int quad = warp & 3, part = (warp - kEpiWarp0) >> 2;
     const int row = quad * 32 + lane;
-    constexpr bool kHalfY = kMode == kDown && sizeof(T) == 2;
+    constexpr bool kHalfY = kMode == kDown && sizeof(T) == 2;   // y in fp16
     const uint32_t base = tmem + ((uint32_t)quad << 21) + (uint32_t)(part * 32);  // lane quad * 32
     uint32_t q = 0, qph = 0;            // accumulator and its phase
     Pos p;
@@ -392,7 +396,6 @@ __device__ void finish(const TcArgs &a, Shared &S, uint8_t *ring, int tiles, uin
 #pragma unroll
         for (int j = 0; j < 32; j++) acc[0][j] = acc[1][j] = 0.f;
         const bool busy = quad * 32 < t.n;
-        float top[2] = {0.f, 0.f};           // the largest scale of each operand's blocks
 #pragma unroll 1
         for (int b = 0; b < a.nkb; b++) {
             if (u == 0 && !waitw(a, S, &S.sc_full[p.s], p.ph)) return;
@@ -401,10 +404,6 @@ __device__ void finish(const TcArgs &a, Shared &S, uint8_t *ring, int tiles, uin
             if (!waitw(a, S, &S.acc_full[q], qph)) return;
             if (busy) {
                 const float f[2] = {v * w.x, v * w.y};
-                if (kHalfY) {
-                    top[0] = fmaxf(top[0], fabsf(f[0]));
-                    top[1] = fmaxf(top[1], fabsf(f[1]));
-                }
                 tc_fence_after();
                 const uint32_t d = base + q * kNW;
 #pragma unroll
@@ -476,19 +475,24 @@ __device__ void finish(const TcArgs &a, Shared &S, uint8_t *ring, int tiles, uin
             }
         } else {
             T *out = static_cast<T *>(a.out) + ((int64_t)t.slot + row) * a.ldo;
+            uint32_t ex = 0u;
 #pragma unroll
             for (int u = 0; u < operands(kMode); u++) {
                 const int r0 = t.rt * width(kMode) + u * 128 + part * 32;
                 if (kHalfY) {
-                    // y as fp16 times a power of two per token and 128 rows: a block's sum is at
-                    // most 128 * 448^2 times its scale, so the power follows from the largest
-                    // scale, the same in every column part
-                    const int e = (int)(__float_as_uint(top[u]) >> 23) - 126 + a.y_exp;
-                    const int x = min(max(e, -126), 126);
+                    // y as fp16 times a power of two per token and 32 columns, which are this thread's:
+                    // the largest magnitude goes to [2^14, 2^15), so that what rounds as a
+                    // subnormal is 2^28 times smaller
+                    float mx = 0.f;                    // (passes over NaN, which stays NaN)
+#pragma unroll
+                    for (int j = 0; j < 32; j++) mx = fmaxf(mx, fabsf(acc[u][j]));
+                    // at most 114
+                    const int x = max((int)(__float_as_uint(mx) >> 23) - 127 - 14, -126);
                     const float inv = __uint_as_float((uint32_t)(127 - x) << 23);
-                    if (part == 0 && row < t.n && r0 < a.rows)
-                        a.ys[((int64_t)t.slot + row) * ((a.rows + 127) / 128) + 2 * t.rt + u] =
-                            __uint_as_float((uint32_t)(127 + x) << 23);
+                    ex |= (uint32_t)(127 + x) << (8 * u);
+                    if (u == 1 && row < t.n)
+                        *reinterpret_cast<uint16_t *>(a.ys + ((int64_t)t.slot + row) * ypitch(a.rows) +
+                                                      8 * t.rt + 2 * part) = (uint16_t)ex;
 #pragma unroll
                     for (int j = 0; j < 32; j++) acc[u][j] *= inv;
                 }
@@ -591,17 +595,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Eight values of y at column 8 c of a slot's row, with their power of two when y is fp16.
-__device__ __forceinline__ void load_y(const float *y, const float *, int64_t slot, int H, int c,
+__device__ __forceinline__ void load_y(const float *y, const uint8_t *, int64_t slot, int H, int c,
                                        float (&v)[8]) {
     const float4 *p = reinterpret_cast<const float4 *>(y + slot * H) + 2 * c;
     const float4 a = __ldg(p), b = __ldg(p + 1);
     v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
     v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
 }
-__device__ __forceinline__ void load_y(const __half *y, const float *ys, int64_t slot, int H, int c,
+__device__ __forceinline__ void load_y(const __half *y, const uint8_t *ys, int64_t slot, int H, int c,
                                        float (&v)[8]) {
     const uint4 r = __ldg(reinterpret_cast<const uint4 *>(y + slot * H) + c);
-    const float s = __ldg(ys + slot * ((H + 127) / 128) + c / 16);
+    const float s = __uint_as_float((uint32_t)__ldg(ys + slot * ypitch(H) + yindex(8 * c)) << 23);
     const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
     for (int i = 0; i < 4; i++) {
@@ -615,7 +619,7 @@ __device__ __forceinline__ void load_y(const __half *y, const float *ys, int64_t
 // takes 256 columns of a token, eight per lane; reads y once: bound by memory.
 template <typename Y, typename T>
 __global__ void __launch_bounds__(256)
-    k_scaled_combine(const Y *__restrict__ y, const float *__restrict__ ys,
+    k_scaled_combine(const Y *__restrict__ y, const uint8_t *__restrict__ ys,
                      const int32_t *__restrict__ inv_perm, const int32_t *__restrict__ ids,
                      const float *__restrict__ w, const float *__restrict__ gate, int tokens,
                      int k, int E, int shared, int H, T *__restrict__ out, uint32_t *status) {
@@ -732,7 +736,7 @@ ExpertsWs experts_ws(const moe_scaled_weights &w, int T, int k) {
     L.hq = take((size_t)L.slots * w.ffn);
     L.hs = take((size_t)sblocks(w.ffn) * L.slots * 4);
     L.y = take((size_t)L.slots * w.hidden * 4);
-    L.ys = take((size_t)L.slots * sblocks(w.hidden) * 4);
+    L.ys = take((size_t)L.slots * ypitch(w.hidden));
     L.most_slices = (int64_t)T * k / kMT + std::min<int64_t>(w.n_experts, (int64_t)T * k) +
                     (w.shared ? (T + kMT - 1) / kMT : 0);
     L.slices = take(sizeof(Job) * (size_t)L.most_slices);
@@ -742,7 +746,7 @@ ExpertsWs experts_ws(const moe_scaled_weights &w, int T, int k) {
 }
 
 template <typename Y, typename E>
-cudaError_t run_combine(const ScaledExpertsArgs &e, const void *y, const float *ys, cudaStream_t st) {
+cudaError_t run_combine(const ScaledExpertsArgs &e, const void *y, const uint8_t *ys, cudaStream_t st) {
     const moe_scaled_weights &w = e.w;
     const int64_t units = (int64_t)e.T * ((w.hidden / 8 + 31) / 32);
     k_scaled_combine<Y, E><<<(unsigned)((units + 7) / 8), 256, 0, st>>>(
@@ -759,7 +763,7 @@ cudaError_t experts_tc(const ScaledExpertsArgs &e, uint8_t *ws, cudaStream_t st)
     Job *slices = reinterpret_cast<Job *>(ws + L.slices);
     int32_t *nslices = reinterpret_cast<int32_t *>(ws + L.nslices);
     float *xs = reinterpret_cast<float *>(ws + L.xs);
-    float *ys = reinterpret_cast<float *>(ws + L.ys);
+    uint8_t *ys = ws + L.ys;
     CUtensorMap gate, up, down, x, x16, h, h16;
     if (!encode(&gate, w.d_gate, H, F, H, n, 128) || !encode(&up, w.d_up, H, F, H, n, 128) ||
         !encode(&down, w.d_down, F, H, F, n, 128) ||
@@ -806,8 +810,6 @@ cudaError_t experts_tc(const ScaledExpertsArgs &e, uint8_t *ws, cudaStream_t st)
                                       : run_combine<float, __half>(e, ws + L.y, nullptr, st);
     }
     a.ys = ys;
-    // 2^y_exp * 65504 >= nkb * 128 * 448^2
-    a.y_exp = (int)std::ceil(std::log2(a.nkb * (128.0 * 448.0 * 448.0) / 65504.0));
     err = run_tc<kDown, __half>(a, down, down, h, h16, tiles, st);
     return err != cudaSuccess ? err : run_combine<__half, __nv_bfloat16>(e, ws + L.y, ys, st);
 }

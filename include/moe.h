@@ -410,7 +410,7 @@ typedef struct {
  *   h = g / (1 + exp(-g)) * u in fp32, h^ = h quantised likewise per 128 values of ffn,
  *   y = W_down h^, d_out[t] = sum_j w[t][j] y[t][ids[t][j]] (+ gate[t] y[t][shared])
  * (y in fp32, or, with a bf16 output and more than 4 tokens, in fp16 times a power of two per
- * token and 128 columns), with d_x and d_out [T][hidden] contiguous of x_dtype and out_dtype, 16-byte aligned, d_gate
+ * token and 32 columns, the largest of which it brings to fp16's top), with d_x and d_out [T][hidden] contiguous of x_dtype and out_dtype, 16-byte aligned, d_gate
  * fp32 [T] (NULL: 1; only with shared).  A routed id or a slot outside its range is skipped and
  * reported as MOE_ERR_BOUNDS in d_status (may be NULL), a non-finite block of x or h is taken as
  * zeros and reported as MOE_ERR_NONFINITE.  1 <= T <= the max_tokens the workspace was sized for

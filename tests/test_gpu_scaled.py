@@ -696,3 +696,70 @@ def test_experts_fp16_output_is_rounded_once(torch, moe, T, E, k, H, F, shared):
     assert layer.status() == 0
     err = np.abs(out.double().cpu().numpy() - want)
     assert (err <= tol + np.abs(want) * EPS["float16"] + 2.0 ** -25).all()
+
+
+def magnitudes(x, ids, w, gate, W):
+    """The sum of |weight * y| over a token's experts [T][H] in 64 bits."""
+    T, E = x.shape[0], W["gate"][0].shape[0] - int(W["shared"])
+    xq = ref.wide_act(*ref.quantize(x))
+    c = np.zeros((T, E + int(W["shared"])))
+    np.add.at(c, (np.arange(T)[:, None], ids), w.astype(np.float64))
+    if W["shared"]:
+        c[:, E] = 1.0 if gate is None else gate
+    out = np.zeros((T, W["down"][0].shape[1]))
+    for e in range(c.shape[1]):
+        m = {n: ref.wide_weight(W[n][0][e], W[n][1][e]) for n in ("gate", "up", "down")}
+        g, u = xq @ m["gate"].T, xq @ m["up"].T
+        y = ref.wide_act(*ref.quantize(g / (1 + np.exp(-g)) * u)) @ m["down"].T
+        out += np.abs(c[:, e:e + 1] * y)
+    return out
+
+
+@pytest.mark.parametrize("unused", [1.0, 2.0 ** 20])
+@pytest.mark.parametrize("T,E,k,H,F", [(5, 8, 3, 400, 640), (150, 6, 2, 640, 384)])
+def test_experts_bf16_output_with_unused_scales(torch, moe, T, E, k, H, F, unused):
+    """A block of zero weights may be stored with any scale (1 instead of 0, say); what the other
+    blocks give keeps its accuracy.  y in fp16 may be off by 2^-11 of it, or by 2^-25 times its power of
+    two, which is at most 2^-14 of the largest of 32 columns."""
+    rng = np.random.default_rng(T + F)
+    W, layer = make_layer(torch, moe, rng, E, H, F, k, False, T)
+    codes, scales = W["down"]
+    codes[:, :, 128:256] = 0
+    scales *= 2.0 ** -12                        # weights of 2^-20 and so
+    scales[:, :, 1] = unused
+    W["down"] = codes, scales
+    layer.tensors[2].copy_(_dev(torch, codes))
+    layer.tensors[5].copy_(_dev(torch, scales))
+    xd = _dev(torch, rng.standard_normal((T, H))).to(torch.bfloat16)
+    ids = np.argsort(-rng.standard_normal((T, E)), 1)[:, :k].astype(np.int32)
+    w = rng.random((T, k)).astype(np.float32)
+    x = xd.double().cpu().numpy()
+    out = run_experts(torch, layer, xd, ids, w, None, torch.bfloat16)
+    want, tol, _ = ref.experts(x, ids, w, None, W)
+    mag = magnitudes(x, ids, w, None, W)
+    top = np.repeat(np.stack([mag[:, i:i + 32].max(1) for i in range(0, H, 32)], 1), 32, 1)[:, :H]
+    assert layer.status() == 0
+    err = np.abs(out.double().cpu().numpy() - want)
+    assert (err <= tol + mag * 2.0 ** -11 + top * 2.0 ** -39 + np.abs(want) * EPS["bfloat16"]).all()
+
+
+def test_experts_bf16_output_of_extreme_magnitudes(torch, moe):
+    """y from 2^-90 to near the largest fp32 (below, a product of two scales is no normal number): the
+    power of two follows."""
+    T, E, k, H, F = 12, 4, 1, 256, 128
+    rng = np.random.default_rng(0)
+    W, layer = make_layer(torch, moe, rng, E, H, F, k, False, T)
+    xd = _dev(torch, rng.standard_normal((T, H))).to(torch.bfloat16)
+    x = xd.double().cpu().numpy()
+    ids = (np.arange(T) % E).astype(np.int32)[:, None]
+    w = np.ones((T, 1), np.float32)
+    base = W["down"][1].copy()
+    for power in (-90, -30, -14, 0, 14, 60, 118):
+        W["down"] = W["down"][0], (base * 2.0 ** power).astype(np.float32)
+        layer.tensors[5].copy_(_dev(torch, W["down"][1]))
+        out = run_experts(torch, layer, xd, ids, w, None, torch.bfloat16)
+        want, tol, _ = ref.experts(x, ids, w, None, W)
+        top = np.abs(want).max(1, keepdims=True)
+        assert layer.status() == 0
+        err = np.abs(out.double().cpu().numpy() - want)
+        assert (err <= tol + np.abs(want) * (2.0 ** -11 + EPS["bfloat16"]) + top * 2.0 ** -39).all(), power
