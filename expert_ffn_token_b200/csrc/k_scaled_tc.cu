@@ -449,9 +449,14 @@ __device__ void finish(const TcArgs &a, Shared &S, uint8_t *ring, int tiles, uin
             if (row < t.n) {
                 const bool fin = mx < 0x7f800000u;
                 const float sc = fin ? __fdiv_rn(__uint_as_float(mx), kE4M3Max) : 0.f;
-                // h / sc as (h * pre) * (1 / (sc * pre)): pre keeps the reciprocal of a tiny scale finite
-                const float pre = sc < 0x1p-100f ? 0x1p100f : 1.0f;
-                const float inv = sc > 0.f ? __frcp_rn(sc * pre) : 0.f;
+                // both sides of h / sc times 2^100, exactly, where a tiny scale has no reciprocal
+                float s = sc;
+                if (sc < 0x1p-100f) {
+                    s *= 0x1p100f;
+#pragma unroll
+                    for (int j = 0; j < 32; j++) acc[0][j] *= 0x1p100f;
+                }
+                const float inv = __frcp_rn(s);
                 const int64_t slot = (int64_t)t.slot + row;
                 if (part == 0) {
                     a.hs[t.rt * a.slots + slot] = sc;
@@ -465,9 +470,8 @@ __device__ void finish(const TcArgs &a, Shared &S, uint8_t *ring, int tiles, uin
 #pragma unroll
                     for (int u = 0; u < 4; u++) {
                         const float *x = acc[0] + 16 * j + 4 * u;
-                        v[u] = cvt_e4m3x2(x[0] * pre * inv, x[1] * pre * inv) |
-                               (cvt_e4m3x2(x[2] * pre * inv, x[3] * pre * inv) << 16);
-                        if (!fin) v[u] = 0u;
+                        v[u] = quant4_normal(make_float4(x[0], x[1], x[2], x[3]), s, inv);
+                        if (!(sc > 0.f)) v[u] = 0u;
                     }
                     if (f + 16 * j < a.rows)
                         *reinterpret_cast<uint4 *>(hq + 16 * j) = make_uint4(v[0], v[1], v[2], v[3]);

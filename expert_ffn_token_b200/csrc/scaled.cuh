@@ -118,9 +118,9 @@ constexpr float kBelow = 1.0f - 0x1p-21f, kAbove = 1.0f + 0x1p-21f;
 __device__ __forceinline__ uint32_t quant4_at(float4 v, float r) {
     return cvt_e4m3x2(v.x * r, v.y * r) | (cvt_e4m3x2(v.z * r, v.w * r) << 16);
 }
-__device__ __forceinline__ uint32_t quant4(float4 v, float s, float inv) {
+// s at least 2^-100: below, 1 / s or the exact remainder may underflow.
+__device__ __forceinline__ uint32_t quant4_normal(float4 v, float s, float inv) {
     const uint32_t lo = quant4_at(v, inv * kBelow), hi = quant4_at(v, inv * kAbove);
-    if (s < 0x1p-100f) return quant4_wide(v, s);       // 1 / s or the exact remainder underflows
     if (lo == hi) return lo;
     const float f[4] = {v.x, v.y, v.z, v.w};
     uint32_t out = 0;
@@ -130,6 +130,10 @@ __device__ __forceinline__ uint32_t quant4(float4 v, float s, float inv) {
         out |= (l == h ? l : quant1_decide(f[i], s, l, h)) << (8 * i);
     }
     return out;
+}
+
+__device__ __forceinline__ uint32_t quant4(float4 v, float s, float inv) {
+    return s < 0x1p-100f ? quant4_wide(v, s) : quant4_normal(v, s, inv);
 }
 
 // The largest magnitude of four values, as the integer whose order it follows.

@@ -763,3 +763,37 @@ def test_experts_bf16_output_of_extreme_magnitudes(torch, moe):
         assert layer.status() == 0
         err = np.abs(out.double().cpu().numpy() - want)
         assert (err <= tol + np.abs(want) * (2.0 ** -11 + EPS["bfloat16"]) + top * 2.0 ** -39).all(), power
+
+
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("power", [0, 40, -120])
+@pytest.mark.parametrize("T", [1, 3, 5, 20, 140])
+def test_experts_h_halfway_between_e4m3_values(torch, moe, T, power, sign):
+    """h exactly halfway between each two e4m3 values goes to the even one, whatever the batch size:
+    g is 128, whose silu is 128; u is 448 w1 + 28 w2 = 448 m for the midpoint m; h is 448 * 128 m, of
+    which the largest, m = 448, makes the scale 448 * 128; the down matrix hands h^ out."""
+    E, H, F = 2, 256, 128
+    m = np.concatenate([sign * ref._MID, [448.0, 0.0]])
+    low = np.concatenate([ref._POS[:-1], [448.0, 0.0]])
+    step = np.concatenate([8 * np.diff(ref._POS), [0.0, 0.0]])
+    x = np.zeros((T, H), np.float32)
+    x[:, :3] = 448, 28, 64
+    W = {"shared": False}
+    gate, up, down = np.zeros((E, F, H)), np.zeros((E, F, H)), np.zeros((E, H, F))
+    gate[:, :, 2] = 2
+    up[:, :, 0], up[:, :, 1] = np.sign(m) * low, np.sign(m) * step
+    down[:, np.arange(F), np.arange(F)] = 1
+    scale = {"gate": 1.0, "up": 2.0 ** power, "down": 2.0 ** -power}
+    for name, v in (("gate", gate), ("up", up), ("down", down)):
+        assert np.array_equal(ref.E4M3[ref.encode(v)], v)
+        s = np.full((E, ref.blocks(v.shape[1]), ref.blocks(v.shape[2])), scale[name], np.float32)
+        W[name] = ref.encode(v), s
+    layer = moe.ScaledExperts(*(_dev(torch, W[n][i]) for n in ("gate", "up", "down") for i in (0, 1)),
+                              T, 1)
+    ids = (np.arange(T) % E).astype(np.int32)[:, None]
+    out = run_experts(torch, layer, _dev(torch, x), ids, np.ones((T, 1), np.float32), None,
+                      torch.float32).cpu().numpy()
+    assert layer.status() == 0
+    want = np.zeros(H)
+    want[:F] = ref.E4M3[ref.encode(m)] * 448 * 128
+    assert (out == want).all(), np.argwhere(out[0] != want).ravel()
