@@ -259,7 +259,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_one_gateup(const ScaledExpertsA
             gv += red[0][w][threadIdx.x];
             uv += red[1][w][threadIdx.x];
         }
-        a.h[(int64_t)j * F + f0 + threadIdx.x] = __fdiv_rn(gv, 1.0f + expf(-gv)) * uv;
+        a.h[(int64_t)j * F + f0 + threadIdx.x] = swiglu(gv, uv);
     }
 }
 
@@ -540,7 +540,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                 const float gv = ag[i] + s_part[warp][lane][i], uv = au[i] + s_part[warp][lane][4 + i];
                 // a column that is not routed here holds another token's products or nothing
                 const bool on = (mask >> (2 * tig + (i & 1))) & 1u;
-                hv[i] = on ? __fdiv_rn(gv, 1.0f + expf(-gv)) * uv : 0.f;
+                hv[i] = on ? swiglu(gv, uv) : 0.f;
             }
         }
         // the largest |h| of each column over the CTA's 128 rows

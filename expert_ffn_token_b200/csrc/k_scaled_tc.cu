@@ -140,12 +140,6 @@ __device__ __forceinline__ Tile tile_at(const TcArgs &a, int i) {
     return t;
 }
 
-// silu(g) * u in fp32 with CUDA's expf and its approximate division (2 ulp; a denominator past
-// 2^126 gives 0, where the quotient is below 2^-119).
-__device__ __forceinline__ float silu_mul(float g, float u) {
-    return __fdividef(g, 1.0f + expf(-g)) * u;
-}
-
 struct Shared {
     uint64_t full[kStages], empty[kStages], acc_full[kAccs], acc_empty[kAccs], sc_full[kScales],
         sc_empty[kScales], quarter[4], done;
@@ -432,12 +426,19 @@ __device__ void finish(const TcArgs &a, Shared &S, uint8_t *ring, int tiles, uin
         if (kMode == kGateUp) {
             // h, and its e4m3 form per token and 128 ffn values: this thread's 32 and those of the
             // other three column quarters
+            bool far = false;
+#pragma unroll
+            for (int j = 0; j < 32; j++) far |= acc[0][j] < kSiluFar;
+            if (far && row < t.n) {
+#pragma unroll
+                for (int j = 0; j < 32; j++) acc[0][j] = swiglu(acc[0][j], acc[1][j]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 32; j++) acc[0][j] = swiglu_near(acc[0][j], acc[1][j]);
+            }
             uint32_t mx = 0u;
 #pragma unroll
-            for (int j = 0; j < 32; j++) {
-                acc[0][j] = silu_mul(acc[0][j], acc[1][j]);
-                mx = max(mx, __float_as_uint(acc[0][j]) & 0x7fffffffu);
-            }
+            for (int j = 0; j < 32; j++) mx = max(mx, __float_as_uint(acc[0][j]) & 0x7fffffffu);
             S.amax[par][part][row] = mx;
             // the quarter's four warps meet at an mbarrier: a warp that gave up must not hold the others
             __syncwarp();

@@ -153,6 +153,20 @@ __device__ __forceinline__ uint32_t quant_block(float4 v, float *s, bool *finite
     return sc > 0.0f ? quant4(v, sc, __frcp_rn(sc)) : 0u;
 }
 
+// silu(g) * u in fp32, a few ulp off: g / (1 + exp(-g)) with CUDA's expf and its division of 2 ulp (an
+// IEEE division, whose slow path the unused rows of a tile take, made 64 tokens 410 us instead of
+// 315).  From -80 on down, where exp(-g) leaves that division's range and then fp32's, the 1 is less
+// than an ulp, and g exp(g) is the same.
+constexpr float kSiluFar = -80.0f;
+__device__ __forceinline__ float swiglu_near(float g, float u) {
+    return __fdividef(g, 1.0f + expf(-g)) * u;
+}
+__device__ __forceinline__ float swiglu(float g, float u) {
+    const bool far = g < kSiluFar;
+    const float e = expf(far ? g : -g);
+    return (far ? g * e : __fdividef(g, 1.0f + e)) * u;
+}
+
 // ------------------------------------------------------------------ launchers
 
 // Launch behind the previous kernel of the stream (programmatic dependent launch): the kernel may

@@ -797,3 +797,34 @@ def test_experts_h_halfway_between_e4m3_values(torch, moe, T, power, sign):
     want = np.zeros(H)
     want[:F] = ref.E4M3[ref.encode(m)] * 448 * 128
     assert (out == want).all(), np.argwhere(out[0] != want).ravel()
+
+
+@pytest.mark.parametrize("T", [1, 3, 5, 20])
+def test_experts_h_of_very_negative_gates(torch, moe, T):
+    """silu from -60 down to fp32's smallest normal results keeps its accuracy at every batch size: a
+    block of such h is as accurate as any other, since its scale is its own.  Four fp32 exponentials
+    and roundings are at most 2^-20 of h; where that crosses a midpoint, the neighbour is right."""
+    E, H, F = 2, 256, 128
+    rng = np.random.default_rng(T)
+    for g in (-60.0, -79.0, -81.0, -83.0, -86.0, -87.5, -88.5, -90.0):
+        u = rng.choice(ref._POS[64:100], F)
+        x = np.zeros((T, H), np.float32)
+        x[:, 0], x[:, 1] = 448, 64
+        v = {"gate": np.zeros((E, F, H)), "up": np.zeros((E, F, H)), "down": np.zeros((E, H, F))}
+        v["gate"][:, :, 1] = 1
+        v["up"][:, :, 0] = u
+        v["down"][:, np.arange(F), np.arange(F)] = 1
+        scale = {"gate": g / 64, "up": 2.0 ** 60, "down": 2.0 ** 50}
+        W = {n: (ref.encode(m), np.full((E, ref.blocks(m.shape[1]), ref.blocks(m.shape[2])), scale[n],
+                                        np.float32)) for n, m in v.items()}
+        layer = moe.ScaledExperts(*(_dev(torch, W[n][i]) for n in v for i in (0, 1)), T, 1)
+        ids = (np.arange(T) % E).astype(np.int32)[:, None]
+        out = run_experts(torch, layer, _dev(torch, x), ids, np.ones((T, 1), np.float32), None,
+                          torch.float32).cpu().numpy().astype(np.float64)[:, :F]
+        assert layer.status() == 0
+        g32 = float(np.float32(64) * W["gate"][1][0, 0, 0])
+        h = g32 / (1 + np.exp(-g32)) * 448 * u * 2.0 ** 60
+        r = np.abs(h) / np.abs(h).max() * 448            # all of one block: the scale's error cancels
+        lo, hi = (ref.E4M3[ref.encode(r * (1 + f * 2.0 ** -20))] for f in (-1, 1))
+        s = np.abs(h).max() / 448 * 2.0 ** 50
+        assert (-out >= lo * s * (1 - 2.0 ** -19)).all() and (-out <= hi * s * (1 + 2.0 ** -19)).all(), g
