@@ -175,12 +175,12 @@ __device__ void route_row(const float *__restrict__ src, int E, int k, const moe
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
         score.top = top;
-        if (bias) {                       // the scores meet the bias: 64 bits
+        if (bias || !rule.renorm) {       // the sum counts in v or in the weights: 64 bits
             double sum = 0.0;
 #pragma unroll 1
             for (int e = lane; e < E; e += 32) sum += exp((double)__ldg(src + e) - (double)top);
             score.inv = 1.0 / warp_sum(sum);
-        } else if (!rule.renorm || rule.group_top == 2) {
+        } else if (rule.group_top == 2) { // a common factor of the group sums
             float sum = 0.f;
 #pragma unroll
             for (int i = 0; i < NV; i++) sum += expf(l[i] - top);

@@ -828,3 +828,18 @@ def test_experts_h_of_very_negative_gates(torch, moe, T):
         lo, hi = (ref.E4M3[ref.encode(r * (1 + f * 2.0 ** -20))] for f in (-1, 1))
         s = np.abs(h).max() / 448 * 2.0 ** 50
         assert (-out >= lo * s * (1 - 2.0 ** -19)).all() and (-out <= hi * s * (1 + 2.0 ** -19)).all(), g
+
+
+@pytest.mark.parametrize("T,E,k", [(1, 256, 8), (70, 512, 10), (9, 1000, 32), (40, 60, 6), (5, 1032, 8)])
+@pytest.mark.parametrize("rule", [dict(), dict(n_group=4, topk_group=2, group_top=2)])
+def test_route_scored_softmax_weights_are_rounded_once(torch, moe, T, E, k, rule):
+    """Weights that are not renormalised are the 64-bit softmax, rounded to fp32 once (half a step; the
+    64-bit arithmetic is off by less than 2^-40)."""
+    rng = np.random.default_rng(T + E)
+    l = (2 * rng.standard_normal((T, E))).astype(np.float32)
+    ids, w, *_, status = run_route(torch, moe, l, k, renorm=False, **rule)
+    full = dict(n_group=1, topk_group=1, group_top=1)
+    full.update(rule)
+    rid, rw = ref.route(l, k, "softmax", renorm=False, scale=1.0, bias=None, **full)
+    assert status == 0 and np.array_equal(ids, rid)
+    assert (np.abs(w - rw) <= (2.0 ** -24 + 2.0 ** -40) * rw).all()
