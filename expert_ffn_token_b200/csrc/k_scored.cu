@@ -6,7 +6,7 @@
 // whatever the order of a sum or the last bits of an fp32 exponential would say.  Only what may
 // be chosen pays for 64 bits (k_scored_rows, a warp per token, the row in registers):
 //   - the k-th largest of the 32 lanes' own maxima is a bound that the k chosen reach, so the
-//     experts at or above it (for fp32 scores: above it less twice their error) hold the choice;
+//     experts at or above it (for fp32 scores: above it less twice the error there) hold the choice;
 //     there are seldom more than a dozen;
 //   - these candidates, one per lane, get 64-bit scores and are sorted by (value, id);
 //   - groups are ranked by fp32 sums, and by 64-bit ones where two lie within the error;
@@ -92,9 +92,14 @@ __device__ __noinline__ int select_rounds(V (&v)[NV], int k) {
     return mine;
 }
 
-// Top two of a lane's share of its group: values come from get(element).
+// The two largest values of a lane's group: values come from get(element).
+template <typename V>
+struct Best {
+    V b1, b2;
+    __device__ __forceinline__ V value(int top) const { return top == 2 ? b1 + b2 : b1; }
+};
 template <typename V, typename Get>
-__device__ __forceinline__ V group_value(int per, int first, int step, int width, int top, Get get) {
+__device__ __forceinline__ Best<V> group_best(int per, int first, int step, int width, Get get) {
     V b1 = -INFINITY, b2 = -INFINITY;
     for (int i = first; i < per; i += step) {
         const V v = get(i);
@@ -106,29 +111,41 @@ __device__ __forceinline__ V group_value(int per, int first, int step, int width
         b2 = fmax(fmin(b1, o1), fmax(b2, o2));
         b1 = fmax(b1, o1);
     }
-    return top == 2 ? b1 + b2 : b1;
+    return {b1, b2};
 }
 
-// Which groups stay (a bit each), from lane g's value of group g.  *gap: the smallest kept value
-// less the largest dropped one.
+// Which groups stay (a bit each), from lane g's value of group g.
 template <typename V>
-__device__ __forceinline__ unsigned keep_groups(V mine, int n_group, int topk_group, V *gap) {
+__device__ __forceinline__ unsigned keep_groups(V mine, int n_group, int topk_group) {
     const int lane = threadIdx.x & 31;
     int rank = 0;
     for (int g = 0; g < n_group; g++) {
         const V o = __shfl_sync(kFull, mine, g);
         rank += o > mine || (o == mine && g < lane);
     }
-    const bool in = lane < n_group, keep = in && rank < topk_group;
-    V lo = keep ? mine : (V)INFINITY, hi = in && !keep ? mine : (V)-INFINITY;
+    return __ballot_sync(kFull, lane < n_group && rank < topk_group);
+}
+
+// Whether every kept group's value is above every dropped one's, each up to err off.  A sum past
+// fp32 is known to be past its largest value only.
+__device__ __forceinline__ bool keep_certain(float mine, float err, unsigned keep, int n_group) {
+    constexpr float kMost = 3.402823466e+38f;
+    const int lane = threadIdx.x & 31;
+    const bool in = lane < n_group, kept = (keep >> lane) & 1u;
+    const float m = fminf(fmaxf(mine, -kMost), kMost);
+    float lo = in && kept ? m - err : INFINITY, hi = in && !kept ? m + err : -INFINITY;
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) {
-        lo = fmin(lo, __shfl_xor_sync(kFull, lo, o));
-        hi = fmax(hi, __shfl_xor_sync(kFull, hi, o));
+        lo = fminf(lo, __shfl_xor_sync(kFull, lo, o));
+        hi = fmaxf(hi, __shfl_xor_sync(kFull, hi, o));
     }
-    *gap = lo - hi;
-    return __ballot_sync(kFull, keep);
+    return lo > hi;
 }
+
+// Bound on what an fp32 value (score plus bias) is off by: a score is at most 1 and a few roundings
+// off, the sum rounds once more.  It goes by the value itself, not by the largest bias: one expert
+// masked by -1e9 must not blur the others.
+__device__ __forceinline__ float value_err(float v) { return 0x1p-19f * (1.0f + fabsf(v)); }
 
 // One token by one warp.  row: E + E / 32 floats of shared memory of the warp's own (groups), cand:
 // 32 ints.  ids and w: k entries each (lane j writes entry j).
@@ -138,7 +155,7 @@ __device__ void route_row(const float *__restrict__ src, int E, int k, const moe
     const int lane = threadIdx.x & 31;
     const float *bias = rule.d_bias;
     const bool sigmoid = rule.score == MOE_SCORE_SIGMOID;
-    float l[NV], top = -INFINITY, size = 0.f;
+    float l[NV], top = -INFINITY;
     uint32_t mag = 0;                     // the largest magnitude: not finite from 0x7f800000 on
 #pragma unroll
     for (int i = 0; i < NV; i++) {
@@ -157,8 +174,6 @@ __device__ void route_row(const float *__restrict__ src, int E, int k, const moe
             const int e = lane + 32 * i;
             if (e < E) b = max(b, __float_as_uint(__ldg(bias + e)) & 0x7fffffffu);
         }
-        b = __reduce_max_sync(kFull, b);
-        size = __uint_as_float(b);
         mag = max(mag, b);
     }
     if (__any_sync(kFull, mag >= 0x7f800000u)) {
@@ -188,14 +203,11 @@ __device__ void route_row(const float *__restrict__ src, int E, int k, const moe
         }
         inv32 = (float)score.inv;
     }
-    // fp32 values: scores plus bias, at most err from the 64-bit ones (a score is at most 1 and a
-    // few roundings off, the sum rounds once more)
+    // fp32 values: scores plus bias, at most value_err from the 64-bit ones
     const bool grouped = rule.n_group > 1;
     const bool need = bias || (grouped && rule.group_top == 2);
     float v[NV];
-    float err = 0.f;
     if (need) {
-        err = 0x1p-19f * (1.0f + size);
 #pragma unroll
         for (int i = 0; i < NV; i++) {
             const int e = lane + 32 * i;
@@ -212,7 +224,7 @@ __device__ void route_row(const float *__restrict__ src, int E, int k, const moe
     if (grouped) {
         per = E / rule.n_group;
         const bool lined = per % 32 == 0;             // a group is whole registers of the warp
-        float value = -INFINITY;                      // lane g: the value of group g
+        float value = -INFINITY, err = 0.f;           // lane g: the value of group g, its error
         int width = 32;                               // else: lanes per group
         while (width > 1 && 32 / width < rule.n_group) width >>= 1;
         const int g = lane / width, base = g * per;
@@ -228,13 +240,16 @@ __device__ void route_row(const float *__restrict__ src, int E, int k, const moe
                 b1 = max(b1, x);
                 if (--left == 0) {                    // the group's last register
                     const uint32_t m1 = __reduce_max_sync(kFull, b1);
-                    float sum = key_value(m1);
+                    Best<float> best{key_value(m1), 0.f};
                     if (rule.group_top == 2) {
                         const unsigned at = __ballot_sync(kFull, b1 == m1);
                         const uint32_t m2 = __reduce_max_sync(kFull, b1 == m1 ? b2 : b1);
-                        sum += key_value(at & (at - 1) ? m1 : m2);
+                        best.b2 = key_value(at & (at - 1) ? m1 : m2);
                     }
-                    if (lane == at_group) value = sum;
+                    if (lane == at_group) {
+                        value = best.value(rule.group_top);
+                        err = value_err(best.b1) + value_err(best.b2);
+                    }
                     at_group++;
                     left = regs;
                     b1 = b2 = 0;
@@ -248,29 +263,28 @@ __device__ void route_row(const float *__restrict__ src, int E, int k, const moe
                 if (e < E) row[e + (e >> 5)] = v[i];
             }
             __syncwarp();
-            value = group_value<float>(mine ? per : 0, lane % width, width, width, rule.group_top,
-                                       [&](int i) {
-                                           const int e = base + i;
-                                           return row[e + (e >> 5)];
-                                       });
-            value = __shfl_sync(kFull, value, (lane * width) & 31);
+            Best<float> best = group_best<float>(mine ? per : 0, lane % width, width, width,
+                                                 [&](int i) {
+                                                     const int e = base + i;
+                                                     return row[e + (e >> 5)];
+                                                 });
+            if (rule.group_top == 1) best.b2 = 0.f;
+            value = __shfl_sync(kFull, best.value(rule.group_top), (lane * width) & 31);
+            err = __shfl_sync(kFull, value_err(best.b1) + value_err(best.b2), (lane * width) & 31);
         }
-        float gap;
-        keep = keep_groups(value, rule.n_group, rule.topk_group, &gap);
-        // (sums past fp32 are infinite, and the gap of two such is a NaN)
-        if (need && rule.topk_group < rule.n_group && !(gap > 4.0f * err)) {
-            const double exact = group_value<double>(
-                mine ? per : 0, lane % width, width, width, rule.group_top, [&](int i) {
+        keep = keep_groups(value, rule.n_group, rule.topk_group);
+        if (need && rule.topk_group < rule.n_group &&
+            !keep_certain(value, err, keep, rule.n_group)) {
+            const double exact =
+                group_best<double>(mine ? per : 0, lane % width, width, width, [&](int i) {
                     const int e = base + i;
                     return score(__ldg(src + e)) + (bias ? (double)__ldg(bias + e) : 0.0);
-                });
-            double gap64;
+                }).value(rule.group_top);
             keep = keep_groups(__shfl_sync(kFull, exact, (lane * width) & 31), rule.n_group,
-                               rule.topk_group, &gap64);
+                               rule.topk_group);
         }
     }
     // the order's values; experts of dropped groups and past the end are out
-    if (!bias) err = 0.f;
     const uint32_t magic = per > 1 ? (uint32_t)(0xffffffffu / (uint32_t)per + 1u) : 0u;
     uint32_t best = 0;
 #pragma unroll
@@ -290,7 +304,12 @@ __device__ void route_row(const float *__restrict__ src, int E, int k, const moe
         if (left == bound) left = 0;
     }
     float least = -3.402823466e+38f;      // every finite value: fewer than k lanes hold any
-    if (bound > order_key(-INFINITY)) least = key_value(bound) - 2.0f * err;
+    if (bound > order_key(-INFINITY)) {
+        // k experts are at least the bound, less its error; what may reach that is off by as much
+        // again (an error grows by 2^-24 of what the value changes by, which the bound covers)
+        least = key_value(bound);
+        if (bias) least -= 2.0f * value_err(least);
+    }
     int held = 0;
 #pragma unroll
     for (int i = 0; i < NV; i++) held += v[i] >= least;

@@ -843,3 +843,26 @@ def test_route_scored_softmax_weights_are_rounded_once(torch, moe, T, E, k, rule
     rid, rw = ref.route(l, k, "softmax", renorm=False, scale=1.0, bias=None, **full)
     assert status == 0 and np.array_equal(ids, rid)
     assert (np.abs(w - rw) <= (2.0 ** -24 + 2.0 ** -40) * rw).all()
+
+
+@pytest.mark.parametrize("E,k", [(64, 6), (256, 8), (512, 10), (120, 5), (1000, 12)])
+@pytest.mark.parametrize("mask", [-1e9, float(np.finfo(np.float32).min), -300.0])
+@pytest.mark.parametrize("name", ["softmax bias", "sigmoid bias", "groups top1 bias", "groups top2 bias"])
+def test_route_scored_masked_by_the_bias(torch, moe, name, mask, E, k):
+    """Experts masked by a large negative bias, whole groups among them, leave near ties of the open
+    ones to be decided as 64-bit values decide them; so do single experts with large biases."""
+    T = 96
+    rng = np.random.default_rng(E + k)
+    rule = dict(RULES[name])
+    bias = (0.25 + rng.integers(-2, 3, E) * 2.0 ** -25).astype(np.float32)
+    per = E // 4
+    bias[rng.permutation(E)[:E // 3]] = mask
+    bias[:per] = mask                                   # a whole group
+    bias[per + 2:2 * per] = mask                        # a group of at most two open experts
+    bias[-per:-per + 3] = 1e6                           # and some that tie far above the scores
+    rule["bias"] = bias
+    base = rng.standard_normal((T, 1)).astype(np.float32)
+    steps = rng.integers(-3, 4, (T, E)).astype(np.float32)
+    l = (base + steps * np.spacing(np.abs(base))).astype(np.float32)
+    l[T // 2:] = (2 * rng.standard_normal((T - T // 2, E))).astype(np.float32)
+    check_route(torch, moe, l, k, rule)
