@@ -108,17 +108,19 @@ __device__ __forceinline__ void put_frag(float *red, const float (&c)[4], int g,
 
 // ------------------------------------------------------------------ one matrix
 
+// grid (rows of weights / 16): up to 8 rows of a, the MMA's columns.
+static_assert(kSmallT == 8, "a row of a per MMA column");
 template <typename T>
 __global__ void __launch_bounds__(kWarps * 32) k_scaled_rows(const ScaledMatmulArgs a) {
     __shared__ float red[kWarps][kTile * 8];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, tig = lane & 3;
-    const int n0 = blockIdx.x * kTile, m0 = blockIdx.y * 8;
+    const int n0 = blockIdx.x * kTile;
     const int nb = sblocks(a.K);
     const uint8_t *lo = a.b + (int64_t)min(n0 + g, a.N - 1) * a.ldb;
     const uint8_t *hi = a.b + (int64_t)min(n0 + g + 8, a.N - 1) * a.ldb;
-    const uint8_t *xr = a.a + (int64_t)min(m0 + g, a.M - 1) * a.lda;
+    const uint8_t *xr = a.a + (int64_t)min(g, a.M - 1) * a.lda;
     const float *ws = a.bs + (int64_t)(n0 / kSBlk) * nb;
-    const int c0 = m0 + 2 * tig, c1 = c0 + 1;
+    const int c0 = 2 * tig, c1 = c0 + 1;
     float acc[4] = {0.f, 0.f, 0.f, 0.f};
     struct Block {
         Half2 l, h, x;
@@ -129,7 +131,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_scaled_rows(const ScaledMatmulA
         const bool in = b < nb;
         k.l.load(lo, in && n0 + g < a.N, k0, a.K);
         k.h.load(hi, in && n0 + g + 8 < a.N, k0, a.K);
-        k.x.load(xr, in && m0 + g < a.M, k0, a.K);
+        k.x.load(xr, in && g < a.M, k0, a.K);
         k.sw = in ? __ldg(ws + b) : 0.f;
         k.s0 = in && c0 < a.M ? __ldg(a.as + b * a.ldas + c0) : 0.f;
         k.s1 = in && c1 < a.M ? __ldg(a.as + b * a.ldas + c1) : 0.f;
@@ -162,7 +164,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_scaled_rows(const ScaledMatmulA
     __syncthreads();
     const int i = threadIdx.x;
     if (i < kTile * 8) {
-        const int m = m0 + i / kTile, n = n0 + i % kTile;
+        const int m = i / kTile, n = n0 + i % kTile;
         if (m < a.M && n < a.N)
             static_cast<T *>(a.out)[m * a.ldo + n] = from_f32<T>(sum_warps(red, i));
     }
@@ -676,7 +678,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
 
 cudaError_t launch_scaled_small(const ScaledMatmulArgs &a, cudaStream_t st) {
     if (a.M <= 0) return cudaSuccess;
-    const dim3 grid((a.N + kTile - 1) / kTile, (a.M + 7) / 8);
+    if (a.M > kSmallT) return cudaErrorInvalidValue;
+    const unsigned grid = (a.N + kTile - 1) / kTile;
     return with_dtype(a.dt, [&](auto *tag) {
         using E = std::remove_pointer_t<decltype(tag)>;
         k_scaled_rows<E><<<grid, kWarps * 32, 0, st>>>(a);

@@ -565,32 +565,14 @@ __global__ void __launch_bounds__(kWarps * 32)
         const int per = E / rule.n_group;
         double mine = -INFINITY;             // lane g: the value of group g
         for (int g = 0; g < rule.n_group; g++) {
-            double b1 = -INFINITY, b2 = -INFINITY;
-            for (int i = lane; i < per; i += 32) {
-                const double v = row[g * per + i];
-                b2 = fmax(b2, fmin(b1, v));
-                b1 = fmax(b1, v);
-            }
-#pragma unroll
-            for (int o = 16; o >= 1; o >>= 1) {
-                const double o1 = __shfl_xor_sync(kFull, b1, o);
-                const double o2 = __shfl_xor_sync(kFull, b2, o);
-                b2 = fmax(fmin(b1, o1), fmax(b2, o2));
-                b1 = fmax(b1, o1);
-            }
+            Best<double> best = group_best<double>(per, lane, 32, 32,
+                                                   [&](int i) { return row[g * per + i]; });
             // without a bias the row holds logits; one value is ordered as its score is
-            if (!bias && rule.group_top == 2) {
-                b1 = score((float)b1);
-                b2 = score((float)b2);
-            }
-            if (lane == g) mine = rule.group_top == 2 ? b1 + b2 : b1;
+            if (!bias && rule.group_top == 2)
+                best = {score((float)best.b1), score((float)best.b2)};
+            if (lane == g) mine = best.value(rule.group_top);
         }
-        int rank = 0;
-        for (int g = 0; g < rule.n_group; g++) {
-            const double o = __shfl_sync(kFull, mine, g);
-            rank += o > mine || (o == mine && g < lane);
-        }
-        const unsigned keep = __ballot_sync(kFull, lane < rule.n_group && rank < rule.topk_group);
+        const unsigned keep = keep_groups(mine, rule.n_group, rule.topk_group);
         for (int e = lane; e < E; e += 32)
             if (!((keep >> (e / per)) & 1u)) row[e] = -INFINITY;
         __syncwarp();

@@ -220,7 +220,7 @@ struct ScaledMatmulArgs {
 // The product on the kernel that suits its sizes, and the workspace it needs.
 size_t scaled_matmul_ws_bytes(int M, int N, int K);
 cudaError_t launch_scaled_matmul(const ScaledMatmulArgs &a, void *ws, cudaStream_t st);
-// k_scaled_small.cu: 8 tokens per pass over the weights.
+// k_scaled_small.cu: M <= kSmallT.
 cudaError_t launch_scaled_small(const ScaledMatmulArgs &a, cudaStream_t st);
 
 constexpr int kScaledMaxDim = 1 << 16;             // hidden and ffn of scaled experts
@@ -255,7 +255,7 @@ cudaError_t launch_scaled_spread(const ScaledExpertsArgs &e, uint8_t *q, float *
 // The layer on the kernels that suit T, and the workspace they need for exactly T tokens.
 size_t scaled_experts_ws_bytes(const moe_scaled_weights &w, int T, int k);
 cudaError_t launch_scaled_experts(const ScaledExpertsArgs &a, void *ws, cudaStream_t st);
-// k_scaled_small.cu: T <= kSmallT, and the workspace for it.
+// k_scaled_small.cu: T <= kSmallExpertsT, and the workspace for it.
 size_t scaled_small_ws_bytes(int T, int k, int shared, int H, int F);
 cudaError_t launch_scaled_experts_small(const ScaledExpertsArgs &a, void *ws, cudaStream_t st);
 
