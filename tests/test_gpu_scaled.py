@@ -866,3 +866,41 @@ def test_route_scored_masked_by_the_bias(torch, moe, name, mask, E, k):
     l = (base + steps * np.spacing(np.abs(base))).astype(np.float32)
     l[T // 2:] = (2 * rng.standard_normal((T - T // 2, E))).astype(np.float32)
     check_route(torch, moe, l, k, rule)
+
+
+def _random_layer(torch, moe, rng, E, H, F, k, shared, T):
+    """Codes even over all finite e4m3 values, which are quick to draw."""
+    W = {"shared": shared}
+    n = E + int(shared)
+    for name, rows, cols in (("gate", F, H), ("up", F, H), ("down", H, F)):
+        q = rng.integers(0, 127, (n, rows, cols), dtype=np.uint8)
+        q |= rng.integers(0, 2, q.shape, dtype=np.uint8) << 7
+        s = np.exp(0.5 * rng.standard_normal((n, ref.blocks(rows), ref.blocks(cols))))
+        W[name] = q, (s / (110 * cols ** 0.5)).astype(np.float32)
+    t = [_dev(torch, W[m][i]) for m in ("gate", "up", "down") for i in (0, 1)]
+    return W, moe.ScaledExperts(*t, T, k, shared=shared)
+
+
+@pytest.mark.parametrize("E,k,H,F,shared,sizes", [
+    (12, 10, 2560, 640, True, (1, 3, 5, 40, 300)), (256, 8, 256, 128, True, (2, 6, 70)),
+    (2, 1, 7168, 2048, False, (1, 4, 20)), (1, 1, 16, 4096, False, (2, 9)), (3, 3, 4096, 16, True, (4, 5))])
+def test_experts_of_whole_layers(torch, moe, E, k, H, F, shared, sizes):
+    """Layers as large as those in use, long and thin ones, and many experts, at each batch size's
+    kernels and with each output type."""
+    rng = np.random.default_rng(H + F)
+    W, layer = _random_layer(torch, moe, rng, E, H, F, k, shared, max(sizes))
+    for T in sizes:
+        xd = _dev(torch, rng.standard_normal((T, H))).to(torch.bfloat16)
+        ids = np.argsort(-rng.standard_normal((T, E)), 1)[:, :k].astype(np.int32)
+        w = rng.random((T, k)).astype(np.float32)
+        x = xd.double().cpu().numpy()
+        want, tol, _ = ref.experts(x, ids, w, None, W)
+        for dtype in EPS:
+            out = run_experts(torch, layer, xd, ids, w, None, getattr(torch, dtype))
+            allowed = tol + np.abs(want) * EPS[dtype] + 2.0 ** -25
+            if T > 4 and dtype == "bfloat16":
+                mag = magnitudes(x, ids, w, None, W)
+                allowed += mag * 2.0 ** -11 + mag.max(1, keepdims=True) * 2.0 ** -39
+            err = np.abs(out.double().cpu().numpy() - want)
+            assert layer.status() == 0
+            assert (err <= allowed).all(), (T, dtype, (err / allowed).max())
