@@ -42,7 +42,7 @@
 // four rows takes about 70 clocks and a block needs 32, and one warp's 16-byte cp.async copies
 // took 1.4 us a block where the loads of neighbouring rows take 0.5 us.
 #include <algorithm>
-#include <cmath>
+#include <cstddef>
 
 #include "route_dev.cuh"
 #include "scaled.cuh"
@@ -150,6 +150,13 @@ struct Shared {
     uint32_t amax[2][4][kMT];             // gate/up: by tile parity and column quarter, per token
     float patch[kEpiWarps][32][kPatch + 1];
 };
+
+// Shared follows the ring, whose stages keep the 1024-byte alignment of its start; scales are copied
+// 4 bytes at a time and the weights' read in pairs.
+static_assert(kStage % 1024 == 0 && alignof(Shared) == 8 && offsetof(Shared, full) == 0 &&
+                  offsetof(Shared, as) % 4 == 0 && offsetof(Shared, ws) % sizeof(float2) == 0 &&
+                  sizeof(float2) == 8,
+              "alignment of what the copies and vector loads touch");
 
 constexpr size_t kSmem = 1024 + (size_t)kStages * kStage + sizeof(Shared);
 static_assert(kSmem <= 232448, "shared memory");

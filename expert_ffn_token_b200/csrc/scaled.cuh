@@ -10,10 +10,17 @@ namespace moe {
 
 constexpr int kSBlk = 128;                 // columns (and weight rows) per scale
 constexpr float kE4M3Max = 448.0f;
-constexpr int kSmallT = 8;                 // most tokens of the small-batch kernels (MMA columns)
-// Most tokens of the experts' small-batch kernels.  10 of 512 experts and the shared one, hidden
-// 2560, ffn 640, all experts equally likely, small / tensor cores: 2 tokens 40 / 50 us, 3 tokens
-// 59 / 66 us, 5 tokens 79 / 73 us, 8 tokens 117 / 93 us.
+// Most rows of the product's small kernel: the columns of one MMA.  Caches cold, small kernel /
+// tensor cores: 8 rows of 1280 x 2560 weights 8.2 / 14.3 us, of 1280 x 8192 14.3 / 28.7, of
+// 8192 x 8192 24.6 / 34.8.  More rows would read the weights once per eight: 9 rows of the same
+// 10.2 / 14.3, 14.4 / 28.7 and 36.9 / 34.8 us, better for few weight rows and worse for many; that
+// form is not kept.
+constexpr int kSmallT = 8;
+// Most tokens of the experts' small-batch kernels.  Caches cold, every expert equally likely, with a
+// shared one, small / tensor cores at 2, 4, 5 and 8 tokens: 10 of 512 experts (hidden 2560, ffn 640)
+// 45 / 55, 74 / 78, 84 / 84, 121 / 107 us; 6 of 64 (2048, 512) 31 / 39, 39 / 45, 45 / 47, 53 / 53; 2 of
+// 8 (2048, 512) 25 / 33, 29 / 35, 29 / 35, 31 / 35.  What moves the crossover is the number of
+// distinct experts; a rule in tokens alone gives up to a sixth away at 5 to 8 tokens of few experts.
 constexpr int kSmallExpertsT = 4;
 
 __host__ __device__ inline int sblocks(int n) { return (n + kSBlk - 1) / kSBlk; }
@@ -89,7 +96,7 @@ static __device__ __noinline__ uint32_t quant4_wide(float4 v, float s) {
 
 // The scale amax / 448 of a largest magnitude given as an fp32 pattern, 0 when it is not finite.  A
 // product with 1 / 448, its exact remainder and one more multiply-add give the correctly rounded
-// quotient; near the subnormals, where the remainder may underflow, the division does.
+// quotient (P. Markstein's correction of a quotient by its remainder); near the subnormals, where the remainder may underflow, the division does.
 __device__ __forceinline__ float scale_of(uint32_t top) {
     const float x = __uint_as_float(top);
     constexpr float r = 1.0f / kE4M3Max;

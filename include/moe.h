@@ -382,8 +382,8 @@ moe_status moe_scaled_quantize(const void *d_x, int dtype, int T, int K, int64_t
 /* d_out [M][N] (dtype, rows ldo elements apart) = the scaled activations d_a [M][K] (rows lda
  * bytes apart, scales d_as with stride ldas >= M) times the transposed scaled weights d_b [N][K]
  * (rows ldb bytes apart, scales d_bs contiguous): every block of 128 k is summed in fp32, scaled
- * in fp32 and added up in fp32, in an order that depends on the sizes alone; one rounding to
- * dtype at the end.  d_a and d_b 16-byte aligned, lda and ldb multiples of 16 (the bytes from
+ * in fp32 (by the product of its two scales, which is accurate while it is a normal fp32 number) and
+ * added up in fp32, in an order that depends on the sizes alone; one rounding to dtype at the end.  d_a and d_b 16-byte aligned, lda and ldb multiples of 16 (the bytes from
  * column K to the next multiple of 16 may be read, in the last row too, but not used).  d_out aligned to its type.  d_status (may be NULL) receives device-side
  * errors.  The workspace (moe_scaled_matmul_workspace_size; may be 0 bytes, then d_ws may be
  * NULL) is 256-byte aligned scratch.  M may be 0 (d_a, d_as and d_out may then be NULL).  M, N and
@@ -407,7 +407,7 @@ typedef struct {
 /* a4-a7 on scaled experts, for tokens routed by moe_route_scored or moe_route_topk (d_ids, d_w,
  * d_offsets, d_inv_perm as written there for T, n_experts, k):
  *   x^ = d_x [T][hidden] as moe_scaled_quantize stores it, g = W_gate x^, u = W_up x^,
- *   h = g / (1 + exp(-g)) * u in fp32, h^ = h quantised likewise per 128 values of ffn,
+ *   h = g / (1 + exp(-g)) * u in fp32 (a few ulp), h^ = h quantised likewise per 128 values of ffn,
  *   y = W_down h^, d_out[t] = sum_j w[t][j] y[t][ids[t][j]] (+ gate[t] y[t][shared])
  * (y in fp32, or, with a bf16 output and more than 4 tokens, in fp16 times a power of two per
  * token and 32 columns, the largest of which it brings to fp16's top), with d_x and d_out [T][hidden] contiguous of x_dtype and out_dtype, 16-byte aligned, d_gate
