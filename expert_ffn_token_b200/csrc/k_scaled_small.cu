@@ -23,7 +23,8 @@
 //
 // On the device: one row times 1280 x 2560 2.8 us (3.3 MB: a launch and one trip to memory); one
 // token of 8 experts, hidden 2048, ffn 512, 8.7 us (25 MB, 2.9 TB/s); 3 tokens of 10 of 512 experts
-// and the shared one, hidden 2560, ffn 640, 48 us (124 MB): list 4.8, gate/up 23.3, down 18.3 us.
+// and the shared one, hidden 2560, ffn 640, 47 us (124 MB): list 5, gate/up 22.5, down 19 us, a third
+// of the issue slots and 2.6 TB/s: few CTAs, and the down kernel spills 156 bytes a thread.
 #include <algorithm>
 
 #include "ptx.cuh"

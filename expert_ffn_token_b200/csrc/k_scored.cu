@@ -17,9 +17,11 @@
 // memory, a second kernel turns them into places per chunk, a third writes the permutation.  Up to
 // one chunk is routed and grouped by one CTA in one launch.
 //
-// Bound by instructions (about 2300 a token at 512 experts in 8 groups), not by the logits' bytes:
-// 8192 such tokens take 43.5 us on the device, 37.5 us of it k_scored_rows alone (16.8 MB); one
-// token of 256 experts 5.0 us.
+// 8192 tokens of 512 experts in 8 groups take 45 us on the device, 38.6 us of it k_scored_rows alone
+// (16.8 MB), which is neither bound by the logits' bytes nor by instructions alone: 2418 a token are
+// 33,500 issue slots a scheduler of its 75,200 clocks.  The rest is 128 CTAs for 148 SMs, two tokens
+// a warp in turn, each a chain of dependent reductions, and at 512 experts spills (64 registers).  One
+// token of 256 experts takes 5.0 us.
 #include <math.h>
 
 #include "ptx.cuh"
