@@ -25,7 +25,7 @@
 // Now, on the device: 8192^3 486 to 504 us back to back (2.2 PFLOP/s; 907 clocks a block of k, 512 of
 // them its MMAs, with the issue slots 65 percent full, mostly of the sums' promotion), 4096 x 1280 x
 // 2560 to fp32 30 us (160 tiles: two rounds).  The experts' layer of 10 of 512 experts and the shared
-// one, hidden 2560, ffn 640: 64 tokens 303 us (5.9 TB/s of weights), 8192 tokens 913 us (to bf16).
+// one, hidden 2560, ffn 640: 64 tokens 303 us (5.9 TB/s of weights), 8192 tokens 910 to 940 us (to bf16).
 //
 // Roles (640 threads; registers move from the first four warps to the epilogue):
 //   warp 0        TMA producer: weight boxes of 128 rows x 128 bytes, token rows as boxes of 16
