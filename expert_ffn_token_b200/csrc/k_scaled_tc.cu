@@ -498,7 +498,13 @@ __device__ void finish(const TcArgs &a, Shared &S, uint8_t *ring, int tiles, uin
                     float mx = 0.f;                    // (passes over NaN, which stays NaN)
 #pragma unroll
                     for (int j = 0; j < 32; j++) mx = fmaxf(mx, fabsf(acc[u][j]));
-                    // at most 114
+                    if (mx == INFINITY && row < t.n) {     // which stays too: the others count
+                        mx = 0.f;
+#pragma unroll
+                        for (int j = 0; j < 32; j++)
+                            if (fabsf(acc[u][j]) < INFINITY) mx = fmaxf(mx, fabsf(acc[u][j]));
+                    }
+                    // at most 113
                     const int x = max((int)(__float_as_uint(mx) >> 23) - 127 - 14, -126);
                     const float inv = __uint_as_float((uint32_t)(127 - x) << 23);
                     ex |= (uint32_t)(127 + x) << (8 * u);

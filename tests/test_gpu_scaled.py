@@ -904,3 +904,40 @@ def test_experts_of_whole_layers(torch, moe, E, k, H, F, shared, sizes):
             err = np.abs(out.double().cpu().numpy() - want)
             assert layer.status() == 0
             assert (err <= allowed).all(), (T, dtype, (err / allowed).max())
+
+
+@pytest.mark.parametrize("dtype", list(EPS))
+@pytest.mark.parametrize("T", [1, 3, 6, 140])
+def test_experts_infinite_output_leaves_its_neighbours(torch, moe, T, dtype):
+    """An output column that passes fp32 (a weight scale of 2^126) or is NaN (a NaN code) is that, and its
+    neighbours are what they are without it."""
+    E, H, F = 2, 64, 256
+    rng = np.random.default_rng(T)
+    W, layer = make_layer(torch, moe, rng, E, H, F, 1, False, T)
+    codes, scales = W["down"]
+    codes[:, :, 128:] = 0
+    layer.tensors[2].copy_(_dev(torch, codes))
+    xd = _dev(torch, rng.standard_normal((T, H))).to(getattr(torch, dtype))
+    ids = (np.arange(T) % E).astype(np.int32)[:, None]
+    w = np.ones((T, 1), np.float32)
+    clean = run_experts(torch, layer, xd, ids, w, None, getattr(torch, dtype))
+    # row 5 takes the largest h of the second block, 448 of its scale, times 448 * 2^126
+    codes[:, 5, 128:], codes[:, 40, 200] = ref.encode(np.array([448.0])), 0x7F
+    scales[:, :, 1] = 2.0 ** 126
+    layer.tensors[2].copy_(_dev(torch, codes))
+    layer.tensors[5].copy_(_dev(torch, scales))
+    out = run_experts(torch, layer, xd, ids, w, None, getattr(torch, dtype))
+    others = np.ones(H, bool)
+    others[[5, 40]] = False
+    keep = torch.from_numpy(np.flatnonzero(others)).cuda()
+    assert layer.status() == 0
+    # (the sum of 128 values of either sign that row 5 takes may by chance stay within fp32; then it
+    # is a finite neighbour, 2^-39 of which the others may be off by)
+    past = ~torch.isfinite(out[:, 5])
+    assert past.double().mean() > 0.9 and torch.isnan(out[:, 40]).all()
+    assert torch.isfinite(out[:, keep]).all()
+    out, clean = out[past], clean[past]
+    # the power of two may change with the neighbours gone, and with it subnormal fp16 values alone
+    gap = (out[:, keep].double() - clean[:, keep].double()).abs()
+    assert (gap <= clean[:, keep].double().abs() * 2 * EPS[dtype] * (dtype == "bfloat16") +
+            clean.double().abs().amax() * 2.0 ** -38).all()
